@@ -89,13 +89,15 @@ enum longnet_impl {
   LONGNET_IMPL_TILES = 4,    /* backward only: bf16 or fp16, D = 64, any
                                 patterns: 64-row tiles of the sparsified
                                 segments on mma.sync tensor cores */
-  LONGNET_IMPL_PATTERNS = 5  /* forward: bf16 or fp16, D = 16, 32, 64 or 128, any number
+  LONGNET_IMPL_PATTERNS = 5, /* forward: bf16 or fp16, D = 16, 32, 64 or 128, any number
                                 of patterns, qk_norm or not, lse required with
                                 more than one:
                                 one tcgen05 launch per pattern, each merging its
                                 rows into out and lse (initialised to 0 and
                                 -inf); out is rounded to the input format
                                 between patterns */
+  LONGNET_IMPL_DECODE = 6    /* paged attention: few query rows per key/value
+                                head, the keys split over the GPU */
 };
 
 /*
@@ -412,6 +414,156 @@ int longnet_dilated_attn_bwd_ws(const void* q, const void* k, const void* v,
                                 int causal, int dtype, int flags, int impl,
                                 void* workspace, int64_t workspace_bytes,
                                 longnet_stream_t stream);
+
+/*
+ * Causal attention with a sliding window and sinks.
+ *
+ * The query at position x sees key j when j <= x and (x - j < window or
+ * j < sinks): the latest `window` keys, itself among them, and the first
+ * `sinks` keys of the sequence, which stay visible from everywhere.
+ *   out_x = sum_j P_xj v_j,  P_xj = e^{s_xj - lse_x},
+ *   s_xj = <q_x, k_j> / sqrt(D),  lse_x = log sum_j e^{s_xj} over visible j.
+ * Query head h reads key/value head h / (H / Hkv): H must be a multiple of Hkv
+ * (Hkv = H: every head has its own keys).  It stands beside the dilated
+ * patterns as the other mask whose cost grows linearly with the sequence.
+ *
+ * longnet_window_attn_fwd
+ *   - q, out: [B, N, H, D]; k, v: [B, N, Hkv, D]; contiguous, of dtype, 16-byte
+ *     aligned; lse: fp32 [B, H, N] or NULL.
+ *   - D in {16, 32, 64, 128} (else LONGNET_ERR_UNSUPPORTED); N >= 1;
+ *     window >= 1 (window >= N: plain causal attention); sinks >= 0.
+ *   - B Hkv <= 65535 and N H <= 2^30, else LONGNET_ERR_UNSUPPORTED.
+ *   - impl: LONGNET_IMPL_AUTO, LONGNET_IMPL_TCGEN05 (bf16 and fp16) or
+ *     LONGNET_IMPL_SIMT (fp32 arithmetic, every dtype).
+ *   Rows of v a query does not see may be read and multiplied by a weight of
+ *   0, so they must be finite.
+ */
+int longnet_window_attn_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
+                            int64_t B, int64_t N, int64_t H, int64_t Hkv, int64_t D,
+                            int64_t window, int64_t sinks, int dtype, int impl,
+                            longnet_stream_t stream);
+
+/*
+ * longnet_window_attn_bwd — the gradients of sum(dout * out) of the call
+ * above: with delta_x = <dout_x, out_x> and dS = P (dout V^T - delta),
+ *   dq = dS K / sqrt(D), dk = dS^T Q / sqrt(D), dv = P^T dout,
+ * dk and dv summed over the query heads that share a key/value head.
+ *   - out, lse: the forward's results; dout: [B, N, H, D] of dtype.
+ *   - dq [B, N, H, D], dk and dv [B, N, Hkv, D]: of dtype, written in full,
+ *     summed in fp32 and rounded once.  They must not alias the inputs.
+ *   - workspace: device memory of the caller, 256-byte aligned, at least
+ *     longnet_window_bwd_workspace_bytes bytes, overlapping no tensor; its
+ *     contents on entry do not matter.  Calls that may run at the same time
+ *     need one each.
+ *   The same inputs give the same bits: no sum depends on an order that may
+ *   change.  Other arguments and errors as the forward.
+ */
+int64_t longnet_window_bwd_workspace_bytes(int64_t B, int64_t N, int64_t H, int64_t Hkv, int64_t D,
+                                           int64_t window, int64_t sinks, int dtype);
+int longnet_window_attn_bwd(const void* q, const void* k, const void* v,
+                            const void* out, const float* lse, const void* dout,
+                            void* dq, void* dk, void* dv,
+                            int64_t B, int64_t N, int64_t H, int64_t Hkv, int64_t D,
+                            int64_t window, int64_t sinks, int dtype, int impl,
+                            void* workspace, int64_t workspace_bytes, longnet_stream_t stream);
+
+/*
+ * A paged key/value cache, for generation.
+ *
+ * k_pages, v_pages: [n_pages, page, Hkv, D] of dtype, 16-byte aligned; a page
+ * holds `page` consecutive keys of one sequence, page a power of two from 8 to
+ * 256 (else LONGNET_ERR_UNSUPPORTED).  For S sequences, in DEVICE memory,
+ * int32, 4-byte aligned:
+ *   - table [S, max_pages]: key j of sequence s lies in page
+ *     table[s][j / page], slot j mod page.  Entries past a sequence's keys
+ *     are not read and may hold anything.
+ *   - kv_len [S]: keys of each sequence, the new tokens' among them;
+ *     0 <= kv_len <= max_pages * page.
+ *   - cu_q [S + 1]: the new tokens of sequence s are the token rows
+ *     [cu_q[s], cu_q[s + 1]), at positions kv_len[s] - (cu_q[s + 1] - cu_q[s])
+ *     and on.  Ascending, from 0 or more to at most T.  Equal neighbours: a
+ *     sequence with no new token.  Token rows of no sequence are not touched.
+ * Slots past a sequence's keys may hold anything, NaN included.  A length or
+ * page number out of range records LONGNET_ERR_DEVICE_BOUNDS in the status
+ * word; what it belongs to is skipped or taken as zeros, nothing outside the
+ * buffers is accessed, and the other sequences are not affected.
+ * Limits: S Hkv <= 65535; max_pages * page, T and max_q H <= 2^30; else
+ * LONGNET_ERR_UNSUPPORTED.
+ *
+ * longnet_paged_append — writes the new tokens' keys and values, k_tok and
+ * v_tok [T, Hkv, D], to their slots.  weights (may be NULL): fp32
+ * [S, Hkv, max_pages * page], set to 0 there.  T = 0 does nothing.
+ */
+int longnet_paged_append(const void* k_tok, const void* v_tok, void* k_pages, void* v_pages, float* weights,
+                         const int32_t* cu_q, const int32_t* kv_len, const int32_t* table,
+                         int64_t T, int64_t S, int64_t Hkv, int64_t D,
+                         int64_t n_pages, int64_t page, int64_t max_pages,
+                         int dtype, longnet_stream_t stream);
+
+/*
+ * longnet_paged_attn_fwd — the new tokens attend to their sequences' cached
+ * keys (longnet_paged_append puts their own there first): chunks of a prompt,
+ * single tokens, or a batch of both.  The mask is that of
+ * longnet_window_attn_fwd; window = 0: every earlier key.
+ *   - q, out: [T, H, D] of dtype; lse: fp32 [T, H] or NULL.  A token at a
+ *     negative position (kv_len below its sequence's new tokens) sees
+ *     nothing: out 0, lse -inf.
+ *   - max_q: no sequence has more new tokens (it sizes the launch, so one
+ *     captured launch serves every batch within it).  A sequence with more:
+ *     LONGNET_ERR_DEVICE_BOUNDS, and it is skipped.
+ *   - weights: NULL, or fp32 [S, Hkv, max_pages * page] to which each key's
+ *     received weight is added: weights[s, f, j] += sum of P_xj over the new
+ *     tokens x of sequence s and the query heads of key/value head f.
+ *     Needs lse.
+ *   - impl: LONGNET_IMPL_AUTO, LONGNET_IMPL_DECODE (bf16 and fp16, at most 64
+ *     query rows, max_q H / Hkv, per key/value head), LONGNET_IMPL_TCGEN05
+ *     (bf16 and fp16, H / Hkv <= 128) or LONGNET_IMPL_SIMT (fp32 arithmetic,
+ *     every dtype).
+ *   - workspace: device memory of the caller, 256-byte aligned, at least
+ *     longnet_paged_workspace_bytes bytes (weights: 1 when they are asked
+ *     for), overlapping no tensor; contents on entry do not matter; NULL when
+ *     0 bytes are needed.  Calls that may run at the same time need one each.
+ *   The same inputs give the same bits.
+ */
+int64_t longnet_paged_workspace_bytes(int64_t S, int64_t max_q, int64_t H, int64_t Hkv, int64_t D,
+                                      int64_t page, int64_t max_pages, int64_t window, int64_t sinks,
+                                      int dtype, int weights);
+int longnet_paged_attn_fwd(const void* q, const void* k_pages, const void* v_pages, void* out, float* lse,
+                           float* weights, const int32_t* cu_q, const int32_t* kv_len, const int32_t* table,
+                           int64_t T, int64_t S, int64_t max_q, int64_t H, int64_t Hkv, int64_t D,
+                           int64_t n_pages, int64_t page, int64_t max_pages,
+                           int64_t window, int64_t sinks, int dtype, int impl,
+                           void* workspace, int64_t workspace_bytes, longnet_stream_t stream);
+
+/*
+ * longnet_cache_evict — cuts every sequence's cache down to at most `budget`
+ * keys.  A sequence of more keys keeps, for each key/value head on its own,
+ * the first `sinks`, the last `recent`, and of the others those with the
+ * largest accumulated weights (longnet_paged_attn_fwd's; ties: the earlier key;
+ * NaN counts as less than every number).  A sequence of at most `budget` keys
+ * keeps all.  Kept keys stay in order and move to new pages: the old ones are
+ * only read, so pages shared with other sequences are safe.
+ *   - weights [S, Hkv, max_pages * page], kv_len, table, k_pages, v_pages: the
+ *     cache as above.
+ *   - k_out, v_out: pools [n_out_pages, page, Hkv, D]; they may be k_pages and
+ *     v_pages themselves, when no page of new_table is one that a sequence of
+ *     the call still holds.  new_table [S, max_out_pages]: the new pages, read
+ *     for the kept keys only, no page twice; budget <= max_out_pages * page.
+ *   - written: new_weights [S, Hkv, max_out_pages * page] (the kept keys'
+ *     weights, then zeros), new_len [S], kept [S, Hkv, budget] (the old
+ *     indices, ascending, then -1) and the kept keys' slots of k_out, v_out.
+ *     None of new_weights, new_len and kept may overlap an input.
+ *   - budget >= 1, sinks + recent <= budget, else LONGNET_ERR_INVALID_ARG.
+ *   After it a key's index is no longer its position: attend to the new cache
+ *   with window = 0.
+ */
+int longnet_cache_evict(const void* k_pages, const void* v_pages, const float* weights,
+                        const int32_t* kv_len, const int32_t* table,
+                        void* k_out, void* v_out, float* new_weights, int32_t* new_len, int32_t* kept,
+                        const int32_t* new_table,
+                        int64_t S, int64_t Hkv, int64_t D, int64_t n_pages, int64_t page, int64_t max_pages,
+                        int64_t n_out_pages, int64_t max_out_pages,
+                        int64_t budget, int64_t sinks, int64_t recent, int dtype, longnet_stream_t stream);
 
 /*
  * longnet_select_impl — which family AUTO would run for these arguments

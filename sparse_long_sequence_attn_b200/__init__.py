@@ -8,6 +8,7 @@ forward (seqpar).
 """
 from .binding import (  # noqa: F401
     LONGNET_IMPL_AUTO,
+    LONGNET_IMPL_DECODE,
     LONGNET_IMPL_PATTERNS,
     LONGNET_IMPL_SIMT,
     LONGNET_IMPL_SMALLSEG,
@@ -15,6 +16,8 @@ from .binding import (  # noqa: F401
     LONGNET_IMPL_TILES,
     DilatedAttnFunction,
     LongNetError,
+    WindowAttnFunction,
+    cache_evict,
     dilated_attention,
     dilated_attn,
     dilated_attn_bwd,
@@ -29,9 +32,19 @@ from .binding import (  # noqa: F401
     longnet_fwd_workspace_bytes,
     longnet_gather_rows,
     longnet_last_device_status,
+    longnet_paged_workspace_bytes,
     longnet_scatter_rows,
     longnet_select_impl,
     longnet_watchdog_selftest,
+    longnet_window_attn_bwd,
+    longnet_window_attn_fwd,
+    longnet_window_bwd_workspace_bytes,
+    paged_append,
+    paged_attn,
+    paged_workspace,
     status_string,
     version,
+    window_attention,
+    window_attn,
+    window_attn_bwd,
 )

@@ -39,6 +39,7 @@ LONGNET_IMPL_TCGEN05 = 2
 LONGNET_IMPL_SMALLSEG = 3
 LONGNET_IMPL_TILES = 4
 LONGNET_IMPL_PATTERNS = 5
+LONGNET_IMPL_DECODE = 6
 
 # Every symbol include/longnet.h declares, with its ctypes signature.
 _i64 = ctypes.c_int64
@@ -82,6 +83,15 @@ SIGNATURES = {
                                                    _i64, _i64, _i64, _i64, ctypes.c_int, _i64p,
                                                    _i64p, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                                    ctypes.c_int, _vp, _i64, _vp]),
+    "longnet_window_attn_fwd": (ctypes.c_int, [_vp] * 5 + [_i64] * 7 + [ctypes.c_int, ctypes.c_int, _vp]),
+    "longnet_window_bwd_workspace_bytes": (ctypes.c_int64, [_i64] * 7 + [ctypes.c_int]),
+    "longnet_window_attn_bwd": (ctypes.c_int, [_vp] * 9 + [_i64] * 7 + [ctypes.c_int, ctypes.c_int, _vp, _i64,
+                                                                        _vp]),
+    "longnet_paged_append": (ctypes.c_int, [_vp] * 8 + [_i64] * 7 + [ctypes.c_int, _vp]),
+    "longnet_paged_workspace_bytes": (ctypes.c_int64, [_i64] * 9 + [ctypes.c_int, ctypes.c_int]),
+    "longnet_paged_attn_fwd": (ctypes.c_int, [_vp] * 9 + [_i64] * 11 + [ctypes.c_int, ctypes.c_int, _vp, _i64,
+                                                                        _vp]),
+    "longnet_cache_evict": (ctypes.c_int, [_vp] * 11 + [_i64] * 11 + [ctypes.c_int, _vp]),
     "longnet_select_impl": (ctypes.c_int, [_i64, _i64, _i64, _i64, ctypes.c_int, _i64p, _i64p,
                                            ctypes.c_int, ctypes.c_int]),
     "longnet_last_device_status": (ctypes.c_int, [_vp]),
@@ -139,6 +149,10 @@ def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.float16:
         return LONGNET_DTYPE_F16
     raise TypeError(f"unsupported dtype {t.dtype}")
+
+
+_DTYPE_CODES = {torch.float32: LONGNET_DTYPE_F32, torch.bfloat16: LONGNET_DTYPE_BF16,
+                torch.float16: LONGNET_DTYPE_F16}
 
 
 def _stream_handle(stream) -> int | None:
@@ -481,6 +495,267 @@ class DilatedAttnFunction(torch.autograd.Function):
 def dilated_attention(q, k, v, patterns, causal: bool = True, qk_norm: bool = False, xpos: bool = False):
     """Differentiable forward: out [B, N, H, D], gradients through the backward."""
     return DilatedAttnFunction.apply(q, k, v, patterns, causal, qk_norm, xpos)
+
+
+def _on_device(t: torch.Tensor, stream):
+    """t's device made current, and the stream's handle (default: torch's current stream there)."""
+    return torch.cuda.device(t.device), _stream_handle(torch.cuda.current_stream(t.device) if stream is None
+                                                       else stream)
+
+
+def _check(what: str, t: torch.Tensor, shape, dtype, like: torch.Tensor) -> None:
+    """One tensor argument: CUDA, on `like`'s device, contiguous, of this shape and dtype."""
+    if not (t.is_cuda and t.device == like.device and t.is_contiguous() and t.dtype == dtype
+            and tuple(t.shape) == tuple(shape)):
+        raise ValueError(f"{what} must be a contiguous {dtype} CUDA tensor {tuple(shape)} on {like.device}, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def longnet_window_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                            lse: torch.Tensor | None, window: int, sinks: int = 0,
+                            impl: int = LONGNET_IMPL_AUTO, stream=None) -> None:
+    """Enqueue causal attention with a sliding window and sinks: the query at
+    position x sees key j when j <= x and (x - j < window or j < sinks).
+
+    q, out: contiguous CUDA [B, N, H, D]; k, v: [B, N, Hkv, D], Hkv dividing H;
+    one dtype (fp32/bf16/fp16); lse: contiguous fp32 [B, H, N] or None.  Raises
+    LongNetError on a non-zero status."""
+    B, N, H, D = q.shape
+    _check("q", q, (B, N, H, D), q.dtype, q)
+    _check("k", k, (B, N, k.shape[2], D), q.dtype, q)
+    _check("v", v, k.shape, q.dtype, q)
+    _check("out", out, q.shape, q.dtype, q)
+    if lse is not None:
+        _check("lse", lse, (B, H, N), torch.float32, q)
+    dev, handle = _on_device(q, stream)
+    with dev:
+        rc = load_library().longnet_window_attn_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+            B, N, H, k.shape[2], D, int(window), int(sinks), _dtype_code(q), int(impl), handle)
+    if rc != LONGNET_OK:
+        raise LongNetError(rc, "longnet_window_attn_fwd")
+
+
+def longnet_window_bwd_workspace_bytes(B: int, N: int, H: int, Hkv: int, D: int, window: int, sinks: int,
+                                       dtype: torch.dtype) -> int:
+    """Device workspace bytes longnet_window_attn_bwd needs."""
+    n = load_library().longnet_window_bwd_workspace_bytes(B, N, H, Hkv, D, int(window), int(sinks),
+                                                          _DTYPE_CODES[dtype])
+    if n < 0:
+        raise LongNetError(n, "longnet_window_bwd_workspace_bytes")
+    return int(n)
+
+
+def longnet_window_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                            lse: torch.Tensor, dout: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor,
+                            dv: torch.Tensor, window: int, sinks: int, workspace: torch.Tensor,
+                            impl: int = LONGNET_IMPL_AUTO, stream=None) -> None:
+    """Enqueue the backward of longnet_window_attn_fwd: dq, dk, dv (of q's
+    dtype) receive the gradients of sum(dout * out); out and lse are the
+    forward's.  workspace: a CUDA tensor of at least
+    longnet_window_bwd_workspace_bytes bytes, 256-byte aligned.  Raises
+    LongNetError on a non-zero status."""
+    B, N, H, D = q.shape
+    _check("q", q, (B, N, H, D), q.dtype, q)
+    _check("k", k, (B, N, k.shape[2], D), q.dtype, q)
+    _check("v", v, k.shape, q.dtype, q)
+    for name, t in (("out", out), ("dout", dout), ("dq", dq)):
+        _check(name, t, q.shape, q.dtype, q)
+    for name, t in (("dk", dk), ("dv", dv)):
+        _check(name, t, k.shape, q.dtype, q)
+    _check("lse", lse, (B, H, N), torch.float32, q)
+    _check("workspace", workspace, workspace.shape, workspace.dtype, q)
+    dev, handle = _on_device(q, stream)
+    with dev:
+        rc = load_library().longnet_window_attn_bwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, N, H, k.shape[2], D, int(window), int(sinks),
+            _dtype_code(q), int(impl), workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
+    if rc != LONGNET_OK:
+        raise LongNetError(rc, "longnet_window_attn_bwd")
+
+
+def window_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, sinks: int = 0,
+                impl: int = LONGNET_IMPL_AUTO, want_lse: bool = True, stream=None):
+    """Allocate out (and lse) with torch and run longnet_window_attn_fwd.
+    Returns (out, lse)."""
+    B, N, H, _ = q.shape
+    out = torch.empty_like(q)
+    lse = torch.empty((B, H, N), device=q.device, dtype=torch.float32) if want_lse else None
+    longnet_window_attn_fwd(q, k, v, out, lse, window, sinks, impl, stream)
+    return out, lse
+
+
+def window_attn_bwd(q, k, v, out, lse, dout, window: int, sinks: int = 0, impl: int = LONGNET_IMPL_AUTO,
+                    stream=None):
+    """Allocate dq, dk, dv (and the workspace) with torch and run the backward
+    matching window_attn.  Returns (dq, dk, dv)."""
+    B, N, H, D = q.shape
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ws = torch.empty(longnet_window_bwd_workspace_bytes(B, N, H, k.shape[2], D, window, sinks, q.dtype),
+                     dtype=torch.uint8, device=q.device)
+    longnet_window_attn_bwd(q, k, v, out, lse, dout.contiguous(), dq, dk, dv, window, sinks, ws, impl, stream)
+    return dq, dk, dv
+
+
+class WindowAttnFunction(torch.autograd.Function):
+    """window_attn and window_attn_bwd as one torch autograd op."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, window, sinks):
+        out, lse = window_attn(q, k, v, window, sinks)
+        ctx.save_for_backward(q, k, v, out, lse)
+        ctx.window, ctx.sinks = window, sinks
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        q, k, v, out, lse = ctx.saved_tensors
+        dq, dk, dv = window_attn_bwd(q, k, v, out, lse, dout.to(q.dtype), ctx.window, ctx.sinks)
+        return dq, dk, dv, None, None
+
+
+def window_attention(q, k, v, window: int, sinks: int = 0):
+    """Differentiable attention with a sliding window and sinks: out
+    [B, N, H, D], gradients through the backward."""
+    return WindowAttnFunction.apply(q.contiguous(), k.contiguous(), v.contiguous(), int(window), int(sinks))
+
+
+def _cache_sizes(k_pages: torch.Tensor, table: torch.Tensor):
+    if k_pages.dim() != 4 or table.dim() != 2:
+        raise ValueError("k_pages must be [n_pages, page, Hkv, D] and table [S, max_pages]")
+    n_pages, page, Hkv, D = k_pages.shape
+    S, max_pages = table.shape
+    return n_pages, page, Hkv, D, S, max_pages
+
+
+def paged_append(k_tok: torch.Tensor, v_tok: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                 cu_q: torch.Tensor, kv_len: torch.Tensor, table: torch.Tensor,
+                 weights: torch.Tensor | None = None, stream=None) -> None:
+    """Write the new tokens' keys and values (k_tok, v_tok [T, Hkv, D]) to
+    their slots of the paged cache (k_pages, v_pages [n_pages, page, Hkv, D];
+    table int32 [S, max_pages]; kv_len int32 [S], the new tokens counted;
+    cu_q int32 [S + 1]).  weights (fp32 [S, Hkv, max_pages * page]) is set to 0
+    there.  Lengths and page numbers are checked on the device (status word).
+    Raises LongNetError on a non-zero status."""
+    n_pages, page, Hkv, D, S, max_pages = _cache_sizes(k_pages, table)
+    T = k_tok.shape[0]
+    _check("k_pages", k_pages, k_pages.shape, k_tok.dtype, k_tok)
+    _check("v_pages", v_pages, k_pages.shape, k_tok.dtype, k_tok)
+    _check("k_tok", k_tok, (T, Hkv, D), k_tok.dtype, k_tok)
+    _check("v_tok", v_tok, (T, Hkv, D), k_tok.dtype, k_tok)
+    _check("cu_q", cu_q, (S + 1,), torch.int32, k_tok)
+    _check("kv_len", kv_len, (S,), torch.int32, k_tok)
+    _check("table", table, (S, max_pages), torch.int32, k_tok)
+    if weights is not None:
+        _check("weights", weights, (S, Hkv, max_pages * page), torch.float32, k_tok)
+    dev, handle = _on_device(k_tok, stream)
+    with dev:
+        rc = load_library().longnet_paged_append(
+            k_tok.data_ptr(), v_tok.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+            None if weights is None else weights.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), table.data_ptr(),
+            T, S, Hkv, D, n_pages, page, max_pages, _dtype_code(k_tok), handle)
+    if rc != LONGNET_OK:
+        raise LongNetError(rc, "longnet_paged_append")
+
+
+def longnet_paged_workspace_bytes(S: int, max_q: int, H: int, Hkv: int, D: int, page: int, max_pages: int,
+                                  window: int, sinks: int, dtype: torch.dtype, weights: bool = False) -> int:
+    """Device workspace bytes longnet_paged_attn_fwd needs."""
+    n = load_library().longnet_paged_workspace_bytes(S, int(max_q), H, Hkv, D, page, max_pages, int(window),
+                                                     int(sinks), _DTYPE_CODES[dtype], int(bool(weights)))
+    if n < 0:
+        raise LongNetError(n, "longnet_paged_workspace_bytes")
+    return int(n)
+
+
+def paged_workspace(q: torch.Tensor, k_pages: torch.Tensor, table: torch.Tensor, max_q: int, window: int = 0,
+                    sinks: int = 0, weights: bool = False) -> torch.Tensor:
+    """A workspace for paged_attn with these arguments, for a program that
+    keeps one (a call without one allocates it with torch)."""
+    n_pages, page, Hkv, D, S, max_pages = _cache_sizes(k_pages, table)
+    n = longnet_paged_workspace_bytes(S, max_q, q.shape[1], Hkv, D, page, max_pages, window, sinks, q.dtype, weights)
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, cu_q: torch.Tensor,
+               kv_len: torch.Tensor, table: torch.Tensor, max_q: int, window: int = 0, sinks: int = 0,
+               weights: torch.Tensor | None = None, out: torch.Tensor | None = None,
+               lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+               impl: int = LONGNET_IMPL_AUTO, stream=None):
+    """The new tokens (q [T, H, D], packed by cu_q, at most max_q per sequence)
+    attend to the paged cache (see paged_append, which puts their own keys
+    there first): causal, window = 0 for every earlier key, else the latest
+    `window` and the first `sinks`.  weights (fp32 [S, Hkv, max_pages * page])
+    has the attention weight each key received added to it.  out, lse
+    (fp32 [T, H]) and workspace are allocated with torch when not given; rows
+    of no sequence are left as they were.  Returns (out, lse).  Raises
+    LongNetError on a non-zero status."""
+    n_pages, page, Hkv, D, S, max_pages = _cache_sizes(k_pages, table)
+    T, H = q.shape[0], q.shape[1]
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if lse is None else lse
+    _check("q", q, (T, H, D), q.dtype, q)
+    _check("k_pages", k_pages, k_pages.shape, q.dtype, q)
+    _check("v_pages", v_pages, k_pages.shape, q.dtype, q)
+    _check("out", out, q.shape, q.dtype, q)
+    _check("lse", lse, (T, H), torch.float32, q)
+    _check("cu_q", cu_q, (S + 1,), torch.int32, q)
+    _check("kv_len", kv_len, (S,), torch.int32, q)
+    _check("table", table, (S, max_pages), torch.int32, q)
+    if weights is not None:
+        _check("weights", weights, (S, Hkv, max_pages * page), torch.float32, q)
+    if workspace is None:
+        workspace = paged_workspace(q, k_pages, table, max_q, window, sinks, weights is not None)
+    _check("workspace", workspace, workspace.shape, workspace.dtype, q)
+    dev, handle = _on_device(q, stream)
+    with dev:
+        rc = load_library().longnet_paged_attn_fwd(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(),
+            None if weights is None else weights.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), table.data_ptr(),
+            T, S, int(max_q), H, Hkv, D, n_pages, page, max_pages, int(window), int(sinks), _dtype_code(q),
+            int(impl), workspace.data_ptr() or None, workspace.numel() * workspace.element_size(), handle)
+    if rc != LONGNET_OK:
+        raise LongNetError(rc, "longnet_paged_attn_fwd")
+    return out, lse
+
+
+def cache_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, weights: torch.Tensor, kv_len: torch.Tensor,
+                table: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor, new_table: torch.Tensor, budget: int,
+                sinks: int = 0, recent: int = 0, stream=None):
+    """Cut each sequence's cache to at most `budget` keys: per key/value head
+    the first `sinks`, the last `recent`, and of the others those with the
+    largest weights (ties: the earlier key), in order, copied to the pages of
+    new_table (int32 [S, max_out_pages]) in k_out, v_out (pools
+    [n_out_pages, page, Hkv, D]; they may be k_pages, v_pages with pages no
+    sequence of the call holds).  Returns (kept int32 [S, Hkv, budget], the
+    old indices then -1; new_len int32 [S]; new_weights fp32
+    [S, Hkv, max_out_pages * page]).  Raises LongNetError on a non-zero
+    status."""
+    n_pages, page, Hkv, D, S, max_pages = _cache_sizes(k_pages, table)
+    n_out, _, _, _, _, max_out = _cache_sizes(k_out, new_table)
+    _check("k_pages", k_pages, k_pages.shape, k_pages.dtype, k_pages)
+    _check("v_pages", v_pages, k_pages.shape, k_pages.dtype, k_pages)
+    _check("k_out", k_out, (n_out, page, Hkv, D), k_pages.dtype, k_pages)
+    _check("v_out", v_out, (n_out, page, Hkv, D), k_pages.dtype, k_pages)
+    _check("weights", weights, (S, Hkv, max_pages * page), torch.float32, k_pages)
+    _check("kv_len", kv_len, (S,), torch.int32, k_pages)
+    _check("table", table, (S, max_pages), torch.int32, k_pages)
+    _check("new_table", new_table, (S, max_out), torch.int32, k_pages)
+    kept = torch.empty((S, Hkv, max(int(budget), 0)), dtype=torch.int32, device=k_pages.device)
+    new_len = torch.empty((S,), dtype=torch.int32, device=k_pages.device)
+    new_weights = torch.empty((S, Hkv, max_out * page), dtype=torch.float32, device=k_pages.device)
+    dev, handle = _on_device(k_pages, stream)
+    with dev:
+        rc = load_library().longnet_cache_evict(
+            k_pages.data_ptr(), v_pages.data_ptr(), weights.data_ptr(), kv_len.data_ptr(), table.data_ptr(),
+            k_out.data_ptr(), v_out.data_ptr(), new_weights.data_ptr(), new_len.data_ptr(), kept.data_ptr(),
+            new_table.data_ptr(), S, Hkv, D, n_pages, page, max_pages, n_out, max_out, int(budget), int(sinks),
+            int(recent), _dtype_code(k_pages), handle)
+    if rc != LONGNET_OK:
+        raise LongNetError(rc, "longnet_cache_evict")
+    return kept, new_len, new_weights
 
 
 def longnet_select_impl(B: int, N: int, H: int, D: int, patterns, causal: bool, dtype) -> int:

@@ -61,6 +61,11 @@ int current_device_state(int* dev_out, int** status_out) {
   return LONGNET_OK;
 }
 
+}  // namespace
+
+int device_state(int* dev, int** status) { return current_device_state(dev, status); }
+
+namespace {
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Argument checks common to every family; fills the problem block.

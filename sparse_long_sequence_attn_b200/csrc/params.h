@@ -47,6 +47,10 @@ constexpr int kStatusBounds = LONGNET_ERR_DEVICE_BOUNDS;
 // Wait limit of every bounded device-side wait in the library.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
+// The current device's number and the device address of its status word;
+// LONGNET_ERR_NO_DEVICE when it is no sm_100 device.
+int device_state(int* dev, int** status);
+
 // Kernel launchers (one per family).  Return a longnet_status.
 int launch_simt(const Problem& p, cudaStream_t stream);
 int launch_tcgen05(const Problem& p, cudaStream_t stream);

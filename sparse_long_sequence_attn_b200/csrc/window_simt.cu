@@ -1,0 +1,614 @@
+// The sliding-window and paged-cache attention on the CUDA cores: forward,
+// weight sums and backward in fp32 arithmetic for every dtype, D = 16, 32, 64
+// or 128.  AUTO takes it for fp32; the 16-bit formats run on the tensor-core
+// families and are checked against it.
+//
+// Mathematics.  Forward: softmax(Q K^T / sqrt(D)) V over the visible keys, one
+// pass with the running maximum and sum of each row.  Weight sums: per key,
+// the sum over its queries of P = e^{s - lse}.  Backward, with
+// delta = <dout, out>: P = e^{s - lse}, dS = P (dout V^T - delta),
+// dQ = dS K / sqrt(D), dK = dS^T Q / sqrt(D), dV = P^T dout.
+//
+// Layout.  A CTA of 16 x 16 threads owns 64 rows (packed query rows, or keys)
+// and streams 64-row blocks of the other side through shared memory as fp32;
+// a thread holds a 4 x 4 piece of the 64 x 64 scores and a 4 x D/16 piece of
+// the accumulators, so every value read from shared memory feeds four
+// multiply-adds.  Rows are padded by four floats, which keeps the 16-byte
+// reads of 8 lanes in different banks.  The bound is the fp32 pipe (no TF32:
+// fp32 inputs keep fp32 products).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "attn_args.cuh"
+
+namespace longnet {
+namespace ws {
+
+constexpr int kT = 64;        // rows of a tile, keys of a block
+constexpr int kThreads = 256;
+constexpr int kPS = kT + 4;   // row stride of a score tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
+
+template <int D>
+struct L {
+  static constexpr int kStride = D + 4;
+  static constexpr int kTile = kT * kStride;  // floats
+  static constexpr int kC = D / 16;           // accumulator columns of a thread
+  static constexpr int kV = kC < 4 ? kC : 4;  // consecutive ones
+  __device__ static int col(int tx, int c) { return (c / kV) * (16 * kV) + tx * kV + c % kV; }
+};
+
+template <typename T>
+__device__ __forceinline__ float to_f(T x);
+template <>
+__device__ __forceinline__ float to_f(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <>
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
+
+// 64 rows of D elements into shared memory as fp32; off(r) is the row's
+// element offset, negative for a row of zeros.
+template <typename T, int D, typename Off>
+__device__ __forceinline__ void load_rows(float* dst, const T* src, Off off) {
+  constexpr int kVec = 16 / sizeof(T);  // elements of a 16-byte load
+  constexpr int kChunks = D / kVec;
+  for (int e = threadIdx.x; e < kT * kChunks; e += kThreads) {
+    const int r = e / kChunks, c = (e % kChunks) * kVec;
+    const int64_t o = off(r);
+    T x[kVec];
+    *reinterpret_cast<uint4*>(x) = o < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src + o + c);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) dst[r * L<D>::kStride + c + i] = to_f<T>(x[i]);
+  }
+}
+
+// acc[r][c] = <A row 4 ty + r, B row tx + 16 c>
+template <int D>
+__device__ __forceinline__ void dots(const float* A, const float* B, int ty, int tx, float (&acc)[4][4]) {
+  constexpr int ST = L<D>::kStride;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
+#pragma unroll 4
+  for (int d = 0; d < D; d += 4) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      x[r] = *reinterpret_cast<const float4*>(A + (4 * ty + r) * ST + d);
+      y[r] = *reinterpret_cast<const float4*>(B + (tx + 16 * r) * ST + d);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        acc[r][c] = fmaf(x[r].x, y[c].x, acc[r][c]);
+        acc[r][c] = fmaf(x[r].y, y[c].y, acc[r][c]);
+        acc[r][c] = fmaf(x[r].z, y[c].z, acc[r][c]);
+        acc[r][c] = fmaf(x[r].w, y[c].w, acc[r][c]);
+      }
+  }
+}
+
+// acc[r][c] += sum_j P[4 ty + r][j] X[j][col c]
+template <int D>
+__device__ __forceinline__ void accumulate(const float* P, const float* X, int ty, int tx,
+                                           float (&acc)[4][L<D>::kC]) {
+  constexpr int ST = L<D>::kStride, C = L<D>::kC, V = L<D>::kV;
+#pragma unroll 2
+  for (int j = 0; j < kT; j += 4) {
+    float p[4][4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float4 t = *reinterpret_cast<const float4*>(P + (4 * ty + r) * kPS + j);
+      p[r][0] = t.x;
+      p[r][1] = t.y;
+      p[r][2] = t.z;
+      p[r][3] = t.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c0 = 0; c0 < C; c0 += V) {
+        float x[V];
+        const float* src = X + (j + i) * ST + L<D>::col(tx, c0);
+        if constexpr (V == 4) {
+          const float4 t = *reinterpret_cast<const float4*>(src);
+          x[0] = t.x;
+          x[1] = t.y;
+          x[2] = t.z;
+          x[3] = t.w;
+        } else {
+#pragma unroll
+          for (int u = 0; u < V; ++u) x[u] = src[u];
+        }
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[r][c0 + u] = fmaf(p[r][i], x[u], acc[r][c0 + u]);
+      }
+  }
+}
+
+__device__ __forceinline__ float sum16(float x) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ float max16(float x) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+// A tile of packed query rows of (sequence s, key/value head f).
+struct Rows {
+  Seq q;
+  int s, f, G, r0, n;  // first packed row, rows in the tile
+  __device__ int token(int r) const { return (r0 + r) / G; }
+  __device__ int head(int r) const { return f * G + (r0 + r) % G; }
+  __device__ int pos(int r) const { return q.first + token(r); }
+  __device__ int64_t elem(int r, int H, int D) const { return ((q.q0 + token(r)) * H + head(r)) * (int64_t)D; }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  float* sQ = sm;
+  float* sKV = sm + L<D>::kTile;
+  float* sP = sm + 2 * L<D>::kTile;
+  Rows R;
+  R.s = blockIdx.y / a.Hkv;
+  R.f = blockIdx.y % a.Hkv;
+  R.q = seq_of(a, R.s);
+  R.G = a.G;
+  R.r0 = (gridDim.x - 1 - blockIdx.x) * kT;  // the longest rows first
+  R.n = R.q.nq * a.G - R.r0;
+  if (R.n <= 0) return;
+  if (R.n > kT) R.n = kT;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  load_rows<T, D>(sQ, static_cast<const T*>(a.q), [&](int r) { return r < R.n ? R.elem(r, a.H, D) : -1; });
+  float acc[4][L<D>::kC] = {}, m[4], l[4];
+  int x[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+    x[r] = 4 * ty + r < R.n ? R.pos(4 * ty + r) : -1;
+  }
+  const BlockList bl = blocks_of<kT>(a, R.pos(0), R.pos(R.n - 1));
+  for (int n = 0; n < bl.count; ++n) {
+    const int j0 = bl.at(n) * kT;
+    auto row = [&](int r) -> int64_t { return j0 + r < R.q.kv ? kv_row(a, R.q, R.s, R.f, j0 + r) : -1; };
+    __syncthreads();
+    load_rows<T, D>(sKV, static_cast<const T*>(a.k), row);
+    __syncthreads();
+    float s[4][4];
+    dots<D>(sQ, sKV, ty, tx, s);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        s[r][c] = sees(a, x[r], j0 + tx + 16 * c) ? s[r][c] * a.scale_log2 : -INFINITY;
+        mx = fmaxf(mx, s[r][c]);
+      }
+      mx = fmaxf(max16(mx), m[r]);
+      const float base = mx == -INFINITY ? 0.f : mx;  // a row with nothing to see so far
+      const float corr = exp2f(m[r] - base);
+      m[r] = mx;
+      float sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float p = exp2f(s[r][c] - base);
+        sum += p;
+        sP[(4 * ty + r) * kPS + tx + 16 * c] = p;
+      }
+      l[r] = l[r] * corr + sum16(sum);
+#pragma unroll
+      for (int c = 0; c < L<D>::kC; ++c) acc[r][c] *= corr;
+    }
+    __syncthreads();
+    load_rows<T, D>(sKV, static_cast<const T*>(a.v), row);
+    __syncthreads();
+    accumulate<D>(sP, sKV, ty, tx, acc);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int i = 4 * ty + r;
+    if (i >= R.n) continue;
+    const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
+    T* o = static_cast<T*>(a.out) + R.elem(i, a.H, D);
+#pragma unroll
+    for (int c = 0; c < L<D>::kC; ++c) o[L<D>::col(tx, c)] = from_f<T>(acc[r][c] * inv);
+    if (tx == 0 && a.lse)
+      a.lse[lse_index(a, R.q, R.s, R.token(i), R.head(i))] = l[r] > 0.f ? (m[r] + log2f(l[r])) * kLn2 : -INFINITY;
+  }
+}
+
+// weights[s, f, j] += sum over the rows that see key j of e^{s - lse}.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) weights_kernel(const AttnArgs a, float* weights) {
+  extern __shared__ __align__(16) float sm[];
+  float* sK = sm;
+  float* sQ = sm + L<D>::kTile;
+  __shared__ float s_lse[kT];
+  __shared__ int s_pos[kT];
+  const int s = blockIdx.y / a.Hkv, f = blockIdx.y % a.Hkv;
+  const Seq q = seq_of(a, s);
+  const int j0 = blockIdx.x * kT;
+  if (j0 >= q.kv || q.nq == 0) return;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  load_rows<T, D>(sK, static_cast<const T*>(a.k),
+                  [&](int r) -> int64_t { return j0 + r < q.kv ? kv_row(a, q, s, f, j0 + r) : -1; });
+  float acc[4] = {};
+  // rows from the first query at or after the tile on
+  int i0 = j0 - q.first;
+  if (i0 < 0) i0 = 0;
+  // and up to the last one whose window reaches it, unless the tile holds a sink
+  int i1 = q.nq;
+  if (a.window && j0 >= a.sinks) {
+    const int64_t last = (int64_t)j0 + kT - 1 + a.window - q.first;
+    if (last < i1) i1 = last < 0 ? 0 : (int)last;
+  }
+  for (int r0 = i0 * a.G; r0 < i1 * a.G; r0 += kT) {
+    Rows R{q, s, f, a.G, r0, i1 * a.G - r0 < kT ? i1 * a.G - r0 : kT};
+    __syncthreads();
+    load_rows<T, D>(sQ, static_cast<const T*>(a.q), [&](int r) { return r < R.n ? R.elem(r, a.H, D) : -1; });
+    for (int r = threadIdx.x; r < kT; r += kThreads) {
+      s_pos[r] = r < R.n ? R.pos(r) : -1;
+      s_lse[r] = r < R.n ? a.lse[lse_index(a, q, s, R.token(r), R.head(r))] * kLog2e : 0.f;
+    }
+    __syncthreads();
+    float st[4][4];
+    dots<D>(sK, sQ, ty, tx, st);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int col = tx + 16 * c;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (sees(a, s_pos[col], j0 + 4 * ty + r)) acc[r] += exp2f(fmaf(st[r][c], a.scale_log2, -s_lse[col]));
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const float t = sum16(acc[r]);
+    const int j = j0 + 4 * ty + r;
+    if (tx == 0 && j < q.kv)
+      weights[((int64_t)s * a.Hkv + f) * ((int64_t)a.max_pages << a.page_shift) + j] += t;
+  }
+}
+
+// delta of every row, [S, H, N] fp32: a warp's 8 lanes per row.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) delta_kernel(const AttnArgs a, const T* out, const T* dout, float* delta) {
+  constexpr int kVec = 16 / sizeof(T);
+  constexpr int kLanes = D / kVec < 8 ? D / kVec : 8;
+  const int64_t rows = a.T * a.H;
+  const int64_t per = 256 / kLanes;
+  const int sub = threadIdx.x % kLanes;
+  for (int64_t r0 = blockIdx.x * per; r0 < rows; r0 += gridDim.x * per) {
+    const int64_t r = r0 + threadIdx.x / kLanes;
+    float acc = 0.f;
+    if (r < rows) {
+#pragma unroll
+      for (int c = sub * kVec; c < D; c += kLanes * kVec) {
+        T x[kVec], y[kVec];
+        *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(out + r * D + c);
+        *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(dout + r * D + c);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) acc = fmaf(to_f<T>(x[i]), to_f<T>(y[i]), acc);
+      }
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (r < rows && sub == 0) {
+      const int64_t h = r % a.H, t = r / a.H;
+      const int64_t s = t / a.nq_max, i = t % a.nq_max;
+      delta[(s * a.H + h) * a.nq_max + i] = acc;
+    }
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a, const WindowBwdArgs g) {
+  extern __shared__ __align__(16) float sm[];
+  float* sQ = sm;
+  float* sO = sm + L<D>::kTile;
+  float* sK = sm + 2 * L<D>::kTile;
+  float* sV = sm + 3 * L<D>::kTile;
+  float* sS = sm + 4 * L<D>::kTile;
+  Rows R;
+  R.s = blockIdx.y / a.Hkv;
+  R.f = blockIdx.y % a.Hkv;
+  R.q = seq_of(a, R.s);
+  R.G = a.G;
+  R.r0 = (gridDim.x - 1 - blockIdx.x) * kT;
+  R.n = R.q.nq * a.G - R.r0;
+  if (R.n <= 0) return;
+  if (R.n > kT) R.n = kT;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  auto qrow = [&](int r) { return r < R.n ? R.elem(r, a.H, D) : -1; };
+  load_rows<T, D>(sQ, static_cast<const T*>(a.q), qrow);
+  load_rows<T, D>(sO, static_cast<const T*>(g.dout), qrow);
+  float acc[4][L<D>::kC] = {}, lse2[4], delta[4];
+  int x[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int i = 4 * ty + r;
+    const bool in = i < R.n;
+    const int64_t at = in ? lse_index(a, R.q, R.s, R.token(i), R.head(i)) : 0;
+    lse2[r] = in ? a.lse[at] * kLog2e : 0.f;
+    delta[r] = in ? g.delta[at] : 0.f;
+    x[r] = in ? R.pos(i) : -1;
+  }
+  const BlockList bl = blocks_of<kT>(a, R.pos(0), R.pos(R.n - 1));
+  for (int n = 0; n < bl.count; ++n) {
+    const int j0 = bl.at(n) * kT;
+    auto row = [&](int r) -> int64_t { return j0 + r < R.q.kv ? kv_row(a, R.q, R.s, R.f, j0 + r) : -1; };
+    __syncthreads();
+    load_rows<T, D>(sK, static_cast<const T*>(a.k), row);
+    load_rows<T, D>(sV, static_cast<const T*>(a.v), row);
+    __syncthreads();
+    float s[4][4], dp[4][4];
+    dots<D>(sQ, sK, ty, tx, s);
+    dots<D>(sO, sV, ty, tx, dp);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float p =
+            sees(a, x[r], j0 + tx + 16 * c) ? exp2f(fmaf(s[r][c], a.scale_log2, -lse2[r])) : 0.f;
+        sS[(4 * ty + r) * kPS + tx + 16 * c] = p * (dp[r][c] - delta[r]);
+      }
+    __syncthreads();
+    accumulate<D>(sS, sK, ty, tx, acc);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int i = 4 * ty + r;
+    if (i >= R.n) continue;
+    T* o = static_cast<T*>(g.dq) + R.elem(i, a.H, D);
+#pragma unroll
+    for (int c = 0; c < L<D>::kC; ++c) o[L<D>::col(tx, c)] = from_f<T>(acc[r][c] * a.scale);
+  }
+}
+
+// dk, dv of a tile of 64 keys.  Blocks past the tiles' own are the far items
+// of the sink tiles: the queries past the tile's window, in chunks, each into
+// a partial of its own (far_reduce adds them in order).
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a, const WindowBwdArgs g, const FarPlan fp) {
+  extern __shared__ __align__(16) float sm[];
+  float* sK = sm;
+  float* sV = sm + L<D>::kTile;
+  float* sQ = sm + 2 * L<D>::kTile;
+  float* sO = sm + 3 * L<D>::kTile;
+  float* sP = sm + 4 * L<D>::kTile;
+  float* sS = sP + kT * kPS;
+  __shared__ float s_lse[kT], s_delta[kT];
+  const int s = blockIdx.y / a.Hkv, f = blockIdx.y % a.Hkv;
+  const Seq q = seq_of(a, s);
+  const int tiles = (a.nq_max + kT - 1) / kT;
+  const int far = (int)blockIdx.x - tiles;  // far item, or the tile itself when negative
+  const int tile = far < 0 ? (int)blockIdx.x : far / fp.chunks;
+  const int j0 = tile * kT;
+  // queries whose window reaches the tile: [j0, near); all later ones where
+  // the tile holds sinks and no far items take them
+  const int64_t reach = (int64_t)j0 + kT - 1 + a.window;
+  const int near = reach >= q.nq || (j0 < a.sinks && tile >= fp.sink_tiles) ? q.nq : (int)reach;
+  int i0 = j0, i1 = near;
+  if (far >= 0) {
+    i0 = near + (far % fp.chunks) * fp.chunk;
+    i1 = i0 + fp.chunk < q.nq ? i0 + fp.chunk : q.nq;
+    // an item past the last query still writes its (zero) partial
+  }
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  auto krow = [&](int r) -> int64_t { return j0 + r < q.kv ? kv_row(a, q, s, f, j0 + r) : -1; };
+  load_rows<T, D>(sK, static_cast<const T*>(a.k), krow);
+  load_rows<T, D>(sV, static_cast<const T*>(a.v), krow);
+  float dk[4][L<D>::kC] = {}, dv[4][L<D>::kC] = {};
+  for (int r0 = i0 * a.G; r0 < i1 * a.G; r0 += kT) {
+    Rows R{q, s, f, a.G, r0, i1 * a.G - r0 < kT ? i1 * a.G - r0 : kT};
+    auto qrow = [&](int r) { return r < R.n ? R.elem(r, a.H, D) : -1; };
+    __syncthreads();
+    load_rows<T, D>(sQ, static_cast<const T*>(a.q), qrow);
+    load_rows<T, D>(sO, static_cast<const T*>(g.dout), qrow);
+    for (int r = threadIdx.x; r < kT; r += kThreads) {
+      const int64_t at = r < R.n ? lse_index(a, q, s, R.token(r), R.head(r)) : 0;
+      s_lse[r] = r < R.n ? a.lse[at] * kLog2e : 0.f;
+      s_delta[r] = r < R.n ? g.delta[at] : 0.f;
+    }
+    __syncthreads();
+    float st[4][4], dp[4][4];
+    dots<D>(sK, sQ, ty, tx, st);
+    dots<D>(sV, sO, ty, tx, dp);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int col = tx + 16 * c;
+      const int x = col < R.n ? R.pos(col) : -1;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float p =
+            sees(a, x, j0 + 4 * ty + r) ? exp2f(fmaf(st[r][c], a.scale_log2, -s_lse[col])) : 0.f;
+        sP[(4 * ty + r) * kPS + col] = p;
+        sS[(4 * ty + r) * kPS + col] = p * (dp[r][c] - s_delta[col]);
+      }
+    }
+    __syncthreads();
+    accumulate<D>(sP, sO, ty, tx, dv);
+    accumulate<D>(sS, sQ, ty, tx, dk);
+  }
+  const bool partial = tile < fp.sink_tiles;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int j = j0 + 4 * ty + r;
+    if (partial) {
+      // slot 0 the tile's own, slot 1 + c far item c: [S Hkv][tile][slot][2][kT][D]
+      const int slot = far < 0 ? 0 : 1 + far % fp.chunks;
+      float* p = g.partial + (((((int64_t)blockIdx.y * fp.sink_tiles + tile) * (fp.chunks + 1) + slot) * 2) * kT +
+                              4 * ty + r) * D;
+#pragma unroll
+      for (int c = 0; c < L<D>::kC; ++c) {
+        p[L<D>::col(tx, c)] = dk[r][c] * a.scale;
+        p[kT * D + L<D>::col(tx, c)] = dv[r][c];
+      }
+    } else if (j < q.kv) {
+      const int64_t at = ((q.q0 + j) * a.Hkv + f) * D;
+#pragma unroll
+      for (int c = 0; c < L<D>::kC; ++c) {
+        static_cast<T*>(g.dk)[at + L<D>::col(tx, c)] = from_f<T>(dk[r][c] * a.scale);
+        static_cast<T*>(g.dv)[at + L<D>::col(tx, c)] = from_f<T>(dv[r][c]);
+      }
+    }
+  }
+}
+
+// dk and dv of the sink tiles: their partials added in slot order (the order
+// is fixed, so the result does not change from run to run).
+template <typename T>
+__global__ void __launch_bounds__(256) far_reduce_kernel(const AttnArgs a, const WindowBwdArgs g, const FarPlan fp) {
+  const int sf = blockIdx.y / fp.sink_tiles, tile = blockIdx.y % fp.sink_tiles;
+  const int s = sf / a.Hkv, f = sf % a.Hkv;
+  const int per = fp.tile * a.D;  // values of one gradient's tile
+  const int e = blockIdx.x * 256 + threadIdx.x;
+  if (e >= 2 * per) return;
+  const float* p = g.partial + ((int64_t)sf * fp.sink_tiles + tile) * (fp.chunks + 1) * 2 * per + e;
+  float acc = 0.f;
+  for (int c = 0; c <= fp.chunks; ++c) acc += p[(int64_t)c * 2 * per];
+  const int which = e / per, r = (e % per) / a.D, d = e % a.D;
+  const int j = tile * fp.tile + r;
+  if (j < a.nq_max)
+    static_cast<T*>(which ? g.dv : g.dk)[(((int64_t)s * a.nq_max + j) * a.Hkv + f) * a.D + d] = from_f<T>(acc);
+}
+
+bool set_smem(const void* fn, int bytes) {
+  if (bytes <= 48 * 1024) return true;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
+int ok_launch() { return cudaGetLastError() == cudaSuccess ? LONGNET_OK : LONGNET_ERR_CUDA; }
+
+template <typename T, int D>
+int fwd(const AttnArgs& a, cudaStream_t st) {
+  const int smem = (2 * L<D>::kTile + kT * kPS) * 4;
+  auto fn = fwd_kernel<T, D>;
+  if (!set_smem((const void*)fn, smem)) return LONGNET_ERR_CUDA;
+  const int64_t tiles = ((int64_t)a.nq_max * a.G + kT - 1) / kT;
+  fn<<<dim3((unsigned)tiles, (unsigned)(a.S * a.Hkv)), kThreads, smem, st>>>(a);
+  return ok_launch();
+}
+template <typename T, int D>
+int weights_sum(const AttnArgs& a, float* w, cudaStream_t st) {
+  const int smem = 2 * L<D>::kTile * 4;
+  auto fn = weights_kernel<T, D>;
+  if (!set_smem((const void*)fn, smem)) return LONGNET_ERR_CUDA;
+  const int64_t tiles = (((int64_t)a.max_pages << a.page_shift) + kT - 1) / kT;
+  fn<<<dim3((unsigned)tiles, (unsigned)(a.S * a.Hkv)), kThreads, smem, st>>>(a, w);
+  return ok_launch();
+}
+template <typename T, int D>
+int bwd(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t st) {
+  int rc = launch_window_delta(a, g, st);
+  if (rc) return rc;
+  const FarPlan fp = far_plan(a.S, a.nq_max, a.H, a.Hkv, a.window, a.sinks, kT);
+  const int smem_q = (4 * L<D>::kTile + kT * kPS) * 4, smem_k = smem_q + kT * kPS * 4;
+  auto fq = dq_kernel<T, D>;
+  auto fk = dkv_kernel<T, D>;
+  if (!set_smem((const void*)fq, smem_q) || !set_smem((const void*)fk, smem_k)) return LONGNET_ERR_CUDA;
+  const int64_t items = (a.nq_max + kT - 1) / kT + (int64_t)fp.sink_tiles * fp.chunks;
+  fk<<<dim3((unsigned)items, (unsigned)(a.S * a.Hkv)), kThreads, smem_k, st>>>(a, g, fp);
+  if ((rc = ok_launch())) return rc;
+  const int64_t tiles = ((int64_t)a.nq_max * a.G + kT - 1) / kT;
+  fq<<<dim3((unsigned)tiles, (unsigned)(a.S * a.Hkv)), kThreads, smem_q, st>>>(a, g);
+  if ((rc = ok_launch())) return rc;
+  return launch_far_reduce(a, g, fp, st);
+}
+template <typename T, int D>
+int delta(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t st) {
+  const int64_t rows = a.T * a.H, per = 256 / (D / (16 / (int)sizeof(T)) < 8 ? D / (16 / (int)sizeof(T)) : 8);
+  int64_t blocks = (rows + per - 1) / per;
+  if (blocks > 148 * 16) blocks = 148 * 16;
+  delta_kernel<T, D><<<(unsigned)blocks, 256, 0, st>>>(a, static_cast<const T*>(a.out),
+                                                       static_cast<const T*>(g.dout), g.delta);
+  return ok_launch();
+}
+
+#define LN_BY_D(FN, T, ...)                                      \
+  (a.D == 16 ? FN<T, 16>(__VA_ARGS__)                            \
+             : a.D == 32 ? FN<T, 32>(__VA_ARGS__)                \
+                         : a.D == 64 ? FN<T, 64>(__VA_ARGS__) : FN<T, 128>(__VA_ARGS__))
+#define LN_BY_TYPE(FN, ...)                                                        \
+  (a.dtype == LONGNET_DTYPE_F32 ? LN_BY_D(FN, float, __VA_ARGS__)                  \
+   : a.dtype == LONGNET_DTYPE_BF16 ? LN_BY_D(FN, __nv_bfloat16, __VA_ARGS__)       \
+                                   : LN_BY_D(FN, __half, __VA_ARGS__))
+
+}  // namespace ws
+
+int launch_window_fwd_simt(const AttnArgs& a, cudaStream_t stream) { return LN_BY_TYPE(ws::fwd, a, stream); }
+int launch_weights_simt(const AttnArgs& a, float* weights, cudaStream_t stream) {
+  return LN_BY_TYPE(ws::weights_sum, a, weights, stream);
+}
+int launch_window_bwd_simt(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream) {
+  return LN_BY_TYPE(ws::bwd, a, g, stream);
+}
+int launch_window_delta(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream) {
+  return LN_BY_TYPE(ws::delta, a, g, stream);
+}
+
+int launch_far_reduce(const AttnArgs& a, const WindowBwdArgs& g, const FarPlan& f, cudaStream_t stream) {
+  if (f.sink_tiles == 0) return LONGNET_OK;
+  const dim3 grid((unsigned)((2 * f.tile * a.D + 255) / 256), (unsigned)((int64_t)a.S * a.Hkv * f.sink_tiles));
+  if (a.dtype == LONGNET_DTYPE_F32)
+    ws::far_reduce_kernel<float><<<grid, 256, 0, stream>>>(a, g, f);
+  else if (a.dtype == LONGNET_DTYPE_BF16)
+    ws::far_reduce_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, g, f);
+  else
+    ws::far_reduce_kernel<__half><<<grid, 256, 0, stream>>>(a, g, f);
+  return ws::ok_launch();
+}
+
+// A sink tile's far queries, about as many per item as its window holds (so
+// an item costs what an ordinary tile does), at least 4 tiles' worth and at
+// most 64 items.  With more than 16 sink tiles there are enough of them to
+// fill the GPU without: each then takes all its queries itself.
+FarPlan far_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, int64_t sinks, int tile) {
+  FarPlan f = {tile, 0, 0, 0};
+  // tiles with sinks and queries past their window
+  if (sinks > N) sinks = N;
+  if (sinks <= 0 || window >= N) return f;
+  int64_t t = (sinks + tile - 1) / tile;
+  const int64_t past = N - (tile - 1 + window);  // queries past the first tile's window
+  if (past <= 0) return f;
+  const int64_t has = (past + tile - 1) / tile;  // tiles that have any
+  if (t > has) t = has;
+  if (t > 16) return f;
+  int64_t chunk = window + tile;
+  if (chunk < 4 * tile) chunk = 4 * tile;
+  if ((past + chunk - 1) / chunk > 64) chunk = (past + 63) / 64;
+  f.sink_tiles = (int)t;
+  f.chunk = (int)chunk;
+  f.chunks = (int)((past + chunk - 1) / chunk);
+  return f;
+}
+
+int64_t far_partial_floats(const FarPlan& f, int64_t S, int64_t Hkv, int64_t D) {
+  return S * Hkv * f.sink_tiles * (int64_t)(f.chunks + 1) * 2 * f.tile * D;
+}
+
+}  // namespace longnet
