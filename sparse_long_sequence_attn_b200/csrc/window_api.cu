@@ -10,6 +10,7 @@
 #include "attn_args.cuh"
 #include "longnet.h"
 #include "params.h"
+#include "window_tc.cuh"
 
 using namespace longnet;
 
@@ -47,7 +48,7 @@ int check_window(int64_t B, int64_t N, int64_t H, int64_t Hkv, int64_t D, int64_
   // packed rows and token rows are 32-bit in the kernels; (batch, head) pairs
   // are a grid's second dimension
   if (B > 65535 || H > 65535 || B * Hkv > 65535 || N > ((int64_t)1 << 30) || N * H > ((int64_t)1 << 30) ||
-      B * N * H > ((int64_t)1 << 40))
+      B * N > ((int64_t)1 << 30))
     return LONGNET_ERR_UNSUPPORTED;
   return LONGNET_OK;
 }
@@ -115,13 +116,15 @@ extern "C" int longnet_window_attn_fwd(const void* q, const void* k, const void*
   if (rc) return rc;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4)))
     return LONGNET_ERR_MISALIGNED;
-  if (impl == LONGNET_IMPL_TCGEN05) return LONGNET_ERR_UNSUPPORTED;
   AttnArgs a;
   fill_window(&a, q, k, v, out, lse, B, N, H, Hkv, D, window, sinks, dtype);
+  const bool tc = window_tc_supports(a);
+  if (impl == LONGNET_IMPL_TCGEN05 && !tc) return LONGNET_ERR_UNSUPPORTED;
   int dev = 0;
   rc = device_state(&dev, &a.status);
   if (rc) return rc;
-  return launch_window_fwd_simt(a, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return tc && impl != LONGNET_IMPL_SIMT ? launch_window_fwd_tc(a, nullptr, st) : launch_window_fwd_simt(a, st);
 }
 
 extern "C" int64_t longnet_window_bwd_workspace_bytes(int64_t B, int64_t N, int64_t H, int64_t Hkv, int64_t D,
@@ -198,6 +201,26 @@ int check_paged(int64_t S, int64_t max_q, int64_t H, int64_t Hkv, int64_t D, int
   if (H > 65535 || max_q * H > ((int64_t)1 << 30) || max_q > ((int64_t)1 << 30)) return LONGNET_ERR_UNSUPPORTED;
   return LONGNET_OK;
 }
+
+// The sizes of a checked paged call (no pointers): what its plan goes by.
+void fill_paged(AttnArgs* a, int64_t S, int64_t max_q, int64_t H, int64_t Hkv, int64_t D, int64_t page,
+                int64_t max_pages, int64_t window, int64_t sinks, int dtype) {
+  static const int32_t paged = 0;  // cu_q set: the paged form
+  memset(a, 0, sizeof(*a));
+  set_heads(a, H, Hkv, D, dtype);
+  fill_cache(a, nullptr, nullptr, &paged, nullptr, nullptr, 0, S, 0, page, max_pages);
+  a->nq_max = (int)max_q;
+  const int64_t cap = max_pages * page;
+  a->window = window == 0 || window >= cap ? 0 : (int)window;
+  a->sinks = (int)(sinks < cap ? sinks : cap);
+}
+
+// The workspace of a paged call: the parts of the family that needs most, so
+// that it does not depend on the family.
+int64_t paged_workspace(const AttnArgs& a) {
+  if (!window_tc_supports(a)) return 0;
+  return round256(4 * window_tc_part_floats(a, window_tc_plan(a)));
+}
 }  // namespace
 }  // namespace longnet
 
@@ -207,7 +230,9 @@ extern "C" int64_t longnet_paged_workspace_bytes(int64_t S, int64_t max_q, int64
   const int rc = check_paged(S, max_q, H, Hkv, D, page, max_pages, window, sinks, dtype);
   if (rc) return rc;
   if (weights != 0 && weights != 1) return LONGNET_ERR_INVALID_ARG;
-  return 0;
+  AttnArgs a;
+  fill_paged(&a, S, max_q, H, Hkv, D, page, max_pages, window, sinks, dtype);
+  return paged_workspace(a);
 }
 
 extern "C" int longnet_paged_attn_fwd(const void* q, const void* k_pages, const void* v_pages, void* out, float* lse,
@@ -234,24 +259,21 @@ extern "C" int longnet_paged_attn_fwd(const void* q, const void* k_pages, const 
       !aligned(weights, 4) || !aligned(cu_q, 4) || !aligned(kv_len, 4) || !aligned(table, 4) ||
       !aligned(workspace, 256))
     return LONGNET_ERR_MISALIGNED;
-  if (impl == LONGNET_IMPL_TCGEN05 || impl == LONGNET_IMPL_DECODE) return LONGNET_ERR_UNSUPPORTED;
   AttnArgs a;
-  memset(&a, 0, sizeof(a));
-  set_heads(&a, H, Hkv, D, dtype);
+  fill_paged(&a, S, max_q, H, Hkv, D, page, max_pages, window, sinks, dtype);
   fill_cache(&a, k_pages, v_pages, cu_q, kv_len, table, T, S, n_pages, page, max_pages);
   a.q = q;
   a.out = out;
   a.lse = lse;
-  a.nq_max = (int)max_q;
-  const int64_t cap = max_pages * page;
-  a.window = window == 0 || window >= cap ? 0 : (int)window;
-  a.sinks = (int)(sinks < cap ? sinks : cap);
+  const bool tc = window_tc_supports(a);
+  if (impl == LONGNET_IMPL_DECODE || (impl == LONGNET_IMPL_TCGEN05 && !tc)) return LONGNET_ERR_UNSUPPORTED;
   int dev = 0;
   rc = device_state(&dev, &a.status);
   if (rc) return rc;
   if (T == 0) return LONGNET_OK;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  rc = launch_window_fwd_simt(a, st);
+  rc = tc && impl != LONGNET_IMPL_SIMT ? launch_window_fwd_tc(a, static_cast<float*>(workspace), st)
+                                       : launch_window_fwd_simt(a, st);
   if (rc || !weights) return rc;
   return launch_weights_simt(a, weights, st);
 }

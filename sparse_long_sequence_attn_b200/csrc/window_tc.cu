@@ -1,0 +1,535 @@
+// The sliding-window and paged-cache attention forward on the tensor cores
+// (tcgen05), bf16 and fp16, D = 16, 32, 64 or 128.
+//
+// Mathematics: softmax(Q K^T / sqrt(D)) V over the visible keys in one pass,
+// with each row's running maximum and sum in fp32; P is rounded to the input
+// format for the second product (the tensor cores take 16-bit operands), the
+// sum is of the unrounded values.
+//
+// Layout.  The G query heads of a key/value head read the same keys, so a
+// tile's 128 rows are 128 / G tokens by G heads.  A CTA owns two row tiles (A
+// and B) of one key/value head and streams 128-key blocks, K and V in turn,
+// through one ring that both tiles read: a key block is fetched once for 256
+// rows.  It visits only the blocks the mask reaches (those with sinks, then
+// those of the window).
+//   warps 0-3, 4-7  softmax of tile A and B, a thread per row: scores from
+//                   TMEM, P back over them in the input format, O rescaled in
+//                   TMEM only when the row maximum grew by more than 2^8
+//   warp 8          TMA loads; a block of a paged cache is a box per page
+//   warp 9          (10 and 11 idle, registers only) MMA issue: per block [P V of A, scores of A], [the same
+//                   of B], so one tile's products run under the other's
+//                   softmax.  In-order issue makes the score buffer's reuse
+//                   safe without a second buffer.
+// TMEM: two 128-column score buffers and two D-column accumulators.
+// With fewer rows than one tile per key/value head (short chunks over a long
+// cache) both streams take the same tile and alternate blocks, and the keys
+// are split over CTAs; the parts are joined by combine_kernel.
+// Slots past a sequence's keys may hold anything: their scores are masked
+// before use and their value rows are overwritten with zeros in shared memory.
+// Every wait is bounded; on a timeout the kernel records the status word,
+// stops issuing, drains what it issued and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "attn_args.cuh"
+#include "tc_ptx.cuh"
+#include "window_tc.cuh"
+
+namespace longnet {
+namespace wt {
+using namespace tc;
+
+// 384 x 168 registers at launch, dealt again as 208 for each softmax thread
+// and 88 for the loading and issuing warps: 128 x (208 + 208 + 88) = 384 x 168
+constexpr int kThreads = 384;
+constexpr int kTma = 8, kMma = 9;  // warps
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;  // after the two score buffers
+
+template <int kD>
+struct L : Panels<kD> {
+  using P = Panels<kD>;
+  static constexpr int kQBytes = kTile * kD * 2;      // one row tile
+  static constexpr int kStageBytes = kTile * kD * 2;  // one block of keys or values
+  static constexpr int kStages = kD == 128 ? 5 : 8;
+  static constexpr int kBars = 2 * kQBytes + kStages * kStageBytes;
+  // one CTA per SM at every D: its TMEM columns are all of the SM's
+  static constexpr int kSmem = kBars + 512 + 1024 > 120 * 1024 ? kBars + 512 + 1024 : 120 * 1024;
+};
+
+template <int kFmt, int kD, bool kPaged>
+__global__ void __launch_bounds__(kThreads, 1)
+    fwd_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Maps maps, const Plan plan) {
+  using LL = L<kD>;
+  constexpr int kPanels = LL::kPanels, kPanelBytes = kTile * LL::kRowBytes, S = LL::kStages;
+  constexpr uint32_t kDescHi = LL::kDescHi;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int s = blockIdx.y / a.Hkv, f = blockIdx.y % a.Hkv;
+  const Seq q = seq_of(a, s);
+  const int split = blockIdx.x % plan.splits;
+  const int pair = (int)(gridDim.x / plan.splits) - 1 - blockIdx.x / plan.splits;  // the longest first
+  const int tpt = plan.tokens;                                                      // tokens of a row tile
+  const int t0 = plan.alternate ? 0 : pair * 2 * tpt;
+  if (t0 >= q.nq) return;  // whole CTA, before any barrier or TMEM use
+  const int t1 = t0 + (plan.alternate ? tpt : 2 * tpt) < q.nq ? t0 + (plan.alternate ? tpt : 2 * tpt) : q.nq;
+  const BlockList bl = blocks_of<kTile>(a, q.first + t0, q.first + t1 - 1);
+  const int per = (bl.count + plan.splits - 1) / plan.splits;
+  const int n0 = split * per < bl.count ? split * per : bl.count;
+  const int cnt = n0 + per < bl.count ? per : bl.count - n0;  // blocks [n0, n0 + cnt) of the list
+  auto block_key = [&](int n) { return bl.at(n0 + n) * kTile; };
+  // tokens [ta, tb) of stream st, empty when it has none
+  auto tok_begin = [&](int st) { return plan.alternate ? t0 : t0 + st * tpt; };
+  auto tok_end = [&](int st) {
+    const int e = tok_begin(st) + tpt;
+    return e < t1 ? e : t1;
+  };
+  auto active = [&](int st, int n) -> bool {
+    if (plan.alternate) return (n & 1) == st;
+    const int b = tok_begin(st), e = tok_end(st), j0 = block_key(n);
+    if (b >= e) return false;
+    const int lo = q.first + b, hi = q.first + e - 1;
+    return j0 <= hi && (a.window == 0 || j0 < a.sinks || j0 + kTile - 1 > lo - a.window);
+  };
+
+  uint8_t* sQ = smem;
+  uint8_t* sStage = smem + 2 * LL::kQBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + LL::kBars);
+  uint64_t* bar_q = bars;
+  uint64_t* bar_full = bars + 1;       // [S]
+  uint64_t* bar_empty = bars + 1 + S;  // [S]
+  uint64_t* bar_s = bars + 1 + 2 * S;  // [2] scores of a stream in TMEM
+  uint64_t* bar_p = bar_s + 2;         // [2] P of a stream in TMEM
+  uint64_t* bar_o = bar_s + 4;         // [2] a stream's last product done
+  uint64_t* bar_tail = bar_s + 6;      // the values of a block with slots past the sequence
+  uint64_t* bar_drain = bar_s + 7;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_s + 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(bar_q, 1);
+    for (int i = 0; i < S; ++i) {
+      mbar_init(bar_full + i, 1);
+      mbar_init(bar_empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_s + i, 1);
+      mbar_init(bar_p + i, 128);
+      mbar_init(bar_o + i, 1);
+    }
+    mbar_init(bar_tail, 1);
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kTma && lane < 3) prefetch_tmap(&maps.m[lane]);
+  if (warp == kMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Waiter wt{abort_flag, a.status, kWaitLimitNs};
+
+  if (warp >= kTma) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp == kTma) {
+    // ------------------------------------------------------------ loads
+    bool ok = true;
+    const int qtiles = plan.alternate || t0 + tpt >= t1 ? 1 : 2;
+    if (cnt > 0 && lane == 0) {
+      mbar_arrive_expect_tx(bar_q, (uint32_t)(qtiles * kPanels * tpt * a.G * LL::kRowBytes));
+      for (int st = 0; st < qtiles; ++st)
+#pragma unroll
+        for (int pn = 0; pn < kPanels; ++pn)
+          tma_load_3d(sQ + st * LL::kQBytes + pn * kPanelBytes, &maps.m[0], bar_q, LL::kPanelElems * pn, f * a.G,
+                      (int)(q.q0 + t0 + st * tpt));
+    }
+    int issued = 0;
+    for (int it = 0; it < 2 * cnt && ok; ++it) {
+      const int st = it % S;
+      if (it >= S) ok = wt.wait_warp(bar_empty + st, ((it / S) - 1) & 1);
+      if (!ok) break;
+      const int j0 = block_key(it >> 1);
+      const CUtensorMap* map = &maps.m[1 + (it & 1)];
+      uint8_t* dst = sStage + st * LL::kStageBytes;
+      if (!kPaged) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar_full + st, LL::kStageBytes);
+#pragma unroll
+          for (int pn = 0; pn < kPanels; ++pn)
+            tma_load_4d(dst + pn * kPanelBytes, map, bar_full + st, LL::kPanelElems * pn, f, j0, s);
+        }
+      } else {
+        load_pages<kD>(a, q, s, f, j0, kTile, (it & 1) != 0, map, dst, bar_full + st, bar_tail, lane, wt, &ok);
+      }
+      issued = it + 1;
+    }
+    // drain: every issued load has landed before the CTA may exit
+    if (lane == 0) {
+      if (cnt > 0 && !mbar_wait(bar_q, 0, kWaitLimitNs)) record_status(a.status, kStatusTimeout);
+      for (int it = issued > S ? issued - S : 0; it < issued && ok; ++it)
+        if (!mbar_wait(bar_full + (it % S), (it / S) & 1, kWaitLimitNs)) {
+          record_status(a.status, kStatusTimeout);
+          break;
+        }
+    }
+  } else if (warp == kMma) {
+    // ------------------------------------------------------------ MMA issue
+    if (lane == 0 && cnt > 0) {
+      constexpr uint32_t kIdS = idesc_f16kind(kTile, kTile, false, kFmt);  // 128 x 128, B K-major
+      constexpr uint32_t kIdO = idesc_f16kind(kTile, kD, true, kFmt);      // 128 x D, B MN-major
+      constexpr uint32_t lbo_mn = ((uint32_t)kPanelBytes >> 4) << 16;      // V's panel stride along D
+      auto stage_lo = [&](int it) -> uint32_t { return smem_u32(sStage + (it % S) * LL::kStageBytes) >> 4; };
+      auto scores = [&](int st, int n) {
+        const uint32_t q_lo = smem_u32(sQ + (plan.alternate ? 0 : st) * LL::kQBytes) >> 4;
+        const uint32_t k_lo = stage_lo(2 * n);
+#pragma unroll
+        for (int pn = 0; pn < kPanels; ++pn)
+#pragma unroll
+          for (int kk = 0; kk < LL::kPanelElems / 16; ++kk)
+            mma_ss(tmem + kTile * st, desc_from(((q_lo + pn * (kPanelBytes >> 4)) | (1u << 16)) + kk * 2, kDescHi),
+                   desc_from(((k_lo + pn * (kPanelBytes >> 4)) | (1u << 16)) + kk * 2, kDescHi), kIdS,
+                   (pn > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(bar_s + st);
+      };
+      int pending[2] = {-1, -1}, done[2] = {0, 0};  // block whose P V is due; blocks whose P V is issued
+      int left[2] = {0, 0};
+      for (int n = 0; n < cnt; ++n)
+        for (int st = 0; st < 2; ++st) left[st] += active(st, n) ? 1 : 0;
+      auto product = [&](int st) -> bool {
+        const int n = pending[st];
+        pending[st] = -1;
+        if (!wt.wait(bar_full + (2 * n + 1) % S, ((2 * n + 1) / S) & 1)) return false;
+        if (!wt.wait(bar_p + st, done[st] & 1)) return false;
+        tc_fence_after();
+        const uint32_t v_lo = stage_lo(2 * n + 1);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_ts(tmem + kColO + kD * st, tmem + kTile * st + kk * 8,
+                 desc_from((v_lo | lbo_mn) + kk * (16 * LL::kRowBytes >> 4), kDescHi), kIdO,
+                 (done[st] > 0 || kk > 0) ? 1u : 0u);
+        if (++done[st] == left[st]) tc_commit(bar_o + st);
+        return true;
+      };
+      bool ok = wt.wait(bar_q, 0);
+      for (int n = 0; n <= cnt && ok; ++n) {
+        bool on[2] = {false, false};
+        if (n < cnt) {
+          ok = wt.wait(bar_full + (2 * n) % S, ((2 * n) / S) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          on[0] = active(0, n);
+          on[1] = active(1, n);
+        }
+        // a stream with nothing due starts its scores before the other's P is
+        // waited for
+        for (int st = 0; st < 2; ++st)
+          if (on[st] && pending[st] < 0) {
+            scores(st, n);
+            on[st] = false;
+            pending[st] = n + cnt + 1;  // due next time
+          }
+        for (int st = 0; st < 2 && ok; ++st) {
+          if (pending[st] >= 0 && pending[st] <= cnt) ok = product(st);
+          if (ok && on[st]) {
+            scores(st, n);
+            pending[st] = n + cnt + 1;
+          }
+          if (pending[st] > cnt) pending[st] -= cnt + 1;
+        }
+        if (!ok) break;
+        if (n < cnt) tc_commit(bar_empty + (2 * n) % S);
+        if (n > 0) tc_commit(bar_empty + (2 * n - 1) % S);
+      }
+      // drain: all issued MMAs complete before TMEM is released
+      tc_commit(bar_drain);
+      if (!mbar_wait(bar_drain, 0, kWaitLimitNs)) record_status(a.status, kStatusTimeout);
+    }
+  }
+  } else {
+    // ------------------------------------------------------------ softmax and epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int st = warp >> 2;
+    const int row = 32 * (warp & 3) + lane;  // TMEM lane = tile row
+    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t s_col = tmem + lane_base + kTile * st, o_col = tmem + lane_base + kColO + kD * st;
+    const int ta = tok_begin(st), tb = tok_end(st);
+    const int i = ta + row / a.G;
+    const bool row_ok = row < tpt * a.G && i < tb;
+    const int x = row_ok ? q.first + i : -1;
+    const int x_lo = q.first + ta, x_hi = q.first + tb - 1;
+    const uint64_t sc2 = f32x2(a.scale_log2, a.scale_log2);
+    float m_use = -INFINITY, l_run = 0.f;
+    int done = 0;
+    bool ok = true;
+    for (int n = 0; n < cnt && ok; ++n) {
+      if (!active(st, n)) continue;
+      const int j0 = block_key(n);
+      ok = wt.wait_warp(bar_s + st, done & 1);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sr[kTile];
+      LN_TMEM_LD32(s_col, (sr + 0));
+      LN_TMEM_LD32(s_col + 32, (sr + 32));
+      LN_TMEM_LD32(s_col + 64, (sr + 64));
+      LN_TMEM_LD32(s_col + 96, (sr + 96));
+      tmem_wait_ld();
+      // a block that some row of the tile does not see whole
+      if (j0 + kTile - 1 > x_lo || (a.window && x_hi - j0 >= a.window && j0 + kTile > a.sinks) || !row_ok) {
+        const int hi = x - j0, lo = a.window ? hi - a.window + 1 : -1, sk = a.sinks - j0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t keep = below(hi + 1 - 32 * w) & (~below(lo - 32 * w) | below(sk - 32 * w));
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (!((keep >> c) & 1)) sr[32 * w + c] = __float_as_uint(-INFINITY);
+        }
+      }
+      float pm[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) pm[e] = __uint_as_float(sr[e]);
+#pragma unroll
+      for (int c = 8; c < kTile; ++c) pm[c & 7] = fmaxf(pm[c & 7], __uint_as_float(sr[c]));
+      const float mx = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
+                             fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
+      const float m_blk = mx * a.scale_log2;
+      float corr = 1.f;
+      if (m_blk > m_use + 8.f) {  // also from -inf, the first visible key
+        corr = ex2(m_use - m_blk);
+        m_use = m_blk;
+      }
+      if (done > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
+        // the products of earlier blocks ran before these scores (in-order issue)
+        l_run *= corr;
+        constexpr int kChunk = kD < 32 ? kD : 32;
+#pragma unroll 1
+        for (int c0 = 0; c0 < kD; c0 += kChunk) {
+          uint32_t rr[kChunk];
+          tmem_load<kChunk>(o_col + c0, rr);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < kChunk; ++c) rr[c] = __float_as_uint(__uint_as_float(rr[c]) * corr);
+          tmem_store<kChunk>(o_col + c0, rr);
+        }
+        tmem_wait_st();
+      }
+      // P = 2^(s scale - m), packed over the first 64 columns
+      const float base = m_use == -INFINITY ? 0.f : m_use;  // a row with nothing to see so far
+      const uint64_t nm2 = f32x2(-base, -base);
+      uint64_t ls[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          float xa, xb;
+          f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[64 * w + 2 * c]), __uint_as_float(sr[64 * w + 2 * c + 1])),
+                                sc2, nm2),
+                      xa, xb);
+          const float pa = ex2(xa), pb = ex2(xb);
+          ls[c & 3] = add_f32x2(ls[c & 3], f32x2(pa, pb));
+          pk[c] = pack2<kFmt>(pa, pb);
+        }
+        LN_TMEM_ST32(s_col + 32 * w, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar_p + st);
+      float t0s, t1s;
+      f32x2_split(add_f32x2(add_f32x2(ls[0], ls[1]), add_f32x2(ls[2], ls[3])), t0s, t1s);
+      l_run += t0s + t1s;
+      ++done;
+    }
+    if (ok && done > 0) ok = wt.wait_warp(bar_o + st, 0);
+    if (ok && ta < tb) {
+      tc_fence_after();
+      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      const int h = f * a.G + row % a.G;
+      constexpr int kChunk = kD < 32 ? kD : 32;
+      const int part = plan.alternate ? 2 * split + st : split;
+      const int64_t prow = (((int64_t)part * a.S + s) * a.nq_max + i) * a.H + h;
+#pragma unroll 1
+      for (int c0 = 0; c0 < kD; c0 += kChunk) {
+        uint32_t rr[kChunk];
+        if (done > 0) {
+          tmem_load<kChunk>(o_col + c0, rr);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int c = 0; c < kChunk; ++c) rr[c] = 0;
+        }
+        if (row_ok) {
+          if (plan.parts > 1) {
+            float4* o = reinterpret_cast<float4*>(plan.part_out + prow * kD + c0);
+#pragma unroll
+            for (int c = 0; c < kChunk; c += 4)
+              o[c / 4] = make_float4(__uint_as_float(rr[c]) * inv, __uint_as_float(rr[c + 1]) * inv,
+                                     __uint_as_float(rr[c + 2]) * inv, __uint_as_float(rr[c + 3]) * inv);
+          } else {
+            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                                ((q.q0 + i) * a.H + h) * (int64_t)kD + c0);
+#pragma unroll
+            for (int c = 0; c < kChunk; c += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack2<kFmt>(__uint_as_float(rr[c + 2 * e]) * inv, __uint_as_float(rr[c + 2 * e + 1]) * inv);
+              o[c / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+      if (row_ok) {
+        const float lse2 = l_run > 0.f ? m_use + log2f(l_run) : -INFINITY;
+        if (plan.parts > 1)
+          plan.part_lse[prow] = lse2;
+        else if (a.lse)
+          a.lse[lse_index(a, q, s, i, h)] = lse2 * kLn2;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+// Joins the parts of every row: out = sum_p 2^(lse_p - m) O_p / sum_p 2^(lse_p - m).
+// A warp per row; a row's parts are added in order.
+template <int kFmt, int kD>
+__global__ void __launch_bounds__(256) combine_kernel(const AttnArgs a, const float* part_out, const float* part_lse,
+                                                      int parts) {
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = (int64_t)a.S * a.nq_max * a.H;
+  if (row >= rows) return;
+  const int h = (int)(row % a.H), i = (int)((row / a.H) % a.nq_max), s = (int)(row / a.H / a.nq_max);
+  const Seq q = seq_of(a, s);
+  if (i >= q.nq) return;
+  float m = -INFINITY;
+  for (int p = lane; p < parts; p += 32) m = fmaxf(m, part_lse[p * rows + row]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float base = m == -INFINITY ? 0.f : m;
+  constexpr int kE = kD / 32 > 0 ? kD / 32 : 1;  // values of a lane
+  const bool on = lane * kE < kD;
+  float acc[kE] = {}, sum = 0.f;
+  for (int p = 0; p < parts; ++p) {
+    const float l = part_lse[p * rows + row];
+    const float w = ex2(l - base);
+    sum += w;
+    if (on && w > 0.f) {
+      const float* src = part_out + (p * rows + row) * kD + lane * kE;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) acc[e] = fmaf(w, src[e], acc[e]);
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  if (on) {
+    uint16_t* o = static_cast<uint16_t*>(a.out) + ((q.q0 + i) * a.H + h) * (int64_t)kD + lane * kE;
+    if constexpr (kE == 1) {
+      o[0] = (uint16_t)pack2<kFmt>(acc[0] * inv, 0.f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kE; e += 2)
+        *reinterpret_cast<uint32_t*>(o + e) = pack2<kFmt>(acc[e] * inv, acc[e + 1] * inv);
+    }
+  }
+  if (lane == 0 && a.lse) a.lse[lse_index(a, q, s, i, h)] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+template <int kFmt, int kD>
+int combine(const AttnArgs& a, const float* po, const float* pl, int parts, cudaStream_t stream) {
+  const int64_t rows = (int64_t)a.S * a.nq_max * a.H;
+  combine_kernel<kFmt, kD><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(a, po, pl, parts);
+  return cudaGetLastError() == cudaSuccess ? LONGNET_OK : LONGNET_ERR_CUDA;
+}
+
+template <int kFmt, int kD>
+int launch_typed(const AttnArgs& a, const Plan& plan, cudaStream_t stream) {
+  using LL = L<kD>;
+  Maps maps;
+  EncodeTiledFn enc = get_encoder();
+  if (!enc) return LONGNET_ERR_CUDA;
+  if (!encode_q(enc, &maps.m[0], a.q, a, plan.tokens) || !encode_kv(enc, &maps.m[1], a.k, a, kTile) ||
+      !encode_kv(enc, &maps.m[2], a.v, a, kTile))
+    return LONGNET_ERR_CUDA;
+  auto fn = a.cu_q ? fwd_kernel<kFmt, kD, true> : fwd_kernel<kFmt, kD, false>;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, LL::kSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return LONGNET_ERR_CUDA;
+  }
+  const int64_t pairs = plan.alternate ? 1 : ((int64_t)a.nq_max + 2 * plan.tokens - 1) / (2 * plan.tokens);
+  fn<<<dim3((unsigned)(pairs * plan.splits), (unsigned)(a.S * a.Hkv)), kThreads, LL::kSmem, stream>>>(a, maps, plan);
+  if (cudaGetLastError() != cudaSuccess) return LONGNET_ERR_CUDA;
+  return plan.parts > 1 ? combine<kFmt, kD>(a, plan.part_out, plan.part_lse, plan.parts, stream) : LONGNET_OK;
+}
+
+}  // namespace wt
+
+bool window_tc_supports(const AttnArgs& a) {
+  return (a.dtype == LONGNET_DTYPE_BF16 || a.dtype == LONGNET_DTYPE_F16) && a.G <= wt::kTile;
+}
+
+#define LN_TC_BY(FN, ...)                                                                              \
+  (a.dtype == LONGNET_DTYPE_F16                                                                        \
+       ? (a.D == 16 ? FN<tc::kFmtF16, 16>(__VA_ARGS__) : a.D == 32 ? FN<tc::kFmtF16, 32>(__VA_ARGS__)   \
+          : a.D == 64 ? FN<tc::kFmtF16, 64>(__VA_ARGS__) : FN<tc::kFmtF16, 128>(__VA_ARGS__))           \
+       : (a.D == 16 ? FN<tc::kFmtBF16, 16>(__VA_ARGS__) : a.D == 32 ? FN<tc::kFmtBF16, 32>(__VA_ARGS__) \
+          : a.D == 64 ? FN<tc::kFmtBF16, 64>(__VA_ARGS__) : FN<tc::kFmtBF16, 128>(__VA_ARGS__)))
+
+// The split of one call.  A contiguous call is never split (its row tiles fill
+// the GPU); a paged one is when its row tiles leave SMs idle: enough splits to
+// fill them once, of at least four blocks each at the cache's capacity.
+WindowTcPlan window_tc_plan(const AttnArgs& a) {
+  WindowTcPlan p;
+  memset(&p, 0, sizeof(p));
+  p.tokens = wt::kTile / a.G;
+  p.splits = 1;
+  p.parts = 1;
+  if (!a.cu_q) return p;
+  p.alternate = a.nq_max <= p.tokens;
+  const int64_t cap_blocks = (((int64_t)a.max_pages << a.page_shift) + wt::kTile - 1) / wt::kTile;
+  // blocks a row tile can visit
+  const int64_t reach = a.window ? ((int64_t)a.window + a.sinks + p.tokens * 2) / wt::kTile + 2 : cap_blocks;
+  const int64_t blocks = reach < cap_blocks ? reach : cap_blocks;
+  const int64_t pairs = p.alternate ? 1 : ((int64_t)a.nq_max + 2 * p.tokens - 1) / (2 * p.tokens);
+  const int64_t ctas = pairs * a.S * a.Hkv;
+  int64_t splits = ctas >= 148 ? 1 : 148 / ctas;
+  if (splits > blocks / 4) splits = blocks / 4;
+  if (splits < 1) splits = 1;
+  if (splits > 64) splits = 64;
+  p.splits = (int)splits;
+  p.parts = (int)(p.alternate ? 2 * splits : splits);
+  return p;
+}
+
+int64_t window_tc_part_floats(const AttnArgs& a, const WindowTcPlan& p) {
+  return p.parts > 1 ? (int64_t)p.parts * a.S * a.nq_max * a.H * (a.D + 1) : 0;
+}
+
+int launch_window_fwd_tc(const AttnArgs& a, float* parts, cudaStream_t stream) {
+  WindowTcPlan p = window_tc_plan(a);
+  p.part_out = parts;
+  p.part_lse = parts ? parts + (int64_t)p.parts * a.S * a.nq_max * a.H * a.D : nullptr;
+  return LN_TC_BY(wt::launch_typed, a, p, stream);
+}
+
+int launch_combine(const AttnArgs& a, const float* part_out, const float* part_lse, int parts, cudaStream_t stream) {
+  return LN_TC_BY(wt::combine, a, part_out, part_lse, parts, stream);
+}
+
+}  // namespace longnet

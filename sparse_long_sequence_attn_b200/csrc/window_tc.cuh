@@ -1,0 +1,206 @@
+// Shared pieces of the tcgen05 kernels of the sliding-window and paged-cache
+// attention: operand tile geometry, tensor maps, page-wise block loads and
+// bounded waits.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "attn_args.cuh"
+#include "tc_ptx.cuh"
+
+namespace longnet {
+
+// How a forward call is cut.  tokens: tokens of a 128-row tile; alternate: one
+// row tile per key/value head, whose blocks the two streams take in turn;
+// splits: CTAs that share a row tile's blocks; parts: partial results of a
+// row, 1 when the kernel writes out itself.
+struct WindowTcPlan {
+  int tokens, splits, alternate, parts;
+  float* part_out;  // [parts, S, nq_max, H, D]
+  float* part_lse;  // [parts, S, nq_max, H], log2 domain
+};
+
+bool window_tc_supports(const AttnArgs& a);
+WindowTcPlan window_tc_plan(const AttnArgs& a);
+int64_t window_tc_part_floats(const AttnArgs& a, const WindowTcPlan& p);
+int launch_window_fwd_tc(const AttnArgs& a, float* parts, cudaStream_t stream);
+int launch_combine(const AttnArgs& a, const float* part_out, const float* part_lse, int parts, cudaStream_t stream);
+
+namespace wt {
+using namespace tc;
+
+using Plan = WindowTcPlan;
+constexpr int kTile = 128;  // rows of a tile, keys of a block
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
+
+// Rows of D 16-bit elements as swizzle panels: D = 64 or 128 is one or two
+// panels of 128-byte rows, D = 32 or 16 one panel of 64- or 32-byte rows.
+template <int kD>
+struct Panels {
+  static constexpr int kPanels = kD >= 64 ? kD / 64 : 1;
+  static constexpr int kPanelElems = kD >= 64 ? 64 : kD;
+  static constexpr int kRowBytes = kPanelElems * 2;
+  // descriptor high word: stride between 8-row groups, sm_100 version, layout
+  // type (128-byte swizzle 2, 64-byte 4, 32-byte 6)
+  static constexpr uint32_t kDescHi = (uint32_t)(8 * kRowBytes >> 4) | (1u << 14) |
+                                      ((kRowBytes == 128 ? 2u : kRowBytes == 64 ? 4u : 6u) << 29);
+};
+
+struct __align__(64) Maps {
+  CUtensorMap m[3];  // q, k, v
+};
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+struct Waiter {
+  volatile int* abort_flag;
+  int* status;
+  uint64_t limit;
+  __device__ bool wait(uint64_t* bar, uint32_t parity) {
+    const uint32_t a = smem_u32(bar);
+    if (mbar_try_wait(a, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t it = 1;; ++it) {
+      if (mbar_try_wait(a, parity)) return true;
+      if ((it & 15u) == 0) {
+        if (*abort_flag) return false;
+        if (global_ns() - t0 > limit) {
+          *abort_flag = 1;
+          record_status(status, kStatusTimeout);
+          return false;
+        }
+      }
+    }
+  }
+  __device__ bool wait_warp(uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); }
+};
+
+// The lowest n bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t below(int n) {
+  return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
+template <int kN>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[kN]) {
+  if constexpr (kN == 32) {
+    LN_TMEM_LD32(taddr, r);
+  } else {
+    LN_TMEM_LD16(taddr, r);
+  }
+}
+template <int kN>
+__device__ __forceinline__ void tmem_store(uint32_t taddr, uint32_t (&r)[kN]) {
+  if constexpr (kN == 32) {
+    LN_TMEM_ST32(taddr, r);
+  } else {
+    LN_TMEM_ST16(taddr, r);
+  }
+}
+
+// Keys [j0, j0 + rows) of a paged cache into a block in shared memory, by one
+// warp: a lane looks up a page and issues its boxes.  Pages past the
+// sequence's last key are not read.  For values, the rows past the last key
+// are then overwritten with zeros (a weight of 0 would turn a NaN there into
+// a NaN row): such a block's loads complete on bar_tail (used once, by the
+// last block) and the warp arrives on bar_full itself.
+template <int kD>
+__device__ __forceinline__ void load_pages(const AttnArgs& a, const Seq& q, int s, int f, int j0, int rows, bool values,
+                                           const CUtensorMap* map, uint8_t* dst, uint64_t* bar_full,
+                                           uint64_t* bar_tail, int lane, Waiter& wt, bool* ok) {
+  using LL = Panels<kD>;
+  const int box = a.page < rows ? a.page : rows;  // rows of a box
+  const int boxes = rows / box;                   // at most 16
+  const int j = j0 + lane * box;
+  const bool live = lane < boxes && j < q.kv;
+  int pg = 0;
+  if (live) {
+    pg = a.table[(int64_t)s * a.max_pages + (j >> a.page_shift)];
+    if (pg < 0 || pg >= a.n_pages) {
+      record_status(a.status, kStatusBounds);
+      pg = a.n_pages;  // past the tensor: zeros
+    }
+  }
+  const uint32_t count = __popc(__ballot_sync(0xffffffffu, live));
+  const bool tail = values && j0 + rows > q.kv;
+  uint64_t* bar = tail ? bar_tail : bar_full;
+  if (lane == 0) mbar_arrive_expect_tx(bar, count * (uint32_t)(box * kD * 2));
+  __syncwarp();
+  if (live) {
+#pragma unroll
+    for (int pn = 0; pn < LL::kPanels; ++pn)
+      tma_load_4d(dst + pn * rows * LL::kRowBytes + lane * box * LL::kRowBytes, map, bar, LL::kPanelElems * pn, f,
+                  j & (a.page - 1), pg);
+  }
+  if (tail) {
+    if (!wt.wait_warp(bar_tail, 0)) {
+      *ok = false;
+      return;
+    }
+    const int keep = q.kv - j0;  // rows with a key
+    constexpr int kCpr = LL::kRowBytes / 16;
+    const int chunks = (rows - keep) * kCpr;  // of one panel
+    for (int pn = 0; pn < LL::kPanels; ++pn)
+      for (int c = lane; c < chunks; c += 32)
+        *reinterpret_cast<uint4*>(dst + pn * rows * LL::kRowBytes + keep * LL::kRowBytes + c * 16) =
+            make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_full);
+  }
+}
+
+// [T, H, D] as (d, h, t): a box is one panel of G heads by `tokens` tokens.
+inline bool encode_q(EncodeTiledFn enc, CUtensorMap* map, const void* base, const AttnArgs& a, int tokens) {
+  const cuuint64_t row = (cuuint64_t)a.D * 2;
+  cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.H, (cuuint64_t)a.T};
+  cuuint64_t strides[2] = {row, row * a.H};
+  const int pe = a.D >= 64 ? 64 : a.D;
+  cuuint32_t box[3] = {(cuuint32_t)pe, (cuuint32_t)a.G, (cuuint32_t)tokens};
+  cuuint32_t one[3] = {1, 1, 1};
+  return enc(map, a.dtype == LONGNET_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             pe == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+             : pe == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                        : CU_TENSOR_MAP_SWIZZLE_32B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Keys or values as (d, head, slot, page) or, contiguous, (d, head, position,
+// batch); a box is one panel of `rows` slots, or of a page with fewer.
+inline bool encode_kv(EncodeTiledFn enc, CUtensorMap* map, const void* base, const AttnArgs& a, int rows) {
+  const bool paged = a.cu_q != nullptr;
+  const int64_t slots = paged ? a.page : a.nq_max, outer = paged ? a.n_pages : a.S;
+  if (paged && rows > a.page) rows = a.page;
+  const cuuint64_t row = (cuuint64_t)a.D * 2;
+  cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.Hkv, (cuuint64_t)slots, (cuuint64_t)outer};
+  cuuint64_t strides[3] = {row, row * a.Hkv, row * a.Hkv * slots};
+  const int pe = a.D >= 64 ? 64 : a.D;
+  cuuint32_t box[4] = {(cuuint32_t)pe, 1, (cuuint32_t)rows, 1};
+  cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc(map, a.dtype == LONGNET_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+             const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             pe == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+             : pe == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                        : CU_TENSOR_MAP_SWIZZLE_32B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace wt
+}  // namespace longnet
