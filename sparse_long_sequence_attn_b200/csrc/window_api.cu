@@ -71,11 +71,14 @@ void fill_window(AttnArgs* a, const void* q, const void* k, const void* v, void*
 
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
-// The workspace of the backward: delta, then the far partials.
-int64_t bwd_workspace(int64_t B, int64_t N, int64_t H, int64_t Hkv, int64_t D, int64_t window, int64_t sinks,
-                      int tile) {
-  const FarPlan f = far_plan(B, N, H, Hkv, window, sinks, tile);
-  return round256(4 * B * N * H) + round256(4 * far_partial_floats(f, B, Hkv, D));
+// The workspace of the backward: delta, then the far partials of the family
+// that needs most, so that it does not depend on the family.
+int64_t bwd_workspace(int64_t B, int64_t N, int64_t H, int64_t Hkv, int64_t D, int64_t window, int64_t sinks) {
+  window = window < N ? window : N;
+  sinks = sinks < N ? sinks : N;
+  const int64_t simt = far_partial_floats(far_plan(B, N, H, Hkv, window, sinks, 64), B, Hkv, D);
+  const int64_t tc = far_partial_floats(far_plan(B, N, H, Hkv, window, sinks, window_bwd_tc_tile(D)), B, Hkv, D);
+  return round256(4 * B * N * H) + round256(4 * (simt > tc ? simt : tc));
 }
 
 int check_cache(int64_t S, int64_t Hkv, int64_t D, int64_t n_pages, int64_t page, int64_t max_pages, int dtype) {
@@ -131,7 +134,7 @@ extern "C" int64_t longnet_window_bwd_workspace_bytes(int64_t B, int64_t N, int6
                                                       int64_t window, int64_t sinks, int dtype) {
   const int rc = check_window(B, N, H, Hkv, D, window, sinks, dtype);
   if (rc) return rc;
-  return bwd_workspace(B, N, H, Hkv, D, window, sinks, 64);
+  return bwd_workspace(B, N, H, Hkv, D, window, sinks);
 }
 
 extern "C" int longnet_window_attn_bwd(const void* q, const void* k, const void* v, const void* out,
@@ -150,9 +153,10 @@ extern "C" int longnet_window_attn_bwd(const void* q, const void* k, const void*
   for (const void* p : {q, k, v, out, dout, (const void*)dq, (const void*)dk, (const void*)dv})
     if (!aligned(p, 16)) return LONGNET_ERR_MISALIGNED;
   if (!aligned(lse, 4) || !aligned(workspace, 256)) return LONGNET_ERR_MISALIGNED;
-  if (impl == LONGNET_IMPL_TCGEN05) return LONGNET_ERR_UNSUPPORTED;
   AttnArgs a;
   fill_window(&a, q, k, v, const_cast<void*>(out), const_cast<float*>(lse), B, N, H, Hkv, D, window, sinks, dtype);
+  const bool tc = window_bwd_tc_supports(a);
+  if (impl == LONGNET_IMPL_TCGEN05 && !tc) return LONGNET_ERR_UNSUPPORTED;
   int dev = 0;
   rc = device_state(&dev, &a.status);
   if (rc) return rc;
@@ -163,7 +167,8 @@ extern "C" int longnet_window_attn_bwd(const void* q, const void* k, const void*
   g.dv = dv;
   g.delta = static_cast<float*>(workspace);
   g.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + round256(4 * B * N * H));
-  return launch_window_bwd_simt(a, g, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return tc && impl != LONGNET_IMPL_SIMT ? launch_window_bwd_tc(a, g, st) : launch_window_bwd_simt(a, g, st);
 }
 
 extern "C" int longnet_paged_append(const void* k_tok, const void* v_tok, void* k_pages, void* v_pages,

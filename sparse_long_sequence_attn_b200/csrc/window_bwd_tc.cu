@@ -1,0 +1,568 @@
+// The backward of the sliding-window attention on the tensor cores (tcgen05),
+// bf16 and fp16, D = 16, 32, 64 or 128.
+//
+// Mathematics.  With P = e^{s - lse} and delta = <dout, out> (from the forward's
+// rounded out, as the call gets it), dS = P (dout V^T - delta):
+//   dV = P^T dout, dK = dS^T Q / sqrt(D), dQ = dS K / sqrt(D).
+// P and dS are computed in fp32 and rounded to the input format for their
+// products (the tensor cores take 16-bit operands); every sum is fp32 and each
+// gradient is rounded once, when it is written.
+//
+// Design.  Two kernels, so that no gradient row is summed by two CTAs and no
+// atomics are needed (the same bits every run), at the price of computing the
+// two score products twice (7 products instead of 5):
+//   key-centric    a CTA holds tiles of 128 keys (K, V) and streams 64-row
+//                  blocks of packed query rows (Q, dout, lse, delta):
+//                  S^T = K Q^T, dP^T = V dout^T, then dV += P^T dout and
+//                  dK += dS^T Q with P^T and dS^T read from TMEM.  The block's
+//                  rows are 64 / G tokens by the G query heads that share the
+//                  keys, so shared heads sum in the accumulators.
+//   query-centric  a CTA holds two tiles of 128 packed query rows (Q, dout) and
+//                  streams 64-key blocks (K, V): S, dP, then dQ += dS K.
+// Two score slots (S and dP, 64 columns each) in TMEM, each with a softmax
+// warpgroup of its own: the tensor cores fill one while the other's P and dS
+// are made.  Query-centric, and key-centric up to D = 64, a slot belongs to one
+// of two tiles that share every streamed block; key-centric at D = 128 the
+// accumulators of one tile fill the rest of TMEM, and the slots take
+// alternate blocks.
+// Warps 0-3 and 4-7 compute, warp 8 loads (TMA; its lanes fetch lse and
+// delta), warp 9 issues.  Every wait is bounded.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "attn_args.cuh"
+#include "tc_ptx.cuh"
+#include "window_tc.cuh"
+
+namespace longnet {
+namespace wb {
+using namespace wt;
+
+constexpr int kThreads = 320;
+constexpr int kTma = 8, kMma = 9;  // warps
+constexpr int kBlk = 64;           // streamed rows
+constexpr uint32_t kTmemCols = 512, kColAcc = 256;
+
+template <int kD, bool kKeys>
+struct B : Panels<kD> {
+  using P = Panels<kD>;
+  static constexpr int kTiles = kKeys && kD > 64 ? 1 : 2;
+  static constexpr int kTileBytes = kTile * kD * 2;
+  static constexpr int kBlkBytes = kBlk * kD * 2;
+  static constexpr int kStageBytes = 2 * kBlkBytes + (kKeys ? 1024 : 0);  // two blocks, then -lse and -delta
+  static constexpr int kStages = kD == 128 ? (kKeys ? 4 : 3) : 6;
+  static constexpr int kStage0 = kTiles * 2 * kTileBytes;
+  static constexpr int kBars = kStage0 + kStages * kStageBytes;
+  // one CTA per SM at every D: its TMEM columns are all of the SM's
+  static constexpr int kSmem = kBars + 512 + 1024 > 120 * 1024 ? kBars + 512 + 1024 : 120 * 1024;
+};
+
+struct __align__(64) BMaps {
+  CUtensorMap t[2], b[2];  // the tiles' two tensors, the blocks' two
+};
+
+struct BPlan {
+  int tokens;    // of a tile (query-centric) or of a block (key-centric)
+  FarPlan far;
+};
+
+// P and dS of 32 streamed rows for this thread's tile row, packed in pairs:
+// P = 2^(s scale log2(e) - lse log2(e)), dS = P (dP - delta); 0 where keep has
+// no bit.
+template <int kFmt, bool kKeys, bool kMask>
+__device__ __forceinline__ void p_ds_half(const uint32_t (&sr)[32], const uint32_t (&dr)[32], const float* nl_col,
+                                          const float* nd_col, uint64_t nl_row, uint64_t nd_row, uint64_t sc2,
+                                          uint32_t keep, uint32_t (&pk)[16], uint32_t (&dk)[16]) {
+#pragma unroll
+  for (int c = 0; c < 32; c += 4) {
+    uint64_t nl[2], nd[2];
+    if (kKeys) {
+      const float4 l4 = *reinterpret_cast<const float4*>(nl_col + c);
+      const float4 d4 = *reinterpret_cast<const float4*>(nd_col + c);
+      nl[0] = f32x2(l4.x, l4.y);
+      nl[1] = f32x2(l4.z, l4.w);
+      nd[0] = f32x2(d4.x, d4.y);
+      nd[1] = f32x2(d4.z, d4.w);
+    } else {
+      nl[0] = nl[1] = nl_row;
+      nd[0] = nd[1] = nd_row;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      float x0, x1;
+      f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[c + e]), __uint_as_float(sr[c + e + 1])), sc2, nl[e / 2]), x0,
+                  x1);
+      float p0 = ex2(x0), p1 = ex2(x1), d0, d1;
+      f32x2_split(mul_f32x2(f32x2(p0, p1),
+                            add_f32x2(f32x2(__uint_as_float(dr[c + e]), __uint_as_float(dr[c + e + 1])), nd[e / 2])),
+                  d0, d1);
+      if (kMask) {
+        const bool v0 = (keep >> (c + e)) & 1, v1 = (keep >> (c + e + 1)) & 1;
+        p0 = v0 ? p0 : 0.f;
+        p1 = v1 ? p1 : 0.f;
+        d0 = v0 ? d0 : 0.f;
+        d1 = v1 ? d1 : 0.f;
+      }
+      if (kKeys) pk[(c + e) / 2] = pack2<kFmt>(p0, p1);
+      dk[(c + e) / 2] = pack2<kFmt>(d0, d1);
+    }
+  }
+}
+
+template <int kFmt, int kD, bool kKeys>
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ WindowBwdArgs g,
+               const __grid_constant__ BMaps maps, const BPlan plan) {
+  using LL = B<kD, kKeys>;
+  constexpr int kTiles = LL::kTiles, kPanels = LL::kPanels, S = LL::kStages;
+  constexpr int kTilePanel = kTile * LL::kRowBytes, kBlkPanel = kBlk * LL::kRowBytes;
+  constexpr uint32_t kDescHi = LL::kDescHi;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int s = blockIdx.y / a.Hkv, f = blockIdx.y % a.Hkv;
+  const int N = a.nq_max, G = a.G, tok = plan.tokens;
+  // ---- the CTA's tiles and the streamed rows
+  int first;                // key-centric: first key; query-centric: first token
+  int i0 = 0, cnt = 0;      // key-centric: first streamed token; blocks
+  int i1 = 0;               // key-centric: end of the streamed tokens
+  int far = -1, ftile = 0;  // key-centric: far item and its tile, or -1 and the tile
+  BlockList bl = {0, 0, 0};
+  if (kKeys) {
+    const int tiles = (N + kTiles * kTile - 1) / (kTiles * kTile);
+    far = (int)blockIdx.x - plan.far.sink_tiles * plan.far.chunks;  // far items first: they are as long as any
+    if (far < 0) {
+      const int item = blockIdx.x;
+      ftile = item / plan.far.chunks;
+      far = item % plan.far.chunks;
+    } else {
+      ftile = far;
+      far = -1;
+    }
+    if (ftile >= tiles) return;
+    first = ftile * kTiles * kTile;
+    const int64_t reach = (int64_t)first + kTiles * kTile - 1 + a.window;
+    const int near = reach >= N || (first < a.sinks && ftile >= plan.far.sink_tiles) ? N : (int)reach;
+    i0 = first;
+    i1 = near;
+    if (far >= 0) {
+      i0 = near + far * plan.far.chunk;
+      i1 = i0 + plan.far.chunk < N ? i0 + plan.far.chunk : N;
+    }
+    cnt = i1 > i0 ? (i1 - i0 + tok - 1) / tok : 0;
+  } else {
+    first = ((int)gridDim.x - 1 - (int)blockIdx.x) * 2 * tok;  // the longest first
+    if (first >= N) return;
+    const int end = first + 2 * tok < N ? first + 2 * tok : N;
+    bl = blocks_of<kBlk>(a, first, end - 1);
+    cnt = bl.count;
+  }
+  auto active = [&](int st, int n) -> bool {
+    if (kTiles == 1) return (n & 1) == st;
+    if (kKeys) {
+      const int jt = first + st * kTile, b0 = i0 + n * tok;
+      const int b1 = b0 + tok < i1 ? b0 + tok : i1;
+      return jt < N && b1 > jt && (jt < a.sinks || b0 - a.window < jt + kTile - 1);
+    }
+    const int t0 = first + st * tok, t1 = t0 + tok < N ? t0 + tok : N, j0 = bl.at(n) * kBlk;
+    return t0 < t1 && j0 < t1 && (j0 < a.sinks || j0 + kBlk - 1 > t0 - a.window);
+  };
+
+  uint8_t* sStage = smem + LL::kStage0;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + LL::kBars);
+  uint64_t* bar_tile = bars;
+  uint64_t* bar_full = bars + 1;       // [S]
+  uint64_t* bar_empty = bars + 1 + S;  // [S]
+  uint64_t* bar_s = bars + 1 + 2 * S;  // [2] scores of a slot in TMEM
+  uint64_t* bar_p = bar_s + 2;         // [2] P and dS of a slot in TMEM
+  uint64_t* bar_acc = bar_s + 4;       // [2] accumulators done
+  uint64_t* bar_drain = bar_s + 6;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_s + 7);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(bar_tile, 1);
+    for (int i = 0; i < S; ++i) {
+      mbar_init(bar_full + i, 32);  // the loading warp's lanes, and the TMA bytes
+      mbar_init(bar_empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_s + i, 1);
+      mbar_init(bar_p + i, 128);
+      mbar_init(bar_acc + i, 1);
+    }
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (kKeys && tok * G < kBlk) {
+    // rows of a block that no token has: zeros, as the products read them
+    const int rows = kBlk - tok * G, chunks = LL::kRowBytes / 16;
+    for (int e = threadIdx.x; e < S * 2 * kPanels * rows * chunks; e += kThreads) {
+      const int c = e % chunks, r = (e / chunks) % rows, pn = e / chunks / rows;  // pn over stages, blocks, panels
+      const int stg = pn / (2 * kPanels);
+      *reinterpret_cast<uint4*>(sStage + stg * LL::kStageBytes + (pn % (2 * kPanels)) * kBlkPanel +
+                                (tok * G + r) * LL::kRowBytes + c * 16) = make_uint4(0, 0, 0, 0);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == kTma && lane < 4) prefetch_tmap(lane < 2 ? &maps.t[lane] : &maps.b[lane - 2]);
+  if (warp == kMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Waiter wt{abort_flag, a.status, kWaitLimitNs};
+  auto tile_ptr = [&](int st, int which) { return smem + (st * 2 + which) * LL::kTileBytes; };
+
+  if (warp == kTma) {
+    // ------------------------------------------------------------ loads
+    bool ok = true;
+    if (cnt > 0 && lane == 0) {
+      const int tiles = kTiles == 2 && first + (kKeys ? kTile : tok) < N ? 2 : 1;
+      mbar_arrive_expect_tx(bar_tile,
+                            (uint32_t)(tiles * 2 * (kKeys ? LL::kTileBytes : kPanels * tok * G * LL::kRowBytes)));
+      for (int st = 0; st < tiles; ++st)
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int pn = 0; pn < kPanels; ++pn)
+            tma_load_4d(tile_ptr(st, w) + pn * kTilePanel, &maps.t[w], bar_tile, LL::kPanelElems * pn,
+                        kKeys ? f : f * G, first + st * (kKeys ? kTile : tok), s);
+    }
+    int issued = 0;
+    for (int n = 0; n < cnt && ok; ++n) {
+      const int st = n % S;
+      if (n >= S) ok = wt.wait_warp(bar_empty + st, ((n / S) - 1) & 1);
+      if (!ok) break;
+      uint8_t* stage = sStage + st * LL::kStageBytes;
+      const int at = kKeys ? i0 + n * tok : bl.at(n) * kBlk;
+      if (lane == 0) {
+        mbar_expect_tx(bar_full + st,
+                       (uint32_t)(2 * (kKeys ? kPanels * tok * G * LL::kRowBytes : LL::kBlkBytes)));
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int pn = 0; pn < kPanels; ++pn)
+            tma_load_4d(stage + w * LL::kBlkBytes + pn * kBlkPanel, &maps.b[w], bar_full + st, LL::kPanelElems * pn,
+                        kKeys ? f * G : f, at, s);
+      }
+      if (kKeys) {
+        // -lse (log2 domain) and -delta of the block's rows; zero where there is none
+        float* sl = reinterpret_cast<float*>(stage + 2 * LL::kBlkBytes);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int c = lane + 32 * e, i = at + c / G;
+          const bool in = c < tok * G && i < N;
+          const int64_t idx = in ? ((int64_t)s * a.H + f * G + c % G) * N + i : 0;
+          sl[c] = in ? -a.lse[idx] * kLog2e : 0.f;
+          sl[kBlk + c] = in ? -g.delta[idx] : 0.f;
+        }
+      }
+      __syncwarp();  // the bytes are expected before the phase can complete
+      mbar_arrive(bar_full + st);
+      issued = n + 1;
+    }
+    // drain: every issued load has landed before the CTA may exit
+    if (lane == 0) {
+      if (cnt > 0 && !mbar_wait(bar_tile, 0, kWaitLimitNs)) record_status(a.status, kStatusTimeout);
+      for (int n = issued > S ? issued - S : 0; n < issued && ok; ++n)
+        if (!mbar_wait(bar_full + (n % S), (n / S) & 1, kWaitLimitNs)) {
+          record_status(a.status, kStatusTimeout);
+          break;
+        }
+    }
+  } else if (warp == kMma) {
+    // ------------------------------------------------------------ MMA issue
+    if (lane == 0 && cnt > 0) {
+      constexpr uint32_t kIdScore = idesc_f16kind(kTile, kBlk, false, kFmt);  // 128 x 64, B K-major
+      constexpr uint32_t kIdGrad = idesc_f16kind(kTile, kD, true, kFmt);      // 128 x D, B MN-major
+      constexpr uint32_t lbo_mn = ((uint32_t)kBlkPanel >> 4) << 16;           // panel stride along D
+      constexpr uint32_t kStep16 = 16 * LL::kRowBytes >> 4;                   // 16 rows of an MN-major operand
+      auto stage_lo = [&](int n) -> uint32_t { return smem_u32(sStage + (n % S) * LL::kStageBytes) >> 4; };
+      auto scores = [&](int st, int n) {
+        const uint32_t b_lo = stage_lo(n);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t t_lo = smem_u32(tile_ptr(kTiles == 2 ? st : 0, w)) >> 4;
+#pragma unroll
+          for (int pn = 0; pn < kPanels; ++pn)
+#pragma unroll
+            for (int kk = 0; kk < LL::kPanelElems / 16; ++kk)
+              mma_ss(tmem + 128 * st + 64 * w, desc_from(((t_lo + pn * (kTilePanel >> 4)) | (1u << 16)) + kk * 2, kDescHi),
+                     desc_from(((b_lo + w * (LL::kBlkBytes >> 4) + pn * (kBlkPanel >> 4)) | (1u << 16)) + kk * 2, kDescHi),
+                     kIdScore, (pn > 0 || kk > 0) ? 1u : 0u);
+        }
+        tc_commit(bar_s + st);
+      };
+      int pending[2] = {-1, -1}, done[2] = {0, 0}, left[2] = {0, 0};
+      for (int n = 0; n < cnt; ++n)
+        for (int st = 0; st < 2; ++st) left[st] += active(st, n) ? 1 : 0;
+      auto product = [&](int st) -> bool {
+        const int n = pending[st];
+        pending[st] = -1;
+        if (!wt.wait(bar_p + st, done[st] & 1)) return false;
+        tc_fence_after();
+        const uint32_t b0 = stage_lo(n), b1 = b0 + (LL::kBlkBytes >> 4);
+        const uint32_t acc = tmem + kColAcc + (kTiles == 2 ? (kKeys ? 2 : 1) * kD * st : 0);
+        const bool fresh = kTiles == 2 ? done[st] == 0 : n == 0;
+#pragma unroll
+        for (int kk = 0; kk < kBlk / 16; ++kk) {
+          const uint32_t add = fresh && kk == 0 ? 0u : 1u;
+          if (kKeys) {
+            // dV += P^T dout, dK += dS^T Q
+            mma_ts(acc, tmem + 128 * st + kk * 8, desc_from((b1 | lbo_mn) + kk * kStep16, kDescHi), kIdGrad, add);
+            mma_ts(acc + kD, tmem + 128 * st + 64 + kk * 8, desc_from((b0 | lbo_mn) + kk * kStep16, kDescHi), kIdGrad,
+                   add);
+          } else {
+            // dQ += dS K
+            mma_ts(acc, tmem + 128 * st + 64 + kk * 8, desc_from((b0 | lbo_mn) + kk * kStep16, kDescHi), kIdGrad, add);
+          }
+        }
+        if (++done[st] == left[st] && kTiles == 2) tc_commit(bar_acc + st);
+        return true;
+      };
+      bool ok = wt.wait(bar_tile, 0);
+      for (int n = 0; n <= cnt && ok; ++n) {
+        bool on[2] = {false, false}, due[2] = {pending[0] >= 0, pending[1] >= 0};
+        if (n < cnt) {
+          ok = wt.wait(bar_full + n % S, (n / S) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          on[0] = active(0, n);
+          on[1] = active(1, n);
+        }
+        // a slot with nothing due starts its scores before the other's P and
+        // dS are waited for
+        for (int st = 0; st < 2; ++st)
+          if (on[st] && !due[st]) {
+            scores(st, n);
+            pending[st] = n;
+          }
+        for (int st = 0; st < 2 && ok; ++st)
+          if (due[st]) {
+            ok = product(st);
+            if (ok && on[st]) {
+              scores(st, n);
+              pending[st] = n;
+            }
+          }
+        if (!ok) break;
+        if (n > 0) tc_commit(bar_empty + (n - 1) % S);
+      }
+      if (ok && kTiles == 1) {
+        tc_commit(bar_acc + 0);
+        tc_commit(bar_acc + 1);
+      }
+      // drain: all issued MMAs complete before TMEM is released
+      tc_commit(bar_drain);
+      if (!mbar_wait(bar_drain, 0, kWaitLimitNs)) record_status(a.status, kStatusTimeout);
+    }
+  } else {
+    // ------------------------------------------------------------ P, dS and the epilogue
+    const int st = warp >> 2;
+    const int row = 32 * (warp & 3) + lane;  // TMEM lane = tile row
+    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t slot = tmem + lane_base + 128 * st;
+    // key-centric: this thread's key; query-centric: its token and head
+    const int j = first + (kTiles == 2 ? st * kTile : 0) + row;
+    const int t0 = first + st * tok, i = t0 + row / G, h = f * G + row % G;
+    const bool row_ok = kKeys ? j < N : row < tok * G && i < N;
+    float lse2 = 0.f, delta = 0.f;
+    if (!kKeys && row_ok) {
+      const int64_t idx = ((int64_t)s * a.H + h) * N + i;
+      lse2 = a.lse[idx] * kLog2e;
+      delta = g.delta[idx];
+    }
+    const uint64_t sc2 = f32x2(a.scale_log2, a.scale_log2);
+    const uint64_t nl_row = f32x2(-lse2, -lse2), nd_row = f32x2(-delta, -delta);
+    int done = 0;
+    bool ok = true;
+    for (int n = 0; n < cnt && ok; ++n) {
+      if (!active(st, n)) continue;
+      const float* sl = reinterpret_cast<const float*>(sStage + (n % S) * LL::kStageBytes + 2 * LL::kBlkBytes);
+      // the columns [lo, hi) that pair with this row, and below sk
+      int lo, hi, sk;
+      if (kKeys) {
+        const int b0 = i0 + n * tok;
+        const int n_tok = i1 - b0 < tok ? i1 - b0 : tok;
+        const int from = j - b0, to = j + a.window - b0;  // tokens
+        lo = (from < 0 ? 0 : from > kBlk ? kBlk : from) * G;
+        hi = (j < a.sinks || to > n_tok ? n_tok : to < 0 ? 0 : to) * G;
+        sk = 0;
+      } else {
+        const int j0 = bl.at(n) * kBlk;
+        hi = row_ok ? i - j0 + 1 : 0;
+        lo = i - j0 - a.window + 1;
+        sk = a.sinks - j0;
+      }
+      if (kKeys) ok = wt.wait_warp(bar_full + n % S, (n / S) & 1);
+      if (ok) ok = wt.wait_warp(bar_s + st, done & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t keep0 = below(hi) & (~below(lo) | below(sk));
+      const uint32_t keep1 = below(hi - 32) & (~below(lo - 32) | below(sk - 32));
+      const bool whole = __all_sync(0xffffffffu, (keep0 & keep1) == 0xffffffffu);
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t sr[32], dr[32], pk[16], dk[16];
+        LN_TMEM_LD32(slot + 32 * hf, sr);
+        LN_TMEM_LD32(slot + 64 + 32 * hf, dr);
+        tmem_wait_ld();
+        if (whole)
+          p_ds_half<kFmt, kKeys, false>(sr, dr, sl + 32 * hf, sl + kBlk + 32 * hf, nl_row, nd_row, sc2, 0, pk, dk);
+        else
+          p_ds_half<kFmt, kKeys, true>(sr, dr, sl + 32 * hf, sl + kBlk + 32 * hf, nl_row, nd_row, sc2,
+                                       hf ? keep1 : keep0, pk, dk);
+        if (kKeys) LN_TMEM_ST16(slot + 16 * hf, pk);
+        LN_TMEM_ST16(slot + 64 + 16 * hf, dk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar_p + st);
+      ++done;
+    }
+    const bool any = kTiles == 2 ? done > 0 : cnt > 0;
+    if (ok && any) ok = wt.wait_warp(bar_acc + st, 0);
+    if (ok) {
+      tc_fence_after();
+      constexpr int kChunk = kD < 32 ? kD : 32;
+      const bool partial = kKeys && ftile < plan.far.sink_tiles;
+      // key-centric with two tiles: a warpgroup writes both gradients of its
+      // tile; with one tile, the first dV and the second dK
+#pragma unroll 1
+      for (int w = 0; w < (kKeys ? 2 : 1); ++w) {
+        if (kTiles == 1 && w != st) continue;
+        // w = 0: dV or dQ, w = 1: dK
+        const float sc = kKeys && w == 0 ? 1.f : a.scale;
+        const uint32_t acc = tmem + lane_base + kColAcc + (kTiles == 2 ? (kKeys ? 2 : 1) * kD * st : 0) + w * kD;
+        uint16_t* dst = kKeys ? static_cast<uint16_t*>(w == 0 ? g.dv : g.dk) + (((int64_t)s * N + j) * a.Hkv + f) * kD
+                              : static_cast<uint16_t*>(g.dq) + (((int64_t)s * N + i) * a.H + h) * kD;
+        const int slot_no = far < 0 ? 0 : 1 + far;
+        // [S Hkv][sink tile][slot][dK, dV][tile rows][D]
+        float* part = g.partial + ((((int64_t)blockIdx.y * plan.far.sink_tiles + ftile) * (plan.far.chunks + 1) + slot_no) * 2 +
+                                   (w == 0 ? 1 : 0)) * (int64_t)(kTiles * kTile * kD) +
+                      (int64_t)(j - first) * kD;
+#pragma unroll 1
+        for (int c0 = 0; c0 < kD; c0 += kChunk) {
+          uint32_t rr[kChunk];
+          if (any) {
+            tmem_load<kChunk>(acc + c0, rr);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int c = 0; c < kChunk; ++c) rr[c] = 0;
+          }
+          if (partial) {
+            float4* o = reinterpret_cast<float4*>(part + c0);
+#pragma unroll
+            for (int c = 0; c < kChunk; c += 4)
+              o[c / 4] = make_float4(__uint_as_float(rr[c]) * sc, __uint_as_float(rr[c + 1]) * sc,
+                                     __uint_as_float(rr[c + 2]) * sc, __uint_as_float(rr[c + 3]) * sc);
+          } else if (row_ok) {
+            uint4* o = reinterpret_cast<uint4*>(dst + c0);
+#pragma unroll
+            for (int c = 0; c < kChunk; c += 8) {
+              uint32_t v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                v[e] = pack2<kFmt>(__uint_as_float(rr[c + 2 * e]) * sc, __uint_as_float(rr[c + 2 * e + 1]) * sc);
+              o[c / 8] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+// Query rows [B, N, H, D] as (d, h, token, batch): a box is one panel of G
+// heads by `tokens` tokens.
+bool encode_rows(EncodeTiledFn enc, CUtensorMap* map, const void* base, const AttnArgs& a, int tokens) {
+  const cuuint64_t row = (cuuint64_t)a.D * 2;
+  cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.H, (cuuint64_t)a.nq_max, (cuuint64_t)a.S};
+  cuuint64_t strides[3] = {row, row * a.H, row * a.H * a.nq_max};
+  const int pe = a.D >= 64 ? 64 : a.D;
+  cuuint32_t box[4] = {(cuuint32_t)pe, (cuuint32_t)a.G, (cuuint32_t)tokens, 1};
+  cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc(map, a.dtype == LONGNET_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+             const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             pe == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+             : pe == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                        : CU_TENSOR_MAP_SWIZZLE_32B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kFmt, int kD>
+int launch_typed(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream) {
+  EncodeTiledFn enc = get_encoder();
+  if (!enc) return LONGNET_ERR_CUDA;
+  BPlan pk, pq;
+  pk.tokens = kBlk / a.G;
+  pq.tokens = kTile / a.G;
+  using LK = B<kD, true>;
+  using LQ = B<kD, false>;
+  pk.far = pq.far = far_plan(a.S, a.nq_max, a.H, a.Hkv, a.window, a.sinks, LK::kTiles * kTile);
+  BMaps mk, mq;
+  if (!encode_kv(enc, &mk.t[0], a.k, a, kTile) || !encode_kv(enc, &mk.t[1], a.v, a, kTile) ||
+      !encode_rows(enc, &mk.b[0], a.q, a, pk.tokens) || !encode_rows(enc, &mk.b[1], g.dout, a, pk.tokens) ||
+      !encode_rows(enc, &mq.t[0], a.q, a, pq.tokens) || !encode_rows(enc, &mq.t[1], g.dout, a, pq.tokens) ||
+      !encode_kv(enc, &mq.b[0], a.k, a, kBlk) || !encode_kv(enc, &mq.b[1], a.v, a, kBlk))
+    return LONGNET_ERR_CUDA;
+  auto fk = bwd_kernel<kFmt, kD, true>;
+  auto fq = bwd_kernel<kFmt, kD, false>;
+  if (cudaFuncSetAttribute(fk, cudaFuncAttributeMaxDynamicSharedMemorySize, LK::kSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(fq, cudaFuncAttributeMaxDynamicSharedMemorySize, LQ::kSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return LONGNET_ERR_CUDA;
+  }
+  int rc = launch_window_delta(a, g, stream);
+  if (rc) return rc;
+  const int64_t items = ((int64_t)a.nq_max + LK::kTiles * kTile - 1) / (LK::kTiles * kTile) +
+                        (int64_t)pk.far.sink_tiles * pk.far.chunks;
+  fk<<<dim3((unsigned)items, (unsigned)(a.S * a.Hkv)), kThreads, LK::kSmem, stream>>>(a, g, mk, pk);
+  if (cudaGetLastError() != cudaSuccess) return LONGNET_ERR_CUDA;
+  const int64_t pairs = ((int64_t)a.nq_max + 2 * pq.tokens - 1) / (2 * pq.tokens);
+  fq<<<dim3((unsigned)pairs, (unsigned)(a.S * a.Hkv)), kThreads, LQ::kSmem, stream>>>(a, g, mq, pq);
+  if (cudaGetLastError() != cudaSuccess) return LONGNET_ERR_CUDA;
+  return launch_far_reduce(a, g, pk.far, stream);
+}
+
+}  // namespace wb
+
+// Shared groups of up to 64 heads: a token's rows fit one streamed block.
+bool window_bwd_tc_supports(const AttnArgs& a) {
+  return (a.dtype == LONGNET_DTYPE_BF16 || a.dtype == LONGNET_DTYPE_F16) && a.G <= wb::kBlk;
+}
+int window_bwd_tc_tile(int64_t D) { return (D > 64 ? 1 : 2) * wt::kTile; }
+
+int launch_window_bwd_tc(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream) {
+  const bool f16 = a.dtype == LONGNET_DTYPE_F16;
+  switch (a.D) {
+    case 16:
+      return f16 ? wb::launch_typed<tc::kFmtF16, 16>(a, g, stream) : wb::launch_typed<tc::kFmtBF16, 16>(a, g, stream);
+    case 32:
+      return f16 ? wb::launch_typed<tc::kFmtF16, 32>(a, g, stream) : wb::launch_typed<tc::kFmtBF16, 32>(a, g, stream);
+    case 64:
+      return f16 ? wb::launch_typed<tc::kFmtF16, 64>(a, g, stream) : wb::launch_typed<tc::kFmtBF16, 64>(a, g, stream);
+    default:
+      return f16 ? wb::launch_typed<tc::kFmtF16, 128>(a, g, stream) : wb::launch_typed<tc::kFmtBF16, 128>(a, g, stream);
+  }
+}
+
+}  // namespace longnet

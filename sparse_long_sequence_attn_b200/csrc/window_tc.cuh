@@ -26,6 +26,9 @@ bool window_tc_supports(const AttnArgs& a);
 WindowTcPlan window_tc_plan(const AttnArgs& a);
 int64_t window_tc_part_floats(const AttnArgs& a, const WindowTcPlan& p);
 int launch_window_fwd_tc(const AttnArgs& a, float* parts, cudaStream_t stream);
+bool window_bwd_tc_supports(const AttnArgs& a);
+int window_bwd_tc_tile(int64_t D);  // keys of a work item of the key-centric kernel
+int launch_window_bwd_tc(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream);
 int launch_combine(const AttnArgs& a, const float* part_out, const float* part_lse, int parts, cudaStream_t stream);
 
 namespace wt {
@@ -67,6 +70,11 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
+}
+
+// Adds bytes to the barrier's current phase without arriving.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
 struct Waiter {
