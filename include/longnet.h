@@ -515,8 +515,8 @@ int longnet_paged_append(const void* k_tok, const void* v_tok, void* k_pages, vo
  *     received weight is added: weights[s, f, j] += sum of P_xj over the new
  *     tokens x of sequence s and the query heads of key/value head f.
  *     Needs lse.
- *   - impl: LONGNET_IMPL_AUTO, LONGNET_IMPL_DECODE (bf16 and fp16, at most 64
- *     query rows, max_q H / Hkv, per key/value head), LONGNET_IMPL_TCGEN05
+ *   - impl: LONGNET_IMPL_AUTO, LONGNET_IMPL_DECODE (bf16 and fp16, at most 16
+ *     query rows, max_q H / Hkv, per key/value head and 2048 sequences), LONGNET_IMPL_TCGEN05
  *     (bf16 and fp16, H / Hkv <= 128) or LONGNET_IMPL_SIMT (fp32 arithmetic,
  *     every dtype).
  *   - workspace: device memory of the caller, 256-byte aligned, at least

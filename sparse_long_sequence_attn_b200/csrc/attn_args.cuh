@@ -63,7 +63,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int s) {
   r.kv = kv;
   r.first = kv - r.nq;
   if (c0 < 0 || c1 < c0 || c1 > a.T || c1 - c0 > a.nq_max || kv < 0 || kv > (int64_t)a.max_pages << a.page_shift) {
-    if (threadIdx.x == 0) record_status(a.status, kStatusBounds);
+    record_status(a.status, kStatusBounds);
     r.q0 = 0;
     r.nq = r.first = r.kv = 0;
   }

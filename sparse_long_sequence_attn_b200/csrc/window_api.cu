@@ -8,6 +8,7 @@
 #include <string.h>
 
 #include "attn_args.cuh"
+#include "decode.cuh"
 #include "longnet.h"
 #include "params.h"
 #include "window_tc.cuh"
@@ -222,9 +223,11 @@ void fill_paged(AttnArgs* a, int64_t S, int64_t max_q, int64_t H, int64_t Hkv, i
 
 // The workspace of a paged call: the parts of the family that needs most, so
 // that it does not depend on the family.
-int64_t paged_workspace(const AttnArgs& a) {
+int64_t paged_workspace(const AttnArgs& a, bool weights) {
   if (!window_tc_supports(a)) return 0;
-  return round256(4 * window_tc_part_floats(a, window_tc_plan(a)));
+  const int64_t tc = window_tc_part_floats(a, window_tc_plan(a));
+  const int64_t dec = decode_supports(a) ? decode_workspace_floats(a, weights) : 0;
+  return round256(4 * (tc > dec ? tc : dec));
 }
 }  // namespace
 }  // namespace longnet
@@ -237,7 +240,7 @@ extern "C" int64_t longnet_paged_workspace_bytes(int64_t S, int64_t max_q, int64
   if (weights != 0 && weights != 1) return LONGNET_ERR_INVALID_ARG;
   AttnArgs a;
   fill_paged(&a, S, max_q, H, Hkv, D, page, max_pages, window, sinks, dtype);
-  return paged_workspace(a);
+  return paged_workspace(a, weights != 0);
 }
 
 extern "C" int longnet_paged_attn_fwd(const void* q, const void* k_pages, const void* v_pages, void* out, float* lse,
@@ -270,13 +273,15 @@ extern "C" int longnet_paged_attn_fwd(const void* q, const void* k_pages, const 
   a.q = q;
   a.out = out;
   a.lse = lse;
-  const bool tc = window_tc_supports(a);
-  if (impl == LONGNET_IMPL_DECODE || (impl == LONGNET_IMPL_TCGEN05 && !tc)) return LONGNET_ERR_UNSUPPORTED;
+  const bool tc = window_tc_supports(a), dec = decode_supports(a);
+  if ((impl == LONGNET_IMPL_DECODE && !dec) || (impl == LONGNET_IMPL_TCGEN05 && !tc)) return LONGNET_ERR_UNSUPPORTED;
   int dev = 0;
   rc = device_state(&dev, &a.status);
   if (rc) return rc;
   if (T == 0) return LONGNET_OK;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (dec && (impl == LONGNET_IMPL_AUTO || impl == LONGNET_IMPL_DECODE))
+    return launch_decode(a, static_cast<float*>(workspace), weights, st);
   rc = tc && impl != LONGNET_IMPL_SIMT ? launch_window_fwd_tc(a, static_cast<float*>(workspace), st)
                                        : launch_window_fwd_simt(a, st);
   if (rc || !weights) return rc;

@@ -56,11 +56,13 @@ def attend(cache, q, cu, max_q, window, sinks, impl, weights=None):
 
 
 def families(dtype):
-    return [AUTO] if dtype == F32 else [AUTO, SIMT]
+    return [AUTO] if dtype == F32 else [AUTO, SIMT, bd.LONGNET_IMPL_TCGEN05, bd.LONGNET_IMPL_DECODE]
 
 
-def refused(impl, case, dtype):
-    return False
+def refused(impl, case, dtype, more=0):
+    """The few-token family takes at most 16 query rows per key/value head."""
+    seqs, H, Hkv = CASES[case][:3]
+    return impl == bd.LONGNET_IMPL_DECODE and (max(n for n, _ in seqs) + more) * (H // Hkv) > 16
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
@@ -73,6 +75,10 @@ def test_attention_and_weights(case, dtype):
         if refused(impl, case, dtype):
             continue
         for max_q in (max(nq), max(nq) + 3):
+            if refused(impl, case, dtype, max_q - max(nq)):
+                with pytest.raises(bd.LongNetError):
+                    attend(cache, q, cu, max_q, window, sinks, impl)
+                continue
             got, got_lse = attend(cache, q, cu, max_q, window, sinks, impl)
             assert bd.longnet_last_device_status() == 0
             within(f"out {impl}", got[:n], out[:n], b_out[:n])
