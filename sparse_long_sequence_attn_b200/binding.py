@@ -497,18 +497,30 @@ def dilated_attention(q, k, v, patterns, causal: bool = True, qk_norm: bool = Fa
     return DilatedAttnFunction.apply(q, k, v, patterns, causal, qk_norm, xpos)
 
 
-def _on_device(t: torch.Tensor, stream):
-    """t's device made current, and the stream's handle (default: torch's current stream there)."""
-    return torch.cuda.device(t.device), _stream_handle(torch.cuda.current_stream(t.device) if stream is None
-                                                       else stream)
+def _call(name: str, t: torch.Tensor, stream, *args) -> None:
+    """Call the library with t's device current; the stream (default: torch's
+    current stream there) is the last argument.  Raises LongNetError on a
+    non-zero status."""
+    at = t.get_device()
+    handle = (torch.cuda.current_stream(at) if stream is None else stream).cuda_stream or None
+    fn = getattr(load_library(), name)
+    if at == torch.cuda.current_device():
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(at):
+            rc = fn(*args, handle)
+    if rc != LONGNET_OK:
+        raise LongNetError(rc, name)
 
 
-def _check(what: str, t: torch.Tensor, shape, dtype, like: torch.Tensor) -> None:
-    """One tensor argument: CUDA, on `like`'s device, contiguous, of this shape and dtype."""
-    if not (t.is_cuda and t.device == like.device and t.is_contiguous() and t.dtype == dtype
-            and tuple(t.shape) == tuple(shape)):
-        raise ValueError(f"{what} must be a contiguous {dtype} CUDA tensor {tuple(shape)} on {like.device}, "
-                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+def _check(like: torch.Tensor, *wanted) -> None:
+    """Tensor arguments, as (name, tensor, shape, dtype): each CUDA, on
+    `like`'s device, contiguous, of this shape and dtype."""
+    at = like.get_device()
+    for what, t, shape, dtype in wanted:
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != at or at < 0 or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous {dtype} CUDA tensor {tuple(shape)} on {like.device}, "
+                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def longnet_window_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
@@ -521,19 +533,14 @@ def longnet_window_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o
     one dtype (fp32/bf16/fp16); lse: contiguous fp32 [B, H, N] or None.  Raises
     LongNetError on a non-zero status."""
     B, N, H, D = q.shape
-    _check("q", q, (B, N, H, D), q.dtype, q)
-    _check("k", k, (B, N, k.shape[2], D), q.dtype, q)
-    _check("v", v, k.shape, q.dtype, q)
-    _check("out", out, q.shape, q.dtype, q)
+    Hkv, dt = k.shape[2], q.dtype
+    _check(q, ("q", q, (B, N, H, D), dt), ("k", k, (B, N, Hkv, D), dt), ("v", v, (B, N, Hkv, D), dt),
+           ("out", out, (B, N, H, D), dt))
     if lse is not None:
-        _check("lse", lse, (B, H, N), torch.float32, q)
-    dev, handle = _on_device(q, stream)
-    with dev:
-        rc = load_library().longnet_window_attn_fwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-            B, N, H, k.shape[2], D, int(window), int(sinks), _dtype_code(q), int(impl), handle)
-    if rc != LONGNET_OK:
-        raise LongNetError(rc, "longnet_window_attn_fwd")
+        _check(q, ("lse", lse, (B, H, N), torch.float32))
+    _call("longnet_window_attn_fwd", q, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+          None if lse is None else lse.data_ptr(), B, N, H, Hkv, D, int(window), int(sinks), _dtype_code(q),
+          int(impl))
 
 
 def longnet_window_bwd_workspace_bytes(B: int, N: int, H: int, Hkv: int, D: int, window: int, sinks: int,
@@ -556,23 +563,15 @@ def longnet_window_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o
     longnet_window_bwd_workspace_bytes bytes, 256-byte aligned.  Raises
     LongNetError on a non-zero status."""
     B, N, H, D = q.shape
-    _check("q", q, (B, N, H, D), q.dtype, q)
-    _check("k", k, (B, N, k.shape[2], D), q.dtype, q)
-    _check("v", v, k.shape, q.dtype, q)
-    for name, t in (("out", out), ("dout", dout), ("dq", dq)):
-        _check(name, t, q.shape, q.dtype, q)
-    for name, t in (("dk", dk), ("dv", dv)):
-        _check(name, t, k.shape, q.dtype, q)
-    _check("lse", lse, (B, H, N), torch.float32, q)
-    _check("workspace", workspace, workspace.shape, workspace.dtype, q)
-    dev, handle = _on_device(q, stream)
-    with dev:
-        rc = load_library().longnet_window_attn_bwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
-            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, N, H, k.shape[2], D, int(window), int(sinks),
-            _dtype_code(q), int(impl), workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
-    if rc != LONGNET_OK:
-        raise LongNetError(rc, "longnet_window_attn_bwd")
+    Hkv, dt = k.shape[2], q.dtype
+    rows, kv = (B, N, H, D), (B, N, Hkv, D)
+    _check(q, ("q", q, rows, dt), ("k", k, kv, dt), ("v", v, kv, dt), ("out", out, rows, dt),
+           ("dout", dout, rows, dt), ("dq", dq, rows, dt), ("dk", dk, kv, dt), ("dv", dv, kv, dt),
+           ("lse", lse, (B, H, N), torch.float32), ("workspace", workspace, workspace.shape, workspace.dtype))
+    _call("longnet_window_attn_bwd", q, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+          lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, N, H, Hkv, D,
+          int(window), int(sinks), _dtype_code(q), int(impl), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
 
 
 def window_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, sinks: int = 0,
@@ -640,24 +639,16 @@ def paged_append(k_tok: torch.Tensor, v_tok: torch.Tensor, k_pages: torch.Tensor
     there.  Lengths and page numbers are checked on the device (status word).
     Raises LongNetError on a non-zero status."""
     n_pages, page, Hkv, D, S, max_pages = _cache_sizes(k_pages, table)
-    T = k_tok.shape[0]
-    _check("k_pages", k_pages, k_pages.shape, k_tok.dtype, k_tok)
-    _check("v_pages", v_pages, k_pages.shape, k_tok.dtype, k_tok)
-    _check("k_tok", k_tok, (T, Hkv, D), k_tok.dtype, k_tok)
-    _check("v_tok", v_tok, (T, Hkv, D), k_tok.dtype, k_tok)
-    _check("cu_q", cu_q, (S + 1,), torch.int32, k_tok)
-    _check("kv_len", kv_len, (S,), torch.int32, k_tok)
-    _check("table", table, (S, max_pages), torch.int32, k_tok)
+    T, dt = k_tok.shape[0], k_tok.dtype
+    _check(k_tok, ("k_tok", k_tok, (T, Hkv, D), dt), ("v_tok", v_tok, (T, Hkv, D), dt),
+           ("k_pages", k_pages, k_pages.shape, dt), ("v_pages", v_pages, k_pages.shape, dt),
+           ("cu_q", cu_q, (S + 1,), torch.int32), ("kv_len", kv_len, (S,), torch.int32),
+           ("table", table, table.shape, torch.int32))
     if weights is not None:
-        _check("weights", weights, (S, Hkv, max_pages * page), torch.float32, k_tok)
-    dev, handle = _on_device(k_tok, stream)
-    with dev:
-        rc = load_library().longnet_paged_append(
-            k_tok.data_ptr(), v_tok.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-            None if weights is None else weights.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), table.data_ptr(),
-            T, S, Hkv, D, n_pages, page, max_pages, _dtype_code(k_tok), handle)
-    if rc != LONGNET_OK:
-        raise LongNetError(rc, "longnet_paged_append")
+        _check(k_tok, ("weights", weights, (S, Hkv, max_pages * page), torch.float32))
+    _call("longnet_paged_append", k_tok, stream, k_tok.data_ptr(), v_tok.data_ptr(), k_pages.data_ptr(),
+          v_pages.data_ptr(), None if weights is None else weights.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
+          table.data_ptr(), T, S, Hkv, D, n_pages, page, max_pages, _dtype_code(k_tok))
 
 
 def longnet_paged_workspace_bytes(S: int, max_q: int, H: int, Hkv: int, D: int, page: int, max_pages: int,
@@ -693,31 +684,22 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, cu
     of no sequence are left as they were.  Returns (out, lse).  Raises
     LongNetError on a non-zero status."""
     n_pages, page, Hkv, D, S, max_pages = _cache_sizes(k_pages, table)
-    T, H = q.shape[0], q.shape[1]
+    T, H, dt = q.shape[0], q.shape[1], q.dtype
     out = torch.empty_like(q) if out is None else out
     lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if lse is None else lse
-    _check("q", q, (T, H, D), q.dtype, q)
-    _check("k_pages", k_pages, k_pages.shape, q.dtype, q)
-    _check("v_pages", v_pages, k_pages.shape, q.dtype, q)
-    _check("out", out, q.shape, q.dtype, q)
-    _check("lse", lse, (T, H), torch.float32, q)
-    _check("cu_q", cu_q, (S + 1,), torch.int32, q)
-    _check("kv_len", kv_len, (S,), torch.int32, q)
-    _check("table", table, (S, max_pages), torch.int32, q)
+    _check(q, ("q", q, (T, H, D), dt), ("k_pages", k_pages, k_pages.shape, dt),
+           ("v_pages", v_pages, k_pages.shape, dt), ("out", out, (T, H, D), dt), ("lse", lse, (T, H), torch.float32),
+           ("cu_q", cu_q, (S + 1,), torch.int32), ("kv_len", kv_len, (S,), torch.int32),
+           ("table", table, table.shape, torch.int32))
     if weights is not None:
-        _check("weights", weights, (S, Hkv, max_pages * page), torch.float32, q)
+        _check(q, ("weights", weights, (S, Hkv, max_pages * page), torch.float32))
     if workspace is None:
         workspace = paged_workspace(q, k_pages, table, max_q, window, sinks, weights is not None)
-    _check("workspace", workspace, workspace.shape, workspace.dtype, q)
-    dev, handle = _on_device(q, stream)
-    with dev:
-        rc = load_library().longnet_paged_attn_fwd(
-            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(),
-            None if weights is None else weights.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), table.data_ptr(),
-            T, S, int(max_q), H, Hkv, D, n_pages, page, max_pages, int(window), int(sinks), _dtype_code(q),
-            int(impl), workspace.data_ptr() or None, workspace.numel() * workspace.element_size(), handle)
-    if rc != LONGNET_OK:
-        raise LongNetError(rc, "longnet_paged_attn_fwd")
+    _check(q, ("workspace", workspace, workspace.shape, workspace.dtype))
+    _call("longnet_paged_attn_fwd", q, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
+          lse.data_ptr(), None if weights is None else weights.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
+          table.data_ptr(), T, S, int(max_q), H, Hkv, D, n_pages, page, max_pages, int(window), int(sinks),
+          _dtype_code(q), int(impl), workspace.data_ptr() or None, workspace.numel() * workspace.element_size())
     return out, lse
 
 
@@ -735,26 +717,18 @@ def cache_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, weights: torch.Ten
     status."""
     n_pages, page, Hkv, D, S, max_pages = _cache_sizes(k_pages, table)
     n_out, _, _, _, _, max_out = _cache_sizes(k_out, new_table)
-    _check("k_pages", k_pages, k_pages.shape, k_pages.dtype, k_pages)
-    _check("v_pages", v_pages, k_pages.shape, k_pages.dtype, k_pages)
-    _check("k_out", k_out, (n_out, page, Hkv, D), k_pages.dtype, k_pages)
-    _check("v_out", v_out, (n_out, page, Hkv, D), k_pages.dtype, k_pages)
-    _check("weights", weights, (S, Hkv, max_pages * page), torch.float32, k_pages)
-    _check("kv_len", kv_len, (S,), torch.int32, k_pages)
-    _check("table", table, (S, max_pages), torch.int32, k_pages)
-    _check("new_table", new_table, (S, max_out), torch.int32, k_pages)
-    kept = torch.empty((S, Hkv, max(int(budget), 0)), dtype=torch.int32, device=k_pages.device)
-    new_len = torch.empty((S,), dtype=torch.int32, device=k_pages.device)
-    new_weights = torch.empty((S, Hkv, max_out * page), dtype=torch.float32, device=k_pages.device)
-    dev, handle = _on_device(k_pages, stream)
-    with dev:
-        rc = load_library().longnet_cache_evict(
-            k_pages.data_ptr(), v_pages.data_ptr(), weights.data_ptr(), kv_len.data_ptr(), table.data_ptr(),
-            k_out.data_ptr(), v_out.data_ptr(), new_weights.data_ptr(), new_len.data_ptr(), kept.data_ptr(),
-            new_table.data_ptr(), S, Hkv, D, n_pages, page, max_pages, n_out, max_out, int(budget), int(sinks),
-            int(recent), _dtype_code(k_pages), handle)
-    if rc != LONGNET_OK:
-        raise LongNetError(rc, "longnet_cache_evict")
+    dt, at = k_pages.dtype, k_pages.device
+    _check(k_pages, ("k_pages", k_pages, k_pages.shape, dt), ("v_pages", v_pages, k_pages.shape, dt),
+           ("k_out", k_out, (n_out, page, Hkv, D), dt), ("v_out", v_out, (n_out, page, Hkv, D), dt),
+           ("weights", weights, (S, Hkv, max_pages * page), torch.float32), ("kv_len", kv_len, (S,), torch.int32),
+           ("table", table, table.shape, torch.int32), ("new_table", new_table, (S, max_out), torch.int32))
+    kept = torch.empty((S, Hkv, max(int(budget), 0)), dtype=torch.int32, device=at)
+    new_len = torch.empty((S,), dtype=torch.int32, device=at)
+    new_weights = torch.empty((S, Hkv, max_out * page), dtype=torch.float32, device=at)
+    _call("longnet_cache_evict", k_pages, stream, k_pages.data_ptr(), v_pages.data_ptr(), weights.data_ptr(),
+          kv_len.data_ptr(), table.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), new_weights.data_ptr(),
+          new_len.data_ptr(), kept.data_ptr(), new_table.data_ptr(), S, Hkv, D, n_pages, page, max_pages, n_out,
+          max_out, int(budget), int(sinks), int(recent), _dtype_code(k_pages))
     return kept, new_len, new_weights
 
 

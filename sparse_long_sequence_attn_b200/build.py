@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblongnet.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["api.cu", "simt.cu", "tcgen05.cu", "smallseg.cu", "backward.cu", "bwd_tcgen05.cu", "exchange.cu", "prologue.cu", "perpattern.cu",
-           "window_api.cu", "window_simt.cu", "window_tc.cu", "decode.cu", "window_bwd_tc.cu", "paged.cu", "evict.cu"]
+           "window_api.cu", "window_simt.cu", "window_tc.cu", "weights_tc.cu", "decode.cu", "window_bwd_tc.cu", "paged.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

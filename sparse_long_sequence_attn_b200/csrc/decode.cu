@@ -410,9 +410,9 @@ __device__ __forceinline__ Pieces pieces_of(const Args& A, int s, int f, int blo
   Pieces p = {0, 0};
   if (blocks == 0) return p;
   const int run = A.plan[A.a.S + 1];
-  const int64_t w = (int64_t)A.plan[s] * A.a.Hkv + (int64_t)f * blocks;
-  const int64_t c0 = w / run, c1 = (w + blocks - 1) / run;
-  p.first = c0 + s * A.a.Hkv + f;
+  const uint32_t w = (uint32_t)(A.plan[s] * A.a.Hkv + f * blocks);  // fewer than 2^30 blocks in all
+  const uint32_t c0 = w / (uint32_t)run, c1 = (w + blocks - 1) / (uint32_t)run;
+  p.first = (int64_t)c0 + s * A.a.Hkv + f;
   p.count = (int)(c1 - c0) + 1;
   return p;
 }
@@ -420,39 +420,83 @@ __device__ __forceinline__ Pieces pieces_of(const Args& A, int s, int f, int blo
 constexpr int kJoinThreads = 256;
 constexpr int kKeysPerBlock = 1024;
 
-// Blocks [0, row_blocks): a warp per (pair, row) joins the row's pieces.  The
-// others: the weights of kKeysPerBlock keys of a pair.
-template <int kFmt, int kD>
+// Blocks [0, row_blocks): kSplit warps per (pair, row) join the row's pieces,
+// each an equal run of them, then the runs in order.  The others: the weights
+// of kKeysPerBlock keys of a pair.
+template <int kFmt, int kD, int kSplit>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args A, int row_blocks) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const AttnArgs& a = A.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if ((int)blockIdx.x < row_blocks) {
-    const int64_t id = (int64_t)blockIdx.x * (kJoinThreads / 32) + warp;
+    constexpr int kWarpsPerBlock = kJoinThreads / 32;
+    constexpr int kE = kD / 32 > 0 ? kD / 32 : 1;  // values of a lane
+    __shared__ float s_acc[kSplit > 1 ? kWarpsPerBlock : 1][kSplit > 1 ? kD : 1], s_sum[kWarpsPerBlock];
+    const int64_t id = (int64_t)blockIdx.x * (kWarpsPerBlock / kSplit) + warp / kSplit;
     const int64_t pair = id / A.rows;
-    if (pair >= (int64_t)a.S * a.Hkv) return;
     const int r = (int)(id % A.rows), s = (int)(pair / a.Hkv), f = (int)(pair % a.Hkv);
-    const Seq q = seq_of(a, s);
-    if (r >= q.nq * a.G) return;
-    const Pieces p = pieces_of(A, s, f, A.plan[s + 1] - A.plan[s]);
-    if (p.count == 1) return;  // written by its CTA
-    float m = -INFINITY;
-    for (int c = lane; c < p.count; c += 32) m = fmaxf(m, A.part_lse[(p.first + c) * A.rows + r]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float base = m == -INFINITY ? 0.f : m;
-    constexpr int kE = kD / 32 > 0 ? kD / 32 : 1;
+    Seq q = {0, 0, 0, 0};
+    Pieces p = {0, 1};
+    if (pair < (int64_t)a.S * a.Hkv) {
+      q = seq_of(a, s);
+      if (r < q.nq * a.G) p = pieces_of(A, s, f, A.plan[s + 1] - A.plan[s]);
+    }
+    const bool mine = p.count != 1;  // one piece was written by its CTA; none: zeros
     const bool on = lane * kE < kD;
-    float acc[kE] = {}, sum = 0.f;
-    for (int c = 0; c < p.count; ++c) {
-      const float wgt = ex2(A.part_lse[(p.first + c) * A.rows + r] - base);
-      sum += wgt;
-      if (on && wgt > 0.f) {
-        const float* src = A.part_out + ((p.first + c) * A.rows + r) * kD + lane * kE;
+    float m = -INFINITY, acc[kE] = {}, sum = 0.f;
+    if (mine) {
+      for (int c = lane; c < p.count; c += 32) m = fmaxf(m, A.part_lse[(p.first + c) * A.rows + r]);
 #pragma unroll
-        for (int e = 0; e < kE; ++e) acc[e] = fmaf(wgt, src[e], acc[e]);
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float base = m == -INFINITY ? 0.f : m;
+      const int per = (p.count + kSplit - 1) / kSplit;
+      const int b0 = (warp % kSplit) * per, b1 = b0 + per < p.count ? b0 + per : p.count;
+      // 32 pieces at a time: a lane weighs one, then all lanes add them in
+      // order (independent loads, so their latencies overlap)
+      for (int c0 = b0; c0 < b1; c0 += 32) {
+        const float wl = c0 + lane < b1 ? ex2(A.part_lse[(p.first + c0 + lane) * A.rows + r] - base) : 0.f;
+        const int n = b1 - c0 < 32 ? b1 - c0 : 32;
+#pragma unroll 8
+        for (int c = 0; c < n; ++c) {
+          const float wgt = __shfl_sync(0xffffffffu, wl, c);
+          sum += wgt;
+          if (on) {
+            const float* src = A.part_out + ((p.first + c0 + c) * A.rows + r) * kD + lane * kE;
+            float t[kE];
+            if constexpr (kE == 4) {
+              const float4 v = *reinterpret_cast<const float4*>(src);
+              t[0] = v.x;
+              t[1] = v.y;
+              t[2] = v.z;
+              t[3] = v.w;
+            } else {
+#pragma unroll
+              for (int e = 0; e < kE; ++e) t[e] = src[e];
+            }
+#pragma unroll
+            for (int e = 0; e < kE; ++e) acc[e] = fmaf(wgt, t[e], acc[e]);
+          }
+        }
       }
     }
+    if (kSplit > 1) {
+      if (on) {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) s_acc[warp][lane * kE + e] = acc[e];
+      }
+      if (lane == 0) s_sum[warp] = sum;
+      __syncthreads();
+      if (warp % kSplit != 0) return;
+#pragma unroll
+      for (int v = 1; v < kSplit; ++v) {
+        sum += s_sum[warp + v];
+        if (on) {
+#pragma unroll
+          for (int e = 0; e < kE; ++e) acc[e] += s_acc[warp + v][lane * kE + e];
+        }
+      }
+    }
+    if (!mine) return;
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     const int i = r / a.G, h = f * a.G + r % a.G;
     if (on) {
@@ -501,6 +545,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int j = j0 + 4 * (int)threadIdx.x;  // keys is a multiple of 8, j of 4
   if (j >= q.kv) return;
   float acc[4] = {};
+#pragma unroll 4
   for (int r = 0; r < rows; ++r) {
     const int x = q.first + r / a.G;
     if (x < 0) continue;
@@ -593,10 +638,15 @@ int launch_typed(const AttnArgs& a, float* workspace, float* weights, cudaStream
   int rc = launch_after(fn, dim3((unsigned)ctas_of(a)), kThreads, smem, stream, A, maps, stages);
   if (rc) return rc;
   const int64_t pairs = (int64_t)a.S * a.Hkv;
-  const int row_blocks = (int)((pairs * A.rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
+  // pairs cut into many pieces (few pairs over the CTAs) are joined by eight
+  // warps a row: 8 pairs of 37 pieces took 14 us with one
+  const bool many = ctas_of(a) >= 8 * pairs;
+  const int per = kJoinThreads / 32 / (many ? 8 : 1);  // rows of a block
+  const int row_blocks = (int)((pairs * A.rows + per - 1) / per);
   const int64_t keys = (int64_t)a.max_pages << a.page_shift;
   const int64_t blocks = row_blocks + (weights ? pairs * ((keys + kKeysPerBlock - 1) / kKeysPerBlock) : 0);
-  return launch_after(join_kernel<kFmt, kD>, dim3((unsigned)blocks), kJoinThreads, 0, stream, A, row_blocks);
+  return launch_after(many ? join_kernel<kFmt, kD, 8> : join_kernel<kFmt, kD, 1>, dim3((unsigned)blocks), kJoinThreads,
+                      0, stream, A, row_blocks);
 }
 
 }  // namespace dc

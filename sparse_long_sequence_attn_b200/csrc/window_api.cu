@@ -282,10 +282,12 @@ extern "C" int longnet_paged_attn_fwd(const void* q, const void* k_pages, const 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (dec && (impl == LONGNET_IMPL_AUTO || impl == LONGNET_IMPL_DECODE))
     return launch_decode(a, static_cast<float*>(workspace), weights, st);
-  rc = tc && impl != LONGNET_IMPL_SIMT ? launch_window_fwd_tc(a, static_cast<float*>(workspace), st)
-                                       : launch_window_fwd_simt(a, st);
-  if (rc || !weights) return rc;
-  return launch_weights_simt(a, weights, st);
+  if (tc && impl != LONGNET_IMPL_SIMT) {
+    rc = launch_window_fwd_tc(a, static_cast<float*>(workspace), st);
+    return rc || !weights ? rc : launch_weights_tc(a, weights, st);
+  }
+  rc = launch_window_fwd_simt(a, st);
+  return rc || !weights ? rc : launch_weights_simt(a, weights, st);
 }
 
 extern "C" int longnet_cache_evict(const void* k_pages, const void* v_pages, const float* weights,

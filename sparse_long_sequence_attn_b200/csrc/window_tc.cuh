@@ -26,6 +26,7 @@ bool window_tc_supports(const AttnArgs& a);
 WindowTcPlan window_tc_plan(const AttnArgs& a);
 int64_t window_tc_part_floats(const AttnArgs& a, const WindowTcPlan& p);
 int launch_window_fwd_tc(const AttnArgs& a, float* parts, cudaStream_t stream);
+int launch_weights_tc(const AttnArgs& a, float* weights, cudaStream_t stream);
 bool window_bwd_tc_supports(const AttnArgs& a);
 int window_bwd_tc_tile(int64_t D);  // keys of a work item of the key-centric kernel
 int launch_window_bwd_tc(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream);
