@@ -8,19 +8,19 @@
 //
 // Layout.  The G query heads of a key/value head read the same keys, so a
 // tile's 128 rows are 128 / G tokens by G heads.  A CTA owns two row tiles (A
-// and B) of one key/value head and streams 128-key blocks, K and V in turn,
-// through one ring that both tiles read: a key block is fetched once for 256
-// rows.  It visits only the blocks the mask reaches (those with sinks, then
-// those of the window).
+// and B) of one key/value head and streams 64-key blocks through one ring that
+// both tiles read: a key block is fetched once for 256 rows.  It visits only
+// the blocks the mask reaches (those with sinks, then those of the window).
 //   warps 0-3, 4-7  softmax of tile A and B, a thread per row: scores from
 //                   TMEM, P back over them in the input format, O rescaled in
 //                   TMEM only when the row maximum grew by more than 2^8
 //   warp 8          TMA loads; a block of a paged cache is a box per page
-//   warp 9          (10 and 11 idle, registers only) MMA issue: per block [P V of A, scores of A], [the same
-//                   of B], so one tile's products run under the other's
-//                   softmax.  In-order issue makes the score buffer's reuse
-//                   safe without a second buffer.
-// TMEM: two 128-column score buffers and two D-column accumulators.
+//   warps 9, 10     MMA issue for tile A and B: per block, P V and then the
+//                   scores two blocks further on.  One warp for both tiles is
+//                   busy all the time and sets the pace (3370 cycles per 64
+//                   keys at D = 128 where the softmax takes 1050)
+// TMEM: two 64-column score buffers per tile, so that a tile's next scores are
+// there when its softmax asks for them, and two D-column accumulators.
 // With fewer rows than one tile per key/value head (short chunks over a long
 // cache) both streams take the same tile and alternate blocks, and the keys
 // are split over CTAs; the parts are joined by combine_kernel.
@@ -44,29 +44,37 @@ namespace longnet {
 namespace wt {
 using namespace tc;
 
-// 384 x 168 registers at launch, dealt again as 208 for each softmax thread
-// and 88 for the loading and issuing warps: 128 x (208 + 208 + 88) = 384 x 168
-constexpr int kThreads = 384;
-constexpr int kTma = 8, kMma = 9;  // warps
+constexpr int kThreads = 352;
+constexpr int kTma = 8, kMma = 9;  // warps; kMma + 1 issues for the second stream
+constexpr int kBlk = 64;           // keys of a block
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 256;  // after the two score buffers
+constexpr uint32_t kColO = 256;  // after two score buffers per stream
 
 template <int kD>
 struct L : Panels<kD> {
   using P = Panels<kD>;
-  static constexpr int kQBytes = kTile * kD * 2;      // one row tile
-  static constexpr int kStageBytes = kTile * kD * 2;  // one block of keys or values
-  static constexpr int kStages = kD == 128 ? 5 : 8;
+  static constexpr int kQBytes = kTile * kD * 2;     // one row tile
+  static constexpr int kStageBytes = kBlk * kD * 2;  // one block of keys or values
+  static constexpr int kStages = kD == 128 ? 10 : 12;
   static constexpr int kBars = 2 * kQBytes + kStages * kStageBytes;
   // one CTA per SM at every D: its TMEM columns are all of the SM's
   static constexpr int kSmem = kBars + 512 + 1024 > 120 * 1024 ? kBars + 512 + 1024 : 120 * 1024;
+};
+
+// The blocks of a CTA's list that one stream takes.
+struct Range {
+  int sinks, begin, end, odd;
+  __device__ __forceinline__ bool has(int n) const {
+    return odd >= 0 ? (n & 1) == odd : n < end && (n < sinks || n >= begin);
+  }
 };
 
 template <int kFmt, int kD, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Maps maps, const Plan plan) {
   using LL = L<kD>;
-  constexpr int kPanels = LL::kPanels, kPanelBytes = kTile * LL::kRowBytes, S = LL::kStages;
+  constexpr int kPanels = LL::kPanels, S = LL::kStages;
+  constexpr int kQPanel = kTile * LL::kRowBytes, kKVPanel = kBlk * LL::kRowBytes;
   constexpr uint32_t kDescHi = LL::kDescHi;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -78,24 +86,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int t0 = plan.alternate ? 0 : pair * 2 * tpt;
   if (t0 >= q.nq) return;  // whole CTA, before any barrier or TMEM use
   const int t1 = t0 + (plan.alternate ? tpt : 2 * tpt) < q.nq ? t0 + (plan.alternate ? tpt : 2 * tpt) : q.nq;
-  const BlockList bl = blocks_of<kTile>(a, q.first + t0, q.first + t1 - 1);
+  const BlockList bl = blocks_of<kBlk>(a, q.first + t0, q.first + t1 - 1);
   const int per = (bl.count + plan.splits - 1) / plan.splits;
   const int n0 = split * per < bl.count ? split * per : bl.count;
   const int cnt = n0 + per < bl.count ? per : bl.count - n0;  // blocks [n0, n0 + cnt) of the list
-  auto block_key = [&](int n) { return bl.at(n0 + n) * kTile; };
+  auto block_key = [&](int n) { return bl.at(n0 + n) * kBlk; };
   // tokens [ta, tb) of stream st, empty when it has none
   auto tok_begin = [&](int st) { return plan.alternate ? t0 : t0 + st * tpt; };
   auto tok_end = [&](int st) {
     const int e = tok_begin(st) + tpt;
     return e < t1 ? e : t1;
   };
-  auto active = [&](int st, int n) -> bool {
-    if (plan.alternate) return (n & 1) == st;
-    const int b = tok_begin(st), e = tok_end(st), j0 = block_key(n);
-    if (b >= e) return false;
-    const int lo = q.first + b, hi = q.first + e - 1;
-    return j0 <= hi && (a.window == 0 || j0 < a.sinks || j0 + kTile - 1 > lo - a.window);
+  // the blocks a stream takes: of the list, those with sinks and those from
+  // its window's first key on, up to its last token
+  auto range_of = [&](int st) {
+    Range r;
+    const int tb = tok_begin(st), te = tok_end(st);
+    const int lo = q.first + tb, low = a.window == 0 || lo < a.window ? 0 : (lo - a.window + 1) / kBlk;
+    r.sinks = (a.sinks + kBlk - 1) / kBlk - n0;
+    r.begin = bl.n_sink + low - bl.win0 - n0;
+    const int end = q.first + te - 1 < 0 ? 0 : bl.n_sink + (q.first + te - 1) / kBlk - bl.win0 + 1 - n0;
+    r.end = tb < te ? (end < cnt ? end : cnt) : 0;
+    r.odd = plan.alternate ? st : -1;
+    return r;
   };
+  // The scores of block n + ahead are issued after P V of block n: two blocks
+  // of a stream further on.  The ring holds keys and values in the order of
+  // their use: the first `ahead` key blocks, then values n and keys n + ahead.
+  const int ahead = plan.alternate ? 4 : 2;
 
   uint8_t* sQ = smem;
   uint8_t* sStage = smem + 2 * LL::kQBytes;
@@ -103,28 +121,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar_q = bars;
   uint64_t* bar_full = bars + 1;       // [S]
   uint64_t* bar_empty = bars + 1 + S;  // [S]
-  uint64_t* bar_s = bars + 1 + 2 * S;  // [2] scores of a stream in TMEM
-  uint64_t* bar_p = bar_s + 2;         // [2] P of a stream in TMEM
-  uint64_t* bar_o = bar_s + 4;         // [2] a stream's last product done
-  uint64_t* bar_tail = bar_s + 6;      // the values of a block with slots past the sequence
-  uint64_t* bar_drain = bar_s + 7;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_s + 8);
+  uint64_t* bar_s = bars + 1 + 2 * S;  // [stream][buffer] scores in TMEM
+  uint64_t* bar_p = bar_s + 4;         // [stream][buffer] P in TMEM
+  uint64_t* bar_pv = bar_s + 8;        // [stream] O += P V of a block done
+  uint64_t* bar_o = bar_s + 10;        // [stream] the last one done
+  uint64_t* bar_tail = bar_s + 12;     // the values of a block with slots past the sequence
+  uint64_t* bar_drain = bar_s + 13;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_s + 14);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(bar_q, 1);
     for (int i = 0; i < S; ++i) {
       mbar_init(bar_full + i, 1);
-      mbar_init(bar_empty + i, 1);
+      mbar_init(bar_empty + i, 2);  // both streams
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(bar_s + i, 1);
       mbar_init(bar_p + i, 128);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_pv + i, 1);
       mbar_init(bar_o + i, 1);
     }
     mbar_init(bar_tail, 1);
-    mbar_init(bar_drain, 1);
+    mbar_init(bar_drain, 2);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -138,11 +160,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   Waiter wt{abort_flag, a.status, kWaitLimitNs};
 
-  if (warp >= kTma) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == kTma) {
     // ------------------------------------------------------------ loads
     bool ok = true;
@@ -152,28 +172,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int st = 0; st < qtiles; ++st)
 #pragma unroll
         for (int pn = 0; pn < kPanels; ++pn)
-          tma_load_3d(sQ + st * LL::kQBytes + pn * kPanelBytes, &maps.m[0], bar_q, LL::kPanelElems * pn, f * a.G,
+          tma_load_3d(sQ + st * LL::kQBytes + pn * kQPanel, &maps.m[0], bar_q, LL::kPanelElems * pn, f * a.G,
                       (int)(q.q0 + t0 + st * tpt));
     }
     int issued = 0;
-    for (int it = 0; it < 2 * cnt && ok; ++it) {
-      const int st = it % S;
+    auto load = [&](int n, int which) {  // which: 1 keys, 2 values
+      const int it = issued, st = it % S;
       if (it >= S) ok = wt.wait_warp(bar_empty + st, ((it / S) - 1) & 1);
-      if (!ok) break;
-      const int j0 = block_key(it >> 1);
-      const CUtensorMap* map = &maps.m[1 + (it & 1)];
+      if (!ok) return;
+      const int j0 = block_key(n);
       uint8_t* dst = sStage + st * LL::kStageBytes;
       if (!kPaged) {
         if (lane == 0) {
           mbar_arrive_expect_tx(bar_full + st, LL::kStageBytes);
 #pragma unroll
           for (int pn = 0; pn < kPanels; ++pn)
-            tma_load_4d(dst + pn * kPanelBytes, map, bar_full + st, LL::kPanelElems * pn, f, j0, s);
+            tma_load_4d(dst + pn * kKVPanel, &maps.m[which], bar_full + st, LL::kPanelElems * pn, f, j0, s);
         }
       } else {
-        load_pages<kD>(a, q, s, f, j0, kTile, (it & 1) != 0, map, dst, bar_full + st, bar_tail, lane, wt, &ok);
+        load_pages<kD>(a, q, s, f, j0, kBlk, which == 2, &maps.m[which], dst, bar_full + st, bar_tail, lane, wt, &ok);
       }
       issued = it + 1;
+    };
+    for (int n = -ahead; n < cnt && ok; ++n) {
+      if (n >= 0) load(n, 2);
+      if (ok && n + ahead < cnt) load(n + ahead, 1);
     }
     // drain: every issued load has landed before the CTA may exit
     if (lane == 0) {
@@ -184,112 +207,112 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
     }
-  } else if (warp == kMma) {
+  } else if (warp >= kMma) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0 && cnt > 0) {
-      constexpr uint32_t kIdS = idesc_f16kind(kTile, kTile, false, kFmt);  // 128 x 128, B K-major
-      constexpr uint32_t kIdO = idesc_f16kind(kTile, kD, true, kFmt);      // 128 x D, B MN-major
-      constexpr uint32_t lbo_mn = ((uint32_t)kPanelBytes >> 4) << 16;      // V's panel stride along D
-      auto stage_lo = [&](int it) -> uint32_t { return smem_u32(sStage + (it % S) * LL::kStageBytes) >> 4; };
-      auto scores = [&](int st, int n) {
-        const uint32_t q_lo = smem_u32(sQ + (plan.alternate ? 0 : st) * LL::kQBytes) >> 4;
-        const uint32_t k_lo = stage_lo(2 * n);
-#pragma unroll
-        for (int pn = 0; pn < kPanels; ++pn)
-#pragma unroll
-          for (int kk = 0; kk < LL::kPanelElems / 16; ++kk)
-            mma_ss(tmem + kTile * st, desc_from(((q_lo + pn * (kPanelBytes >> 4)) | (1u << 16)) + kk * 2, kDescHi),
-                   desc_from(((k_lo + pn * (kPanelBytes >> 4)) | (1u << 16)) + kk * 2, kDescHi), kIdS,
-                   (pn > 0 || kk > 0) ? 1u : 0u);
-        tc_commit(bar_s + st);
+    if (cnt > 0) {
+      constexpr uint32_t kIdS = idesc_f16kind(kTile, kBlk, false, kFmt);  // 128 x 64, B K-major
+      constexpr uint32_t kIdO = idesc_f16kind(kTile, kD, true, kFmt);     // 128 x D, B MN-major
+      constexpr uint32_t lbo_mn = ((uint32_t)kKVPanel >> 4) << 16;        // V's panel stride along D
+      const int st = warp - kMma;
+      const uint32_t leader = elect_leader();
+      const Range r = range_of(st);
+      int left = 0;  // blocks of this stream
+      for (int n = 0; n < cnt; ++n) left += r.has(n) ? 1 : 0;
+      const uint32_t q_lo = (smem_u32(sQ + (plan.alternate ? 0 : st) * LL::kQBytes) >> 4) | (1u << 16);
+      const uint32_t ring_lo = smem_u32(sStage) >> 4;
+      const uint32_t s_base = tmem + 2 * kBlk * st, o_base = tmem + kColO + kD * st;
+      int asked = 0, done = 0;     // blocks whose scores, whose P V are issued
+      int stage = 0, phase = 0;    // of the ring, in the order of its items
+      auto advance = [&] {
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1;
+        }
       };
-      int pending[2] = {-1, -1}, done[2] = {0, 0};  // block whose P V is due; blocks whose P V is issued
-      int left[2] = {0, 0};
-      for (int n = 0; n < cnt; ++n)
-        for (int st = 0; st < 2; ++st) left[st] += active(st, n) ? 1 : 0;
-      auto product = [&](int st) -> bool {
-        const int n = pending[st];
-        pending[st] = -1;
-        if (!wt.wait(bar_full + (2 * n + 1) % S, ((2 * n + 1) / S) & 1)) return false;
-        if (!wt.wait(bar_p + st, done[st] & 1)) return false;
-        tc_fence_after();
-        const uint32_t v_lo = stage_lo(2 * n + 1);
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_ts(tmem + kColO + kD * st, tmem + kTile * st + kk * 8,
-                 desc_from((v_lo | lbo_mn) + kk * (16 * LL::kRowBytes >> 4), kDescHi), kIdO,
-                 (done[st] > 0 || kk > 0) ? 1u : 0u);
-        if (++done[st] == left[st]) tc_commit(bar_o + st);
-        return true;
-      };
-      bool ok = wt.wait(bar_q, 0);
-      for (int n = 0; n <= cnt && ok; ++n) {
-        bool on[2] = {false, false};
-        if (n < cnt) {
-          ok = wt.wait(bar_full + (2 * n) % S, ((2 * n) / S) & 1);
+      bool ok = wt.wait_warp(bar_q, 0);
+      for (int n = -ahead; n < cnt && ok; ++n) {
+        if (n >= 0) {  // O += P V of block n
+          // (a block of the other stream's too is released only once it is
+          // there, so that this stream stays within a ring of the other)
+          ok = wt.wait_warp(bar_full + stage, phase);
           if (!ok) break;
-          tc_fence_after();
-          on[0] = active(0, n);
-          on[1] = active(1, n);
-        }
-        // a stream with nothing due starts its scores before the other's P is
-        // waited for
-        for (int st = 0; st < 2; ++st)
-          if (on[st] && pending[st] < 0) {
-            scores(st, n);
-            on[st] = false;
-            pending[st] = n + cnt + 1;  // due next time
+          if (r.has(n)) {
+            ok = wt.wait_warp(bar_p + 2 * st + (done & 1), (done >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t v_lo = (ring_lo + stage * (LL::kStageBytes >> 4)) | lbo_mn;
+            const uint32_t p_col = s_base + kBlk * (done & 1);
+#pragma unroll
+            for (int kk = 0; kk < kBlk / 16; ++kk)
+              mma_ts_if(leader, o_base, p_col + kk * 8, desc_from(v_lo + kk * (16 * LL::kRowBytes >> 4), kDescHi), kIdO,
+                        (done > 0 || kk > 0) ? 1u : 0u);
+            tc_commit_if(leader, bar_pv + st);
+            if (++done == left) tc_commit_if(leader, bar_o + st);
+            tc_commit_if(leader, bar_empty + stage);
+          } else {
+            mbar_arrive_if(leader, bar_empty + stage);
           }
-        for (int st = 0; st < 2 && ok; ++st) {
-          if (pending[st] >= 0 && pending[st] <= cnt) ok = product(st);
-          if (ok && on[st]) {
-            scores(st, n);
-            pending[st] = n + cnt + 1;
-          }
-          if (pending[st] > cnt) pending[st] -= cnt + 1;
+          advance();
         }
-        if (!ok) break;
-        if (n < cnt) tc_commit(bar_empty + (2 * n) % S);
-        if (n > 0) tc_commit(bar_empty + (2 * n - 1) % S);
+        if (n + ahead < cnt) {  // the scores of block n + ahead
+          ok = wt.wait_warp(bar_full + stage, phase);
+          if (!ok) break;
+          if (r.has(n + ahead)) {
+            tc_fence_after();
+            const uint32_t k_lo = (ring_lo + stage * (LL::kStageBytes >> 4)) | (1u << 16);
+            const uint32_t s_col = s_base + kBlk * (asked & 1);
+#pragma unroll
+            for (int pn = 0; pn < kPanels; ++pn)
+#pragma unroll
+              for (int kk = 0; kk < LL::kPanelElems / 16; ++kk)
+                mma_ss_if(leader, s_col, desc_from(q_lo + pn * (kQPanel >> 4) + kk * 2, kDescHi),
+                          desc_from(k_lo + pn * (kKVPanel >> 4) + kk * 2, kDescHi), kIdS, (pn > 0 || kk > 0) ? 1u : 0u);
+            tc_commit_if(leader, bar_s + 2 * st + (asked & 1));
+            tc_commit_if(leader, bar_empty + stage);
+            ++asked;
+          } else {
+            mbar_arrive_if(leader, bar_empty + stage);
+          }
+          advance();
+        }
       }
       // drain: all issued MMAs complete before TMEM is released
-      tc_commit(bar_drain);
+      tc_commit_if(leader, bar_drain);
       if (!mbar_wait(bar_drain, 0, kWaitLimitNs)) record_status(a.status, kStatusTimeout);
     }
-  }
-  } else {
+  } else if (warp < kTma) {
     // ------------------------------------------------------------ softmax and epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int st = warp >> 2;
     const int row = 32 * (warp & 3) + lane;  // TMEM lane = tile row
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t s_col = tmem + lane_base + kTile * st, o_col = tmem + lane_base + kColO + kD * st;
+    const uint32_t o_col = tmem + lane_base + kColO + kD * st;
     const int ta = tok_begin(st), tb = tok_end(st);
     const int i = ta + row / a.G;
     const bool row_ok = row < tpt * a.G && i < tb;
     const int x = row_ok ? q.first + i : -1;
     const int x_lo = q.first + ta, x_hi = q.first + tb - 1;
     const uint64_t sc2 = f32x2(a.scale_log2, a.scale_log2);
+    const Range r = range_of(st);
     float m_use = -INFINITY, l_run = 0.f;
     int done = 0;
     bool ok = true;
     for (int n = 0; n < cnt && ok; ++n) {
-      if (!active(st, n)) continue;
+      if (!r.has(n)) continue;
       const int j0 = block_key(n);
-      ok = wt.wait_warp(bar_s + st, done & 1);
+      const int buf = 2 * st + (done & 1);
+      const uint32_t s_col = tmem + lane_base + kBlk * buf;
+      ok = wt.wait_warp(bar_s + buf, (done >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      uint32_t sr[kTile];
+      uint32_t sr[kBlk];
       LN_TMEM_LD32(s_col, (sr + 0));
       LN_TMEM_LD32(s_col + 32, (sr + 32));
-      LN_TMEM_LD32(s_col + 64, (sr + 64));
-      LN_TMEM_LD32(s_col + 96, (sr + 96));
       tmem_wait_ld();
       // a block that some row of the tile does not see whole
-      if (j0 + kTile - 1 > x_lo || (a.window && x_hi - j0 >= a.window && j0 + kTile > a.sinks) || !row_ok) {
+      if (j0 + kBlk - 1 > x_lo || (a.window && x_hi - j0 >= a.window && j0 + kBlk > a.sinks) || !row_ok) {
         const int hi = x - j0, lo = a.window ? hi - a.window + 1 : -1, sk = a.sinks - j0;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < 2; ++w) {
           const uint32_t keep = below(hi + 1 - 32 * w) & (~below(lo - 32 * w) | below(sk - 32 * w));
 #pragma unroll
           for (int c = 0; c < 32; ++c)
@@ -300,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 8; ++e) pm[e] = __uint_as_float(sr[e]);
 #pragma unroll
-      for (int c = 8; c < kTile; ++c) pm[c & 7] = fmaxf(pm[c & 7], __uint_as_float(sr[c]));
+      for (int c = 8; c < kBlk; ++c) pm[c & 7] = fmaxf(pm[c & 7], __uint_as_float(sr[c]));
       const float mx = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
                              fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
       const float m_blk = mx * a.scale_log2;
@@ -310,7 +333,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         m_use = m_blk;
       }
       if (done > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
-        // the products of earlier blocks ran before these scores (in-order issue)
+        // the product of the block before is the latest that may still run
+        ok = wt.wait_warp(bar_pv + st, (done - 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
         l_run *= corr;
         constexpr int kChunk = kD < 32 ? kD : 32;
 #pragma unroll 1
@@ -324,28 +350,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_wait_st();
       }
-      // P = 2^(s scale - m), packed over the first 64 columns
+      // P = 2^(s scale - m), packed over the buffer's first 32 columns
       const float base = m_use == -INFINITY ? 0.f : m_use;  // a row with nothing to see so far
       const uint64_t nm2 = f32x2(-base, -base);
       uint64_t ls[4] = {0, 0, 0, 0};
+      uint32_t pk[32];
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          float xa, xb;
-          f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[64 * w + 2 * c]), __uint_as_float(sr[64 * w + 2 * c + 1])),
-                                sc2, nm2),
-                      xa, xb);
-          const float pa = ex2(xa), pb = ex2(xb);
-          ls[c & 3] = add_f32x2(ls[c & 3], f32x2(pa, pb));
-          pk[c] = pack2<kFmt>(pa, pb);
-        }
-        LN_TMEM_ST32(s_col + 32 * w, pk);
+      for (int c = 0; c < 32; ++c) {
+        float xa, xb;
+        f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), sc2, nm2), xa, xb);
+        const float pa = ex2(xa), pb = ex2(xb);
+        ls[c & 3] = add_f32x2(ls[c & 3], f32x2(pa, pb));
+        pk[c] = pack2<kFmt>(pa, pb);
       }
+      LN_TMEM_ST32(s_col, pk);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(bar_p + st);
+      mbar_arrive(bar_p + buf);
       float t0s, t1s;
       f32x2_split(add_f32x2(add_f32x2(ls[0], ls[1]), add_f32x2(ls[2], ls[3])), t0s, t1s);
       l_run += t0s + t1s;
@@ -464,8 +485,8 @@ int launch_typed(const AttnArgs& a, const Plan& plan, cudaStream_t stream) {
   Maps maps;
   EncodeTiledFn enc = get_encoder();
   if (!enc) return LONGNET_ERR_CUDA;
-  if (!encode_q(enc, &maps.m[0], a.q, a, plan.tokens) || !encode_kv(enc, &maps.m[1], a.k, a, kTile) ||
-      !encode_kv(enc, &maps.m[2], a.v, a, kTile))
+  if (!encode_q(enc, &maps.m[0], a.q, a, plan.tokens) || !encode_kv(enc, &maps.m[1], a.k, a, kBlk) ||
+      !encode_kv(enc, &maps.m[2], a.v, a, kBlk))
     return LONGNET_ERR_CUDA;
   auto fn = a.cu_q ? fwd_kernel<kFmt, kD, true> : fwd_kernel<kFmt, kD, false>;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, LL::kSmem) != cudaSuccess) {
@@ -493,7 +514,7 @@ bool window_tc_supports(const AttnArgs& a) {
 
 // The split of one call.  A contiguous call is never split (its row tiles fill
 // the GPU); a paged one is when its row tiles leave SMs idle: enough splits to
-// fill them once, of at least four blocks each at the cache's capacity.
+// fill them once, of at least eight blocks each at the cache's capacity.
 WindowTcPlan window_tc_plan(const AttnArgs& a) {
   WindowTcPlan p;
   memset(&p, 0, sizeof(p));
@@ -502,14 +523,14 @@ WindowTcPlan window_tc_plan(const AttnArgs& a) {
   p.parts = 1;
   if (!a.cu_q) return p;
   p.alternate = a.nq_max <= p.tokens;
-  const int64_t cap_blocks = (((int64_t)a.max_pages << a.page_shift) + wt::kTile - 1) / wt::kTile;
+  const int64_t cap_blocks = (((int64_t)a.max_pages << a.page_shift) + wt::kBlk - 1) / wt::kBlk;
   // blocks a row tile can visit
-  const int64_t reach = a.window ? ((int64_t)a.window + a.sinks + p.tokens * 2) / wt::kTile + 2 : cap_blocks;
+  const int64_t reach = a.window ? ((int64_t)a.window + a.sinks + p.tokens * 2) / wt::kBlk + 2 : cap_blocks;
   const int64_t blocks = reach < cap_blocks ? reach : cap_blocks;
   const int64_t pairs = p.alternate ? 1 : ((int64_t)a.nq_max + 2 * p.tokens - 1) / (2 * p.tokens);
   const int64_t ctas = pairs * a.S * a.Hkv;
   int64_t splits = ctas >= 148 ? 1 : 148 / ctas;
-  if (splits > blocks / 4) splits = blocks / 4;
+  if (splits > blocks / 8) splits = blocks / 8;
   if (splits < 1) splits = 1;
   if (splits > 64) splits = 64;
   p.splits = (int)splits;
