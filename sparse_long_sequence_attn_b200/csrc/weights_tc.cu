@@ -109,7 +109,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == kTma) {
     // ------------------------------------------------------------ loads
     bool ok = true;
-    load_pages<kD>(a, q, s, f, j0, kTile, false, &maps.m[1], smem, bar_k, nullptr, lane, wt, &ok);
+    load_pages<kD>(a, q, s, f, j0, kTile, &maps.m[1], smem, bar_k, lane);
+    if (lane == 0) mbar_arrive(bar_k);
     int issued = 0;
     for (int n = 0; n < cnt && ok; ++n) {
       const int st = n % S;

@@ -54,19 +54,22 @@ template <int kD>
 struct L : Panels<kD> {
   using P = Panels<kD>;
   static constexpr int kQBytes = kTile * kD * 2;     // one row tile
-  static constexpr int kStageBytes = kBlk * kD * 2;  // one block of keys or values
-  static constexpr int kStages = kD == 128 ? 10 : 12;
+  static constexpr int kHalf = kBlk * kD * 2;        // one block of keys or values
+  static constexpr int kStageBytes = 2 * kHalf;      // values of block n, keys of block n + ahead
+  static constexpr int kStages = kD == 128 ? 5 : 6;
   static constexpr int kBars = 2 * kQBytes + kStages * kStageBytes;
   // one CTA per SM at every D: its TMEM columns are all of the SM's
   static constexpr int kSmem = kBars + 512 + 1024 > 120 * 1024 ? kBars + 512 + 1024 : 120 * 1024;
 };
 
-// The blocks of a CTA's list that one stream takes.
+// The blocks of a CTA's list that one stream takes: a run [begin, end), or
+// every second one.  A run has no gap, since the softmax asks for a block's
+// scores before it hands over the P of the block before; so a stream with
+// sinks also takes the few blocks between them and its window that only the
+// other stream sees, all masked.
 struct Range {
-  int sinks, begin, end, odd;
-  __device__ __forceinline__ bool has(int n) const {
-    return odd >= 0 ? (n & 1) == odd : n < end && (n < sinks || n >= begin);
-  }
+  int begin, end, odd;
+  __device__ __forceinline__ bool has(int n) const { return odd >= 0 ? (n & 1) == odd : n >= begin && n < end; }
 };
 
 template <int kFmt, int kD, bool kPaged>
@@ -97,22 +100,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int e = tok_begin(st) + tpt;
     return e < t1 ? e : t1;
   };
-  // the blocks a stream takes: of the list, those with sinks and those from
-  // its window's first key on, up to its last token
   auto range_of = [&](int st) {
     Range r;
     const int tb = tok_begin(st), te = tok_end(st);
     const int lo = q.first + tb, low = a.window == 0 || lo < a.window ? 0 : (lo - a.window + 1) / kBlk;
-    r.sinks = (a.sinks + kBlk - 1) / kBlk - n0;
-    r.begin = bl.n_sink + low - bl.win0 - n0;
+    r.begin = n0 * kBlk < a.sinks ? 0 : bl.n_sink + low - bl.win0 - n0;
     const int end = q.first + te - 1 < 0 ? 0 : bl.n_sink + (q.first + te - 1) / kBlk - bl.win0 + 1 - n0;
     r.end = tb < te ? (end < cnt ? end : cnt) : 0;
     r.odd = plan.alternate ? st : -1;
     return r;
   };
   // The scores of block n + ahead are issued after P V of block n: two blocks
-  // of a stream further on.  The ring holds keys and values in the order of
-  // their use: the first `ahead` key blocks, then values n and keys n + ahead.
+  // of a stream further on.  Item n of the ring holds what that step takes:
+  // the values of block n (none for n < 0) and the keys of block n + ahead
+  // (none past the last).
   const int ahead = plan.alternate ? 4 : 2;
 
   uint8_t* sQ = smem;
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar_empty = bars + 1 + S;  // [S]
   uint64_t* bar_s = bars + 1 + 2 * S;  // [stream][buffer] scores in TMEM
   uint64_t* bar_p = bar_s + 4;         // [stream][buffer] P in TMEM
-  uint64_t* bar_pv = bar_s + 8;        // [stream] O += P V of a block done
+  uint64_t* bar_pv = bar_s + 8;        // [stream] the last product but one done
   uint64_t* bar_o = bar_s + 10;        // [stream] the last one done
   uint64_t* bar_tail = bar_s + 12;     // the values of a block with slots past the sequence
   uint64_t* bar_drain = bar_s + 13;
@@ -176,32 +177,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                       (int)(q.q0 + t0 + st * tpt));
     }
     int issued = 0;
-    auto load = [&](int n, int which) {  // which: 1 keys, 2 values
-      const int it = issued, st = it % S;
-      if (it >= S) ok = wt.wait_warp(bar_empty + st, ((it / S) - 1) & 1);
-      if (!ok) return;
-      const int j0 = block_key(n);
+    for (int n = -ahead; n < cnt && ok; ++n, ++issued) {
+      const int st = issued % S;
+      if (issued >= S) ok = wt.wait_warp(bar_empty + st, ((issued / S) - 1) & 1);
+      if (!ok) break;
       uint8_t* dst = sStage + st * LL::kStageBytes;
+      const bool v = n >= 0, k = n + ahead < cnt;
       if (!kPaged) {
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar_full + st, LL::kStageBytes);
+          mbar_arrive_expect_tx(bar_full + st, ((v ? 1 : 0) + (k ? 1 : 0)) * LL::kHalf);
 #pragma unroll
-          for (int pn = 0; pn < kPanels; ++pn)
-            tma_load_4d(dst + pn * kKVPanel, &maps.m[which], bar_full + st, LL::kPanelElems * pn, f, j0, s);
+          for (int pn = 0; pn < kPanels; ++pn) {
+            if (v)
+              tma_load_4d(dst + pn * kKVPanel, &maps.m[2], bar_full + st, LL::kPanelElems * pn, f, block_key(n), s);
+            if (k)
+              tma_load_4d(dst + LL::kHalf + pn * kKVPanel, &maps.m[1], bar_full + st, LL::kPanelElems * pn, f,
+                          block_key(n + ahead), s);
+          }
         }
       } else {
-        load_pages<kD>(a, q, s, f, j0, kBlk, which == 2, &maps.m[which], dst, bar_full + st, bar_tail, lane, wt, &ok);
+        // expect each half's bytes, then arrive once
+        if (k) load_pages<kD>(a, q, s, f, block_key(n + ahead), kBlk, &maps.m[1], dst + LL::kHalf, bar_full + st, lane);
+        if (v) {
+          const int j0 = block_key(n);
+          const bool tail = j0 + kBlk > q.kv;  // the sequence's last block
+          load_pages<kD>(a, q, s, f, j0, kBlk, &maps.m[2], dst, tail ? bar_tail : bar_full + st, lane);
+          if (tail) {
+            if (lane == 0) mbar_arrive(bar_tail);
+            ok = wt.wait_warp(bar_tail, 0);
+            if (!ok) break;
+            zero_rows<kD>(dst, kBlk, q.kv - j0, lane);
+          }
+        }
+        if (lane == 0) mbar_arrive(bar_full + st);
       }
-      issued = it + 1;
-    };
-    for (int n = -ahead; n < cnt && ok; ++n) {
-      if (n >= 0) load(n, 2);
-      if (ok && n + ahead < cnt) load(n + ahead, 1);
     }
     // drain: every issued load has landed before the CTA may exit
     if (lane == 0) {
       if (cnt > 0 && !mbar_wait(bar_q, 0, kWaitLimitNs)) record_status(a.status, kStatusTimeout);
-      for (int it = issued > S ? issued - S : 0; it < issued && ok; ++it)
+      for (int it = issued > S ? issued - S : 0; it < issued; ++it)
         if (!mbar_wait(bar_full + (it % S), (it / S) & 1, kWaitLimitNs)) {
           record_status(a.status, kStatusTimeout);
           break;
@@ -221,66 +235,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_lo = (smem_u32(sQ + (plan.alternate ? 0 : st) * LL::kQBytes) >> 4) | (1u << 16);
       const uint32_t ring_lo = smem_u32(sStage) >> 4;
       const uint32_t s_base = tmem + 2 * kBlk * st, o_base = tmem + kColO + kD * st;
-      int asked = 0, done = 0;     // blocks whose scores, whose P V are issued
-      int stage = 0, phase = 0;    // of the ring, in the order of its items
-      auto advance = [&] {
+      int asked = 0, done = 0;   // blocks whose scores, whose P V are issued
+      int stage = 0, phase = 0;  // of the ring
+      bool ok = wt.wait_warp(bar_q, 0);
+      for (int n = -ahead; n < cnt && ok; ++n) {
+        const bool pv = n >= 0 && r.has(n), sc = n + ahead < cnt && r.has(n + ahead);
+        // (an item that only the other stream uses is released once it is
+        // there, so that this stream stays within a ring of the other)
+        ok = wt.wait_warp(bar_full + stage, phase);
+        if (!ok) break;
+        const uint32_t v_lo = ring_lo + stage * (LL::kStageBytes >> 4);
+        if (pv) {  // O += P V of block n
+          ok = wt.wait_warp(bar_p + 2 * st + (done & 1), (done >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t p_col = s_base + kBlk * (done & 1);
+#pragma unroll
+          for (int kk = 0; kk < kBlk / 16; ++kk)
+            mma_ts_if(leader, o_base, p_col + kk * 8, desc_from((v_lo | lbo_mn) + kk * (16 * LL::kRowBytes >> 4), kDescHi),
+                      kIdO, (done > 0 || kk > 0) ? 1u : 0u);
+          ++done;
+          if (done >= left - 1) tc_commit_if(leader, done == left ? bar_o + st : bar_pv + st);
+        }
+        if (sc) {  // the scores of block n + ahead
+          tc_fence_after();
+          const uint32_t k_lo = (v_lo + (LL::kHalf >> 4)) | (1u << 16);
+          const uint32_t s_col = s_base + kBlk * (asked & 1);
+#pragma unroll
+          for (int pn = 0; pn < kPanels; ++pn)
+#pragma unroll
+            for (int kk = 0; kk < LL::kPanelElems / 16; ++kk)
+              mma_ss_if(leader, s_col, desc_from(q_lo + pn * (kQPanel >> 4) + kk * 2, kDescHi),
+                        desc_from(k_lo + pn * (kKVPanel >> 4) + kk * 2, kDescHi), kIdS, (pn > 0 || kk > 0) ? 1u : 0u);
+          tc_commit_if(leader, bar_s + 2 * st + (asked & 1));
+          ++asked;
+        }
+        if (pv || sc)
+          tc_commit_if(leader, bar_empty + stage);
+        else
+          mbar_arrive_if(leader, bar_empty + stage);
         if (++stage == S) {
           stage = 0;
           phase ^= 1;
-        }
-      };
-      bool ok = wt.wait_warp(bar_q, 0);
-      for (int n = -ahead; n < cnt && ok; ++n) {
-        if (n >= 0) {  // O += P V of block n
-          // (a block of the other stream's too is released only once it is
-          // there, so that this stream stays within a ring of the other)
-          ok = wt.wait_warp(bar_full + stage, phase);
-          if (!ok) break;
-          if (r.has(n)) {
-            ok = wt.wait_warp(bar_p + 2 * st + (done & 1), (done >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t v_lo = (ring_lo + stage * (LL::kStageBytes >> 4)) | lbo_mn;
-            const uint32_t p_col = s_base + kBlk * (done & 1);
-#pragma unroll
-            for (int kk = 0; kk < kBlk / 16; ++kk)
-              mma_ts_if(leader, o_base, p_col + kk * 8, desc_from(v_lo + kk * (16 * LL::kRowBytes >> 4), kDescHi), kIdO,
-                        (done > 0 || kk > 0) ? 1u : 0u);
-            tc_commit_if(leader, bar_pv + st);
-            if (++done == left) tc_commit_if(leader, bar_o + st);
-            tc_commit_if(leader, bar_empty + stage);
-          } else {
-            mbar_arrive_if(leader, bar_empty + stage);
-          }
-          advance();
-        }
-        if (n + ahead < cnt) {  // the scores of block n + ahead
-          ok = wt.wait_warp(bar_full + stage, phase);
-          if (!ok) break;
-          if (r.has(n + ahead)) {
-            tc_fence_after();
-            const uint32_t k_lo = (ring_lo + stage * (LL::kStageBytes >> 4)) | (1u << 16);
-            const uint32_t s_col = s_base + kBlk * (asked & 1);
-#pragma unroll
-            for (int pn = 0; pn < kPanels; ++pn)
-#pragma unroll
-              for (int kk = 0; kk < LL::kPanelElems / 16; ++kk)
-                mma_ss_if(leader, s_col, desc_from(q_lo + pn * (kQPanel >> 4) + kk * 2, kDescHi),
-                          desc_from(k_lo + pn * (kKVPanel >> 4) + kk * 2, kDescHi), kIdS, (pn > 0 || kk > 0) ? 1u : 0u);
-            tc_commit_if(leader, bar_s + 2 * st + (asked & 1));
-            tc_commit_if(leader, bar_empty + stage);
-            ++asked;
-          } else {
-            mbar_arrive_if(leader, bar_empty + stage);
-          }
-          advance();
         }
       }
       // drain: all issued MMAs complete before TMEM is released
       tc_commit_if(leader, bar_drain);
       if (!mbar_wait(bar_drain, 0, kWaitLimitNs)) record_status(a.status, kStatusTimeout);
     }
-  } else if (warp < kTma) {
+  } else {
     // ------------------------------------------------------------ softmax and epilogue
     const int st = warp >> 2;
     const int row = 32 * (warp & 3) + lane;  // TMEM lane = tile row
@@ -289,52 +292,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ta = tok_begin(st), tb = tok_end(st);
     const int i = ta + row / a.G;
     const bool row_ok = row < tpt * a.G && i < tb;
-    const int x = row_ok ? q.first + i : -1;
+    const int pos = row_ok ? q.first + i : -1;
     const int x_lo = q.first + ta, x_hi = q.first + tb - 1;
     const uint64_t sc2 = f32x2(a.scale_log2, a.scale_log2);
     const Range r = range_of(st);
+    int left = 0;  // blocks of this stream
+    for (int n = 0; n < cnt; ++n) left += r.has(n) ? 1 : 0;
     float m_use = -INFINITY, l_run = 0.f;
     int done = 0;
     bool ok = true;
-    for (int n = 0; n < cnt && ok; ++n) {
-      if (!r.has(n)) continue;
-      const int j0 = block_key(n);
-      const int buf = 2 * st + (done & 1);
-      const uint32_t s_col = tmem + lane_base + kBlk * buf;
-      ok = wt.wait_warp(bar_s + buf, (done >> 1) & 1);
-      if (!ok) break;
+    // Scores of block n from TMEM, what the row does not see at -inf.
+    auto take = [&](int n, int k, uint32_t(&x)[kBlk]) {
+      const uint32_t s_col = tmem + lane_base + kBlk * (2 * st + (k & 1));
+      ok = wt.wait_warp(bar_s + 2 * st + (k & 1), (k >> 1) & 1);
+      if (!ok) return;
       tc_fence_after();
-      uint32_t sr[kBlk];
-      LN_TMEM_LD32(s_col, (sr + 0));
-      LN_TMEM_LD32(s_col + 32, (sr + 32));
+      LN_TMEM_LD32(s_col, (x + 0));
+      LN_TMEM_LD32(s_col + 32, (x + 32));
       tmem_wait_ld();
+      const int j0 = block_key(n);
       // a block that some row of the tile does not see whole
       if (j0 + kBlk - 1 > x_lo || (a.window && x_hi - j0 >= a.window && j0 + kBlk > a.sinks) || !row_ok) {
-        const int hi = x - j0, lo = a.window ? hi - a.window + 1 : -1, sk = a.sinks - j0;
+        const int hi = pos - j0, lo = a.window ? hi - a.window + 1 : -1, sk = a.sinks - j0;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const uint32_t keep = below(hi + 1 - 32 * w) & (~below(lo - 32 * w) | below(sk - 32 * w));
 #pragma unroll
           for (int c = 0; c < 32; ++c)
-            if (!((keep >> c) & 1)) sr[32 * w + c] = __float_as_uint(-INFINITY);
+            if (!((keep >> c) & 1)) x[32 * w + c] = __float_as_uint(-INFINITY);
         }
       }
-      float pm[8];
+    };
+    auto maximum = [&](const uint32_t(&x)[kBlk]) -> float {
+      float pm[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) pm[e] = __uint_as_float(sr[e]);
+      for (int e = 0; e < 4; ++e) pm[e] = max3(__uint_as_float(x[e]), __uint_as_float(x[e + 4]), __uint_as_float(x[e + 8]));
 #pragma unroll
-      for (int c = 8; c < kBlk; ++c) pm[c & 7] = fmaxf(pm[c & 7], __uint_as_float(sr[c]));
-      const float mx = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
-                             fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
-      const float m_blk = mx * a.scale_log2;
+      for (int c = 12; c + 8 <= kBlk; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          pm[e] = max3(pm[e], __uint_as_float(x[c + e]), __uint_as_float(x[c + e + 4]));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) pm[e] = fmaxf(pm[e], __uint_as_float(x[kBlk - 4 + e]));
+      return max3(fmaxf(pm[0], pm[1]), pm[2], pm[3]) * a.scale_log2;
+    };
+    uint32_t x[kBlk], pk[32];
+    for (int n = 0; n < cnt; ++n) {
+      if (!r.has(n)) continue;
+      take(n, done, x);
+      if (!ok) break;
+      const float m_blk = maximum(x);
       float corr = 1.f;
       if (m_blk > m_use + 8.f) {  // also from -inf, the first visible key
         corr = ex2(m_use - m_blk);
         m_use = m_blk;
       }
       if (done > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
-        // the product of the block before is the latest that may still run
-        ok = wt.wait_warp(bar_pv + st, (done - 1) & 1);
+        // O holds the products up to the block before, the latest that may
+        // still run: it is done when the next block's scores are, which were
+        // issued after it
+        ok = done + 1 < left ? wt.wait_warp(bar_s + 2 * st + ((done + 1) & 1), ((done + 1) >> 1) & 1)
+                             : wt.wait_warp(bar_pv + st, 0);
         if (!ok) break;
         tc_fence_after();
         l_run *= corr;
@@ -348,25 +366,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < kChunk; ++c) rr[c] = __float_as_uint(__uint_as_float(rr[c]) * corr);
           tmem_store<kChunk>(o_col + c0, rr);
         }
-        tmem_wait_st();
       }
       // P = 2^(s scale - m), packed over the buffer's first 32 columns
       const float base = m_use == -INFINITY ? 0.f : m_use;  // a row with nothing to see so far
       const uint64_t nm2 = f32x2(-base, -base);
       uint64_t ls[4] = {0, 0, 0, 0};
-      uint32_t pk[32];
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
         float xa, xb;
-        f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), sc2, nm2), xa, xb);
+        f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sc2, nm2), xa, xb);
         const float pa = ex2(xa), pb = ex2(xb);
         ls[c & 3] = add_f32x2(ls[c & 3], f32x2(pa, pb));
         pk[c] = pack2<kFmt>(pa, pb);
       }
-      LN_TMEM_ST32(s_col, pk);
+      LN_TMEM_ST32(tmem + lane_base + kBlk * (2 * st + (done & 1)), pk);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(bar_p + buf);
+      mbar_arrive(bar_p + 2 * st + (done & 1));
       float t0s, t1s;
       f32x2_split(add_f32x2(add_f32x2(ls[0], ls[1]), add_f32x2(ls[2], ls[3])), t0s, t1s);
       l_run += t0s + t1s;

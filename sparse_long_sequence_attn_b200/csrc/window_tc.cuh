@@ -152,6 +152,13 @@ struct Waiter {
   __device__ bool wait_warp(uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); }
 };
 
+// The largest of three, in one instruction.
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+  return m;
+}
+
 // The lowest n bits (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t below(int n) {
   return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
@@ -174,16 +181,13 @@ __device__ __forceinline__ void tmem_store(uint32_t taddr, uint32_t (&r)[kN]) {
   }
 }
 
-// Keys [j0, j0 + rows) of a paged cache into a block in shared memory, by one
-// warp: a lane looks up a page and issues its boxes.  Pages past the
-// sequence's last key are not read.  For values, the rows past the last key
-// are then overwritten with zeros (a weight of 0 would turn a NaN there into
-// a NaN row): such a block's loads complete on bar_tail (used once, by the
-// last block) and the warp arrives on bar_full itself.
+// Rows [j0, j0 + rows) of a paged cache into a block in shared memory, by one
+// warp: a lane looks up a page and issues its boxes, whose bytes are added to
+// the barrier's current phase (the caller arrives).  Pages past the sequence's
+// last key are not read.
 template <int kD>
-__device__ __forceinline__ void load_pages(const AttnArgs& a, const Seq& q, int s, int f, int j0, int rows, bool values,
-                                           const CUtensorMap* map, uint8_t* dst, uint64_t* bar_full,
-                                           uint64_t* bar_tail, int lane, Waiter& wt, bool* ok) {
+__device__ __forceinline__ void load_pages(const AttnArgs& a, const Seq& q, int s, int f, int j0, int rows,
+                                           const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int lane) {
   using LL = Panels<kD>;
   const int box = a.page < rows ? a.page : rows;  // rows of a box
   const int boxes = rows / box;                   // at most 16
@@ -198,9 +202,7 @@ __device__ __forceinline__ void load_pages(const AttnArgs& a, const Seq& q, int 
     }
   }
   const uint32_t count = __popc(__ballot_sync(0xffffffffu, live));
-  const bool tail = values && j0 + rows > q.kv;
-  uint64_t* bar = tail ? bar_tail : bar_full;
-  if (lane == 0) mbar_arrive_expect_tx(bar, count * (uint32_t)(box * kD * 2));
+  if (lane == 0) mbar_expect_tx(bar, count * (uint32_t)(box * kD * 2));
   __syncwarp();
   if (live) {
 #pragma unroll
@@ -208,22 +210,21 @@ __device__ __forceinline__ void load_pages(const AttnArgs& a, const Seq& q, int 
       tma_load_4d(dst + pn * rows * LL::kRowBytes + lane * box * LL::kRowBytes, map, bar, LL::kPanelElems * pn, f,
                   j & (a.page - 1), pg);
   }
-  if (tail) {
-    if (!wt.wait_warp(bar_tail, 0)) {
-      *ok = false;
-      return;
-    }
-    const int keep = q.kv - j0;  // rows with a key
-    constexpr int kCpr = LL::kRowBytes / 16;
-    const int chunks = (rows - keep) * kCpr;  // of one panel
-    for (int pn = 0; pn < LL::kPanels; ++pn)
-      for (int c = lane; c < chunks; c += 32)
-        *reinterpret_cast<uint4*>(dst + pn * rows * LL::kRowBytes + keep * LL::kRowBytes + c * 16) =
-            make_uint4(0, 0, 0, 0);
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_full);
-  }
+}
+
+// Rows [keep, rows) of a loaded block overwritten with zeros, for the products
+// to read: slots past a sequence's keys may hold anything, and a weight of 0
+// would turn a NaN there into a NaN row.
+template <int kD>
+__device__ __forceinline__ void zero_rows(uint8_t* dst, int rows, int keep, int lane) {
+  using LL = Panels<kD>;
+  const int chunks = (rows - keep) * (LL::kRowBytes / 16);  // of one panel
+  for (int pn = 0; pn < LL::kPanels; ++pn)
+    for (int c = lane; c < chunks; c += 32)
+      *reinterpret_cast<uint4*>(dst + pn * rows * LL::kRowBytes + keep * LL::kRowBytes + c * 16) =
+          make_uint4(0, 0, 0, 0);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
 }
 
 // [T, H, D] as (d, h, t): a box is one panel of G heads by `tokens` tokens.
