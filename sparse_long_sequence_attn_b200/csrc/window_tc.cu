@@ -68,8 +68,10 @@ struct L : Panels<kD> {
 // sinks also takes the few blocks between them and its window that only the
 // other stream sees, all masked.
 struct Range {
-  int begin, end, odd;
-  __device__ __forceinline__ bool has(int n) const { return odd >= 0 ? (n & 1) == odd : n >= begin && n < end; }
+  int begin, end, step, count;
+  __device__ __forceinline__ bool has(int n) const {
+    return n >= begin && n < end && (step == 1 || ((n - begin) & 1) == 0);
+  }
 };
 
 template <int kFmt, int kD, bool kPaged>
@@ -104,10 +106,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     Range r;
     const int tb = tok_begin(st), te = tok_end(st);
     const int lo = q.first + tb, low = a.window == 0 || lo < a.window ? 0 : (lo - a.window + 1) / kBlk;
+    if (plan.alternate) {
+      r.begin = st;
+      r.end = cnt;
+      r.step = 2;
+      r.count = (cnt + 1 - st) / 2;
+      return r;
+    }
     r.begin = n0 * kBlk < a.sinks ? 0 : bl.n_sink + low - bl.win0 - n0;
+    if (r.begin < 0) r.begin = 0;
     const int end = q.first + te - 1 < 0 ? 0 : bl.n_sink + (q.first + te - 1) / kBlk - bl.win0 + 1 - n0;
     r.end = tb < te ? (end < cnt ? end : cnt) : 0;
-    r.odd = plan.alternate ? st : -1;
+    r.step = 1;
+    r.count = r.end > r.begin ? r.end - r.begin : 0;
     return r;
   };
   // The scores of block n + ahead are issued after P V of block n: two blocks
@@ -230,8 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int st = warp - kMma;
       const uint32_t leader = elect_leader();
       const Range r = range_of(st);
-      int left = 0;  // blocks of this stream
-      for (int n = 0; n < cnt; ++n) left += r.has(n) ? 1 : 0;
+      const int left = r.count;
       const uint32_t q_lo = (smem_u32(sQ + (plan.alternate ? 0 : st) * LL::kQBytes) >> 4) | (1u << 16);
       const uint32_t ring_lo = smem_u32(sStage) >> 4;
       const uint32_t s_base = tmem + 2 * kBlk * st, o_base = tmem + kColO + kD * st;
@@ -296,8 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x_lo = q.first + ta, x_hi = q.first + tb - 1;
     const uint64_t sc2 = f32x2(a.scale_log2, a.scale_log2);
     const Range r = range_of(st);
-    int left = 0;  // blocks of this stream
-    for (int n = 0; n < cnt; ++n) left += r.has(n) ? 1 : 0;
+    const int left = r.count;
     float m_use = -INFINITY, l_run = 0.f;
     int done = 0;
     bool ok = true;
@@ -337,8 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return max3(fmaxf(pm[0], pm[1]), pm[2], pm[3]) * a.scale_log2;
     };
     uint32_t x[kBlk], pk[32];
-    for (int n = 0; n < cnt; ++n) {
-      if (!r.has(n)) continue;
+    for (int n = r.begin; n < r.end; n += r.step) {
       take(n, done, x);
       if (!ok) break;
       const float m_blk = maximum(x);
@@ -346,6 +354,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (m_blk > m_use + 8.f) {  // also from -inf, the first visible key
         corr = ex2(m_use - m_blk);
         m_use = m_blk;
+      }
+      // P = 2^(s scale - m), packed over the buffer's first 32 columns
+      const float base = m_use == -INFINITY ? 0.f : m_use;  // a row with nothing to see so far
+      const uint64_t nm2 = f32x2(-base, -base);
+      uint64_t ls[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        float xa, xb;
+        f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sc2, nm2), xa, xb);
+        const float pa = ex2(xa), pb = ex2(xb);
+        ls[c & 3] = add_f32x2(ls[c & 3], f32x2(pa, pb));
+        pk[c] = pack2<kFmt>(pa, pb);
       }
       if (done > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
         // O holds the products up to the block before, the latest that may
@@ -367,18 +387,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_store<kChunk>(o_col + c0, rr);
         }
       }
-      // P = 2^(s scale - m), packed over the buffer's first 32 columns
-      const float base = m_use == -INFINITY ? 0.f : m_use;  // a row with nothing to see so far
-      const uint64_t nm2 = f32x2(-base, -base);
-      uint64_t ls[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        float xa, xb;
-        f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sc2, nm2), xa, xb);
-        const float pa = ex2(xa), pb = ex2(xb);
-        ls[c & 3] = add_f32x2(ls[c & 3], f32x2(pa, pb));
-        pk[c] = pack2<kFmt>(pa, pb);
-      }
       LN_TMEM_ST32(tmem + lane_base + kBlk * (2 * st + (done & 1)), pk);
       tmem_wait_st();
       tc_fence_before();
@@ -393,39 +401,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
       const int h = f * a.G + row % a.G;
-      constexpr int kChunk = kD < 32 ? kD : 32;
       const int part = plan.alternate ? 2 * split + st : split;
       const int64_t prow = (((int64_t)part * a.S + s) * a.nq_max + i) * a.H + h;
+      if (plan.parts > 1) {
+        constexpr int kChunk = kD < 32 ? kD : 32;
 #pragma unroll 1
-      for (int c0 = 0; c0 < kD; c0 += kChunk) {
-        uint32_t rr[kChunk];
-        if (done > 0) {
-          tmem_load<kChunk>(o_col + c0, rr);
-          tmem_wait_ld();
-        } else {
+        for (int c0 = 0; c0 < kD; c0 += kChunk) {
+          uint32_t rr[kChunk];
+          if (done > 0) {
+            tmem_load<kChunk>(o_col + c0, rr);
+            tmem_wait_ld();
+          } else {
 #pragma unroll
-          for (int c = 0; c < kChunk; ++c) rr[c] = 0;
-        }
-        if (row_ok) {
-          if (plan.parts > 1) {
+            for (int c = 0; c < kChunk; ++c) rr[c] = 0;
+          }
+          if (row_ok) {
             float4* o = reinterpret_cast<float4*>(plan.part_out + prow * kD + c0);
 #pragma unroll
             for (int c = 0; c < kChunk; c += 4)
               o[c / 4] = make_float4(__uint_as_float(rr[c]) * inv, __uint_as_float(rr[c + 1]) * inv,
                                      __uint_as_float(rr[c + 2]) * inv, __uint_as_float(rr[c + 3]) * inv);
-          } else {
-            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
-                                                ((q.q0 + i) * a.H + h) * (int64_t)kD + c0);
-#pragma unroll
-            for (int c = 0; c < kChunk; c += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack2<kFmt>(__uint_as_float(rr[c + 2 * e]) * inv, __uint_as_float(rr[c + 2 * e + 1]) * inv);
-              o[c / 8] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
           }
         }
+      } else {
+        // this tile's queries are read: its last product is done
+        store_rows<kFmt, kD>(sQ + st * LL::kQBytes, o_col, done > 0, inv, 32 * (warp & 3), lane,
+                             static_cast<uint16_t*>(a.out) + ((q.q0 + i) * a.H + h) * (int64_t)kD, row_ok);
       }
       if (row_ok) {
         const float lse2 = l_run > 0.f ? m_use + log2f(l_run) : -INFINITY;

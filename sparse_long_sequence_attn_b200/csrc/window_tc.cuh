@@ -124,6 +124,57 @@ __device__ __forceinline__ void mbar_arrive_if(uint32_t leader, uint64_t* bar) {
       : "memory");
 }
 
+// A warp's 32 rows of an accumulator (TMEM columns acc.., scaled) to global
+// memory in the 16-bit format, through its own rows of `tile`, an operand tile
+// (128 rows, swizzled panels) that nothing reads any more: written a row per
+// lane, read back a whole row per group of lanes.  (Stores of 16 bytes a lane to
+// 32 different rows took 3000 cycles of a CTA at D = 64, 6000 at D = 128.)
+// dst: the lane's row; rows without live are not written.  any = false: zeros.
+template <int kFmt, int kD>
+__device__ __forceinline__ void store_rows(uint8_t* tile, uint32_t acc, bool any, float scale, int row0, int lane,
+                                           uint16_t* dst, bool live) {
+  using LL = Panels<kD>;
+  constexpr int kCpr = LL::kRowBytes / 16, kRow16 = kD / 8;  // 16-byte chunks of a panel row, of a row
+  constexpr int kChunk = kD < 32 ? kD : 32;
+  auto at = [&](int r, int c) -> uint4* {
+    const int cc = c % kCpr;
+    const int sw = LL::kRowBytes == 128 ? (r & 7) : LL::kRowBytes == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1);
+    return reinterpret_cast<uint4*>(tile + (c / kCpr) * kTile * LL::kRowBytes + r * LL::kRowBytes + ((cc ^ sw) << 4));
+  };
+#pragma unroll
+  for (int c0 = 0; c0 < kD; c0 += kChunk) {
+    uint32_t rr[kChunk];
+    if (any) {
+      if constexpr (kChunk == 32) {
+        LN_TMEM_LD32(acc + c0, rr);
+      } else {
+        LN_TMEM_LD16(acc + c0, rr);
+      }
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int c = 0; c < kChunk; ++c) rr[c] = 0;
+    }
+#pragma unroll
+    for (int c = 0; c < kChunk; c += 8) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = pack2<kFmt>(__uint_as_float(rr[c + 2 * e]) * scale, __uint_as_float(rr[c + 2 * e + 1]) * scale);
+      *at(row0 + lane, (c0 + c) / 8) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  __syncwarp();
+  const uint32_t mask = __ballot_sync(0xffffffffu, live);
+  const uint64_t mine = reinterpret_cast<uint64_t>(dst);
+#pragma unroll 4
+  for (int r0 = 0; r0 < 32; r0 += 32 / kRow16) {
+    const int r = r0 + lane / kRow16, c = lane % kRow16;
+    const uint64_t to = __shfl_sync(0xffffffffu, mine, r);
+    if ((mask >> r) & 1) reinterpret_cast<uint4*>(to)[c] = *at(row0 + r, c);
+  }
+}
+
 // Adds bytes to the barrier's current phase without arriving.
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
