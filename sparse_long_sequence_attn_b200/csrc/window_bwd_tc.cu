@@ -26,7 +26,8 @@
 // accumulators of one tile fill the rest of TMEM, and the slots take
 // alternate blocks.
 // Warps 0-3 and 4-7 compute, warp 8 loads (TMA; its lanes fetch lse and
-// delta), warp 9 issues.  Every wait is bounded.
+// delta), warps 9 and 10 issue, one for each tile (one tile: warp 9 alone, as
+// both slots add to the same accumulators).  Every wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -43,7 +44,7 @@ namespace longnet {
 namespace wb {
 using namespace wt;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kTma = 8, kMma = 9;  // warps
 constexpr int kBlk = 64;           // streamed rows
 constexpr uint32_t kTmemCols = 512, kColAcc = 256;
@@ -69,6 +70,11 @@ struct __align__(64) BMaps {
 struct BPlan {
   int tokens;    // of a tile (query-centric) or of a block (key-centric)
   FarPlan far;
+};
+
+struct Run {
+  int begin, end, step, count;
+  __device__ __forceinline__ bool has(int n) const { return n >= begin && n < end; }  // of a run of step 1
 };
 
 // P and dS of 32 streamed rows for this thread's tile row, packed in pairs:
@@ -161,15 +167,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     bl = blocks_of<kBlk>(a, first, end - 1);
     cnt = bl.count;
   }
-  auto active = [&](int st, int n) -> bool {
-    if (kTiles == 1) return (n & 1) == st;
-    if (kKeys) {
-      const int jt = first + st * kTile, b0 = i0 + n * tok;
-      const int b1 = b0 + tok < i1 ? b0 + tok : i1;
-      return jt < N && b1 > jt && (jt < a.sinks || b0 - a.window < jt + kTile - 1);
+  // the blocks of slot st: a run of those streamed, or every second one
+  auto run_of = [&](int st) {
+    Run r = {0, 0, 1, 0};
+    if (kTiles == 1) {
+      r = {st, cnt, 2, (cnt + 1 - st) / 2};
+      return r;
     }
-    const int t0 = first + st * tok, t1 = t0 + tok < N ? t0 + tok : N, j0 = bl.at(n) * kBlk;
-    return t0 < t1 && j0 < t1 && (j0 < a.sinks || j0 + kBlk - 1 > t0 - a.window);
+    if (kKeys) {
+      const int jt = first + st * kTile;
+      if (jt < N) {
+        r.begin = jt > i0 ? (jt - i0) / tok : 0;  // the first with a token at or after the tile's first key
+        // and up to the last whose first token's window reaches the tile's last key
+        const int64_t reach = (int64_t)jt + kTile - 1 + a.window - i0;
+        const int64_t end = jt < a.sinks ? cnt : reach <= 0 ? 0 : (reach + tok - 1) / tok;
+        r.end = end < cnt ? (int)end : cnt;
+      }
+    } else {
+      const int t0 = first + st * tok, t1 = t0 + tok < N ? t0 + tok : N;
+      if (t0 < t1) {
+        // (with sinks, also the few blocks between them and the tile's window
+        // that only the other tile sees, all masked)
+        const int low = t0 < a.window ? 0 : (t0 - a.window + 1) / kBlk;
+        r.begin = a.sinks > 0 ? 0 : bl.n_sink + low - bl.win0;
+        r.end = bl.n_sink + (t1 - 1) / kBlk - bl.win0 + 1;
+      }
+    }
+    r.count = r.end > r.begin ? r.end - r.begin : 0;
+    return r;
   };
 
   uint8_t* sStage = smem + LL::kStage0;
@@ -184,19 +209,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_s + 7);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(bar_tile, 1);
     for (int i = 0; i < S; ++i) {
       mbar_init(bar_full + i, 32);  // the loading warp's lanes, and the TMA bytes
-      mbar_init(bar_empty + i, 1);
+      mbar_init(bar_empty + i, kTiles);  // the issuing warps
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_s + i, 1);
       mbar_init(bar_p + i, 128);
       mbar_init(bar_acc + i, 1);
     }
-    mbar_init(bar_drain, 1);
+    mbar_init(bar_drain, kTiles);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -221,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   Waiter wt{abort_flag, a.status, kWaitLimitNs};
   auto tile_ptr = [&](int st, int which) { return smem + (st * 2 + which) * LL::kTileBytes; };
 
@@ -275,96 +300,110 @@ __global__ void __launch_bounds__(kThreads, 1)
     // drain: every issued load has landed before the CTA may exit
     if (lane == 0) {
       if (cnt > 0 && !mbar_wait(bar_tile, 0, kWaitLimitNs)) record_status(a.status, kStatusTimeout);
-      for (int n = issued > S ? issued - S : 0; n < issued && ok; ++n)
+      for (int n = issued > S ? issued - S : 0; n < issued; ++n)
         if (!mbar_wait(bar_full + (n % S), (n / S) & 1, kWaitLimitNs)) {
           record_status(a.status, kStatusTimeout);
           break;
         }
     }
-  } else if (warp == kMma) {
+  } else if (warp >= kMma) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0 && cnt > 0) {
+    if (cnt > 0 && warp < kMma + kTiles) {
       constexpr uint32_t kIdScore = idesc_f16kind(kTile, kBlk, false, kFmt);  // 128 x 64, B K-major
       constexpr uint32_t kIdGrad = idesc_f16kind(kTile, kD, true, kFmt);      // 128 x D, B MN-major
       constexpr uint32_t lbo_mn = ((uint32_t)kBlkPanel >> 4) << 16;           // panel stride along D
       constexpr uint32_t kStep16 = 16 * LL::kRowBytes >> 4;                   // 16 rows of an MN-major operand
-      auto stage_lo = [&](int n) -> uint32_t { return smem_u32(sStage + (n % S) * LL::kStageBytes) >> 4; };
-      auto scores = [&](int st, int n) {
-        const uint32_t b_lo = stage_lo(n);
+      const int st = warp - kMma;  // the tile
+      const uint32_t leader = elect_leader();
+      const Run r = run_of(st);
+      const uint32_t t_lo[2] = {(smem_u32(tile_ptr(st, 0)) >> 4) | (1u << 16), (smem_u32(tile_ptr(st, 1)) >> 4) | (1u << 16)};
+      const uint32_t ring_lo = smem_u32(sStage) >> 4;
+      const uint32_t acc = tmem + kColAcc + (kTiles == 2 ? (kKeys ? 2 : 1) * kD * st : 0);
+      // S and dP of the block in `stage` into slot `slot`
+      auto scores = [&](int stage, int slot) {
+        tc_fence_after();
+        const uint32_t b_lo = (ring_lo + stage * (LL::kStageBytes >> 4)) | (1u << 16);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const uint32_t t_lo = smem_u32(tile_ptr(kTiles == 2 ? st : 0, w)) >> 4;
+        for (int w = 0; w < 2; ++w)
 #pragma unroll
           for (int pn = 0; pn < kPanels; ++pn)
 #pragma unroll
             for (int kk = 0; kk < LL::kPanelElems / 16; ++kk)
-              mma_ss(tmem + 128 * st + 64 * w, desc_from(((t_lo + pn * (kTilePanel >> 4)) | (1u << 16)) + kk * 2, kDescHi),
-                     desc_from(((b_lo + w * (LL::kBlkBytes >> 4) + pn * (kBlkPanel >> 4)) | (1u << 16)) + kk * 2, kDescHi),
-                     kIdScore, (pn > 0 || kk > 0) ? 1u : 0u);
-        }
-        tc_commit(bar_s + st);
+              mma_ss_if(leader, tmem + 128 * slot + 64 * w, desc_from(t_lo[w] + pn * (kTilePanel >> 4) + kk * 2, kDescHi),
+                        desc_from(b_lo + w * (LL::kBlkBytes >> 4) + pn * (kBlkPanel >> 4) + kk * 2, kDescHi), kIdScore,
+                        (pn > 0 || kk > 0) ? 1u : 0u);
+        tc_commit_if(leader, bar_s + slot);
       };
-      int pending[2] = {-1, -1}, done[2] = {0, 0}, left[2] = {0, 0};
-      for (int n = 0; n < cnt; ++n)
-        for (int st = 0; st < 2; ++st) left[st] += active(st, n) ? 1 : 0;
-      auto product = [&](int st) -> bool {
-        const int n = pending[st];
-        pending[st] = -1;
-        if (!wt.wait(bar_p + st, done[st] & 1)) return false;
+      // the gradient products of the block in `stage`, P and dS in slot `slot`
+      auto grads = [&](int stage, int slot, bool fresh) {
         tc_fence_after();
-        const uint32_t b0 = stage_lo(n), b1 = b0 + (LL::kBlkBytes >> 4);
-        const uint32_t acc = tmem + kColAcc + (kTiles == 2 ? (kKeys ? 2 : 1) * kD * st : 0);
-        const bool fresh = kTiles == 2 ? done[st] == 0 : n == 0;
+        const uint32_t b0 = (ring_lo + stage * (LL::kStageBytes >> 4)) | lbo_mn, b1 = b0 + (LL::kBlkBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < kBlk / 16; ++kk) {
           const uint32_t add = fresh && kk == 0 ? 0u : 1u;
           if (kKeys) {
             // dV += P^T dout, dK += dS^T Q
-            mma_ts(acc, tmem + 128 * st + kk * 8, desc_from((b1 | lbo_mn) + kk * kStep16, kDescHi), kIdGrad, add);
-            mma_ts(acc + kD, tmem + 128 * st + 64 + kk * 8, desc_from((b0 | lbo_mn) + kk * kStep16, kDescHi), kIdGrad,
-                   add);
+            mma_ts_if(leader, acc, tmem + 128 * slot + kk * 8, desc_from(b1 + kk * kStep16, kDescHi), kIdGrad, add);
+            mma_ts_if(leader, acc + kD, tmem + 128 * slot + 64 + kk * 8, desc_from(b0 + kk * kStep16, kDescHi), kIdGrad,
+                      add);
           } else {
             // dQ += dS K
-            mma_ts(acc, tmem + 128 * st + 64 + kk * 8, desc_from((b0 | lbo_mn) + kk * kStep16, kDescHi), kIdGrad, add);
+            mma_ts_if(leader, acc, tmem + 128 * slot + 64 + kk * 8, desc_from(b0 + kk * kStep16, kDescHi), kIdGrad, add);
           }
         }
-        if (++done[st] == left[st] && kTiles == 2) tc_commit(bar_acc + st);
-        return true;
       };
-      bool ok = wt.wait(bar_tile, 0);
-      for (int n = 0; n <= cnt && ok; ++n) {
-        bool on[2] = {false, false}, due[2] = {pending[0] >= 0, pending[1] >= 0};
-        if (n < cnt) {
-          ok = wt.wait(bar_full + n % S, (n / S) & 1);
+      bool ok = wt.wait_warp(bar_tile, 0);
+      if (kTiles == 2) {
+        int stage = 0, phase = 0, done = 0;
+        for (int n = 0; n < cnt && ok; ++n) {
+          // (a block that only the other tile uses is released once it is
+          // there, so that this warp stays within a ring of the other)
+          ok = wt.wait_warp(bar_full + stage, phase);
           if (!ok) break;
-          tc_fence_after();
-          on[0] = active(0, n);
-          on[1] = active(1, n);
+          if (r.has(n)) {
+            scores(stage, st);
+            ok = wt.wait_warp(bar_p + st, done & 1);
+            if (!ok) break;
+            grads(stage, st, done == 0);
+            tc_commit_if(leader, bar_empty + stage);
+            if (++done == r.count) tc_commit_if(leader, bar_acc + st);
+          } else {
+            mbar_arrive_if(leader, bar_empty + stage);
+          }
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
-        // a slot with nothing due starts its scores before the other's P and
-        // dS are waited for
-        for (int st = 0; st < 2; ++st)
-          if (on[st] && !due[st]) {
-            scores(st, n);
-            pending[st] = n;
+      } else {
+        // a block's scores are issued before the P and dS of the one before
+        // are waited for
+        int stage = 0, before = 0, phase = 0;
+        for (int n = 0; n <= cnt && ok; ++n) {
+          if (n < cnt) {
+            ok = wt.wait_warp(bar_full + stage, phase);
+            if (!ok) break;
+            scores(stage, n & 1);
           }
-        for (int st = 0; st < 2 && ok; ++st)
-          if (due[st]) {
-            ok = product(st);
-            if (ok && on[st]) {
-              scores(st, n);
-              pending[st] = n;
-            }
+          if (n > 0) {
+            ok = wt.wait_warp(bar_p + ((n - 1) & 1), ((n - 1) >> 1) & 1);
+            if (!ok) break;
+            grads(before, (n - 1) & 1, n == 1);
+            tc_commit_if(leader, bar_empty + before);
           }
-        if (!ok) break;
-        if (n > 0) tc_commit(bar_empty + (n - 1) % S);
-      }
-      if (ok && kTiles == 1) {
-        tc_commit(bar_acc + 0);
-        tc_commit(bar_acc + 1);
+          before = stage;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (ok) {
+          tc_commit_if(leader, bar_acc + 0);
+          tc_commit_if(leader, bar_acc + 1);
+        }
       }
       // drain: all issued MMAs complete before TMEM is released
-      tc_commit(bar_drain);
+      tc_commit_if(leader, bar_drain);
       if (!mbar_wait(bar_drain, 0, kWaitLimitNs)) record_status(a.status, kStatusTimeout);
     }
   } else {
@@ -385,10 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const uint64_t sc2 = f32x2(a.scale_log2, a.scale_log2);
     const uint64_t nl_row = f32x2(-lse2, -lse2), nd_row = f32x2(-delta, -delta);
+    const Run r = run_of(st);
     int done = 0;
     bool ok = true;
-    for (int n = 0; n < cnt && ok; ++n) {
-      if (!active(st, n)) continue;
+    for (int n = r.begin; n < r.end && ok; n += r.step) {
       const float* sl = reinterpret_cast<const float*>(sStage + (n % S) * LL::kStageBytes + 2 * LL::kBlkBytes);
       // the columns [lo, hi) that pair with this row, and below sk
       int lo, hi, sk;
@@ -435,7 +474,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && any) ok = wt.wait_warp(bar_acc + st, 0);
     if (ok) {
       tc_fence_after();
-      constexpr int kChunk = kD < 32 ? kD : 32;
       const bool partial = kKeys && ftile < plan.far.sink_tiles;
       // key-centric with two tiles: a warpgroup writes both gradients of its
       // tile; with one tile, the first dV and the second dK
@@ -447,11 +485,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t acc = tmem + lane_base + kColAcc + (kTiles == 2 ? (kKeys ? 2 : 1) * kD * st : 0) + w * kD;
         uint16_t* dst = kKeys ? static_cast<uint16_t*>(w == 0 ? g.dv : g.dk) + (((int64_t)s * N + j) * a.Hkv + f) * kD
                               : static_cast<uint16_t*>(g.dq) + (((int64_t)s * N + i) * a.H + h) * kD;
+        if (!partial) {
+          // through an operand tile that nothing reads any more
+          store_rows<kFmt, kD>(tile_ptr(kTiles == 2 ? st : 0, w), acc, any, sc, 32 * (warp & 3), lane, dst, row_ok);
+          continue;
+        }
         const int slot_no = far < 0 ? 0 : 1 + far;
         // [S Hkv][sink tile][slot][dK, dV][tile rows][D]
         float* part = g.partial + ((((int64_t)blockIdx.y * plan.far.sink_tiles + ftile) * (plan.far.chunks + 1) + slot_no) * 2 +
                                    (w == 0 ? 1 : 0)) * (int64_t)(kTiles * kTile * kD) +
                       (int64_t)(j - first) * kD;
+        constexpr int kChunk = kD < 32 ? kD : 32;
 #pragma unroll 1
         for (int c0 = 0; c0 < kD; c0 += kChunk) {
           uint32_t rr[kChunk];
@@ -462,23 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < kChunk; ++c) rr[c] = 0;
           }
-          if (partial) {
-            float4* o = reinterpret_cast<float4*>(part + c0);
+          float4* o = reinterpret_cast<float4*>(part + c0);
 #pragma unroll
-            for (int c = 0; c < kChunk; c += 4)
-              o[c / 4] = make_float4(__uint_as_float(rr[c]) * sc, __uint_as_float(rr[c + 1]) * sc,
-                                     __uint_as_float(rr[c + 2]) * sc, __uint_as_float(rr[c + 3]) * sc);
-          } else if (row_ok) {
-            uint4* o = reinterpret_cast<uint4*>(dst + c0);
-#pragma unroll
-            for (int c = 0; c < kChunk; c += 8) {
-              uint32_t v[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                v[e] = pack2<kFmt>(__uint_as_float(rr[c + 2 * e]) * sc, __uint_as_float(rr[c + 2 * e + 1]) * sc);
-              o[c / 8] = make_uint4(v[0], v[1], v[2], v[3]);
-            }
-          }
+          for (int c = 0; c < kChunk; c += 4)
+            o[c / 4] = make_float4(__uint_as_float(rr[c]) * sc, __uint_as_float(rr[c + 1]) * sc,
+                                   __uint_as_float(rr[c + 2]) * sc, __uint_as_float(rr[c + 3]) * sc);
         }
       }
     }
