@@ -264,6 +264,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_4d(tile_ptr(st, w) + pn * kTilePanel, &maps.t[w], bar_tile, LL::kPanelElems * pn,
                         kKeys ? f : f * G, first + st * (kKeys ? kTile : tok), s);
     }
+    // key-centric: -lse (log2 domain) and -delta of a block's rows, fetched a
+    // block ahead (their latency would otherwise stand between the loads);
+    // zero where there is no row
+    float l2[2] = {0.f, 0.f}, dl[2] = {0.f, 0.f};
+    const int c_tok[2] = {lane / G, (lane + 32) / G}, c_head[2] = {lane % G, (lane + 32) % G};
+    auto fetch = [&](int n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = i0 + n * tok + c_tok[e];
+        const bool in = n < cnt && c_tok[e] < tok && i < N;
+        const int64_t idx = ((int64_t)s * a.H + f * G + c_head[e]) * N + i;
+        l2[e] = in ? a.lse[idx] : 0.f;
+        dl[e] = in ? g.delta[idx] : 0.f;
+      }
+    };
+    if (kKeys) fetch(0);
     int issued = 0;
     for (int n = 0; n < cnt && ok; ++n) {
       const int st = n % S;
@@ -282,19 +298,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         kKeys ? f * G : f, at, s);
       }
       if (kKeys) {
-        // -lse (log2 domain) and -delta of the block's rows; zero where there is none
         float* sl = reinterpret_cast<float*>(stage + 2 * LL::kBlkBytes);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int c = lane + 32 * e, i = at + c / G;
-          const bool in = c < tok * G && i < N;
-          const int64_t idx = in ? ((int64_t)s * a.H + f * G + c % G) * N + i : 0;
-          sl[c] = in ? -a.lse[idx] * kLog2e : 0.f;
-          sl[kBlk + c] = in ? -g.delta[idx] : 0.f;
+          sl[lane + 32 * e] = -l2[e] * kLog2e;
+          sl[kBlk + lane + 32 * e] = -dl[e];
         }
       }
       __syncwarp();  // the bytes are expected before the phase can complete
       mbar_arrive(bar_full + st);
+      if (kKeys) fetch(n + 1);
       issued = n + 1;
     }
     // drain: every issued load has landed before the CTA may exit
