@@ -587,27 +587,6 @@ Sizes sizes_of(const AttnArgs& a, bool weights) {
   return z;
 }
 
-template <typename... P, typename... V>
-int launch_after(void (*fn)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, V&&... args) {
-  // programmatic dependent launch: the kernel's set-up overlaps the end of the
-  // launch before it, whose results it waits for (griddepcontrol.wait)
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fn, args...) != cudaSuccess) {
-    cudaGetLastError();
-    return LONGNET_ERR_CUDA;
-  }
-  return LONGNET_OK;
-}
-
 template <int kFmt, int kD>
 int launch_typed(const AttnArgs& a, float* workspace, float* weights, cudaStream_t stream) {
   using LL = L<kD>;

@@ -22,8 +22,12 @@
 // TMEM: two 64-column score buffers per tile, so that a tile's next scores are
 // there when its softmax asks for them, and two D-column accumulators.
 // With fewer rows than one tile per key/value head (short chunks over a long
-// cache) both streams take the same tile and alternate blocks, and the keys
-// are split over CTAs; the parts are joined by combine_kernel.
+// cache) both streams take the same tile and alternate blocks.  A paged call
+// with few row tiles is cut along the keys too: into pieces of nearly equal
+// runs of blocks, as many as SMs, which each CTA works out for itself from the
+// lengths on the device; join_kernel adds them.  (Three chunks of up to 1024
+// tokens over 8K keys, 96 row-tile pairs of very different lengths: 141 us
+// uncut.)
 // Slots past a sequence's keys may hold anything: their scores are masked
 // before use and their value rows are overwritten with zeros in shared memory.
 // Every wait is bounded; on a timeout the kernel records the status word,
@@ -49,6 +53,7 @@ constexpr int kTma = 8, kMma = 9;  // warps; kMma + 1 issues for the second stre
 constexpr int kBlk = 64;           // keys of a block
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;  // after two score buffers per stream
+constexpr int kSms = 148;
 
 template <int kD>
 struct L : Panels<kD> {
@@ -74,6 +79,57 @@ struct Range {
   }
 };
 
+constexpr int kMaxItems = 320;  // ten per lane of the numbering warp
+constexpr int kMinRun = 8;      // blocks of a piece: shorter ones cost more in joining than they spread
+
+// base[i] = pieces of the items before i, of one head, by one warp.  The run
+// length is the least, in steps of an eighth, for which all heads' pieces fit
+// one CTA per SM (or, with more items than SMs, for which none is cut).
+__device__ __forceinline__ void number_pieces(const AttnArgs& a, const Plan& plan, int* base, int lane) {
+  int c[kMaxItems / 32], sum = 0, some = 0;
+#pragma unroll
+  for (int k = 0; k < kMaxItems / 32; ++k) {
+    const int it = lane + 32 * k;
+    c[k] = 0;
+    if (it < plan.items) {
+      const Seq q = seq_of(a, it / plan.pairs);
+      const int t0 = (it % plan.pairs) * 2 * plan.tokens, t1 = t0 + 2 * plan.tokens < q.nq ? t0 + 2 * plan.tokens : q.nq;
+      if (t0 < q.nq) c[k] = blocks_of<kBlk>(a, q.first + t0, q.first + t1 - 1).count;
+      if (t0 < q.nq && c[k] == 0) c[k] = 1;  // rows that see nothing are written too
+    }
+    sum += c[k];
+    some += c[k] > 0 ? 1 : 0;
+  }
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  some = __reduce_add_sync(0xffffffffu, some);
+  const int limit = (some * a.Hkv > kSms ? some * a.Hkv : kSms) / a.Hkv;  // pieces of one head
+  int run = limit > 0 ? (sum + limit - 1) / limit : 1;
+  if (run < kMinRun) run = kMinRun;
+  while (true) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kMaxItems / 32; ++k) n += (c[k] + run - 1) / run;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (n <= limit) break;  // at the latest when no item is cut
+    run += run / 8;
+  }
+  int before = 0;
+#pragma unroll
+  for (int k = 0; k < kMaxItems / 32; ++k) {
+    const int n = (c[k] + run - 1) / run;
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const int it = lane + 32 * k;
+    if (it <= plan.items) base[it] = before + x - n;
+    before += __shfl_sync(0xffffffffu, x, 31);
+  }
+  if (plan.items == kMaxItems && lane == 0) base[kMaxItems] = before;
+}
+
 template <int kFmt, int kD, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Maps maps, const Plan plan) {
@@ -83,21 +139,55 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kDescHi = LL::kDescHi;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int s = blockIdx.y / a.Hkv, f = blockIdx.y % a.Hkv;
+  uint8_t* sQ = smem;
+  uint8_t* sStage = smem + 2 * LL::kQBytes;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  // the join may be scheduled; and what the launch before this one wrote is
+  // read only from here on
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tpt = plan.tokens;  // tokens of a row tile
+  const bool alternate = kPaged && plan.alternate;
+  int s, f, pair, slot = 0, piece = 0, pieces = 1;
+  if (kPaged && plan.items) {
+    // this CTA's piece: of `pieces` equal runs of an item's blocks, run `piece`
+    int* base = reinterpret_cast<int*>(sStage);
+    if (warp == 0) number_pieces(a, plan, base, lane);
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int i = threadIdx.x; i <= plan.items; i += kThreads) plan.base[i] = base[i];
+    slot = blockIdx.x;
+    int lo = 0, hi = plan.items;
+    const bool none = slot >= base[hi] * a.Hkv;
+    while (!none && hi - lo > 1) {  // the last item with base Hkv <= slot
+      const int mid = (lo + hi) >> 1;
+      if (base[mid] * a.Hkv <= slot) lo = mid;
+      else hi = mid;
+    }
+    pieces = base[lo + 1] - base[lo];
+    const int in = slot - base[lo] * a.Hkv;
+    __syncthreads();  // base is read: the ring may take its place
+    if (none) return;
+    s = lo / plan.pairs;
+    pair = lo % plan.pairs;
+    f = in / pieces;
+    piece = in % pieces;
+  } else {
+    s = blockIdx.y / a.Hkv;
+    f = blockIdx.y % a.Hkv;
+    pair = (int)gridDim.x - 1 - blockIdx.x;  // the longest first
+  }
   const Seq q = seq_of(a, s);
-  const int split = blockIdx.x % plan.splits;
-  const int pair = (int)(gridDim.x / plan.splits) - 1 - blockIdx.x / plan.splits;  // the longest first
-  const int tpt = plan.tokens;                                                      // tokens of a row tile
-  const int t0 = plan.alternate ? 0 : pair * 2 * tpt;
-  if (t0 >= q.nq) return;  // whole CTA, before any barrier or TMEM use
-  const int t1 = t0 + (plan.alternate ? tpt : 2 * tpt) < q.nq ? t0 + (plan.alternate ? tpt : 2 * tpt) : q.nq;
+  const int t0 = pair * 2 * tpt;  // alternate: pair 0
+  if (t0 >= q.nq) return;         // whole CTA, before any barrier or TMEM use
+  const int t1 = t0 + (alternate ? tpt : 2 * tpt) < q.nq ? t0 + (alternate ? tpt : 2 * tpt) : q.nq;
   const BlockList bl = blocks_of<kBlk>(a, q.first + t0, q.first + t1 - 1);
-  const int per = (bl.count + plan.splits - 1) / plan.splits;
-  const int n0 = split * per < bl.count ? split * per : bl.count;
+  const int per = (bl.count + pieces - 1) / pieces;
+  const int n0 = piece * per < bl.count ? piece * per : bl.count;
   const int cnt = n0 + per < bl.count ? per : bl.count - n0;  // blocks [n0, n0 + cnt) of the list
   auto block_key = [&](int n) { return bl.at(n0 + n) * kBlk; };
   // tokens [ta, tb) of stream st, empty when it has none
-  auto tok_begin = [&](int st) { return plan.alternate ? t0 : t0 + st * tpt; };
+  auto tok_begin = [&](int st) { return alternate ? t0 : t0 + st * tpt; };
   auto tok_end = [&](int st) {
     const int e = tok_begin(st) + tpt;
     return e < t1 ? e : t1;
@@ -106,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Range r;
     const int tb = tok_begin(st), te = tok_end(st);
     const int lo = q.first + tb, low = a.window == 0 || lo < a.window ? 0 : (lo - a.window + 1) / kBlk;
-    if (plan.alternate) {
+    if (alternate) {
       r.begin = st;
       r.end = cnt;
       r.step = 2;
@@ -125,10 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // of a stream further on.  Item n of the ring holds what that step takes:
   // the values of block n (none for n < 0) and the keys of block n + ahead
   // (none past the last).
-  const int ahead = plan.alternate ? 4 : 2;
+  const int ahead = alternate ? 4 : 2;
 
-  uint8_t* sQ = smem;
-  uint8_t* sStage = smem + 2 * LL::kQBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + LL::kBars);
   uint64_t* bar_q = bars;
   uint64_t* bar_full = bars + 1;       // [S]
@@ -142,7 +230,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_s + 14);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(bar_q, 1);
     for (int i = 0; i < S; ++i) {
@@ -178,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kTma) {
     // ------------------------------------------------------------ loads
     bool ok = true;
-    const int qtiles = plan.alternate || t0 + tpt >= t1 ? 1 : 2;
+    const int qtiles = alternate || t0 + tpt >= t1 ? 1 : 2;
     if (cnt > 0 && lane == 0) {
       mbar_arrive_expect_tx(bar_q, (uint32_t)(qtiles * kPanels * tpt * a.G * LL::kRowBytes));
       for (int st = 0; st < qtiles; ++st)
@@ -242,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t leader = elect_leader();
       const Range r = range_of(st);
       const int left = r.count;
-      const uint32_t q_lo = (smem_u32(sQ + (plan.alternate ? 0 : st) * LL::kQBytes) >> 4) | (1u << 16);
+      const uint32_t q_lo = (smem_u32(sQ + (alternate ? 0 : st) * LL::kQBytes) >> 4) | (1u << 16);
       const uint32_t ring_lo = smem_u32(sStage) >> 4;
       const uint32_t s_base = tmem + 2 * kBlk * st, o_base = tmem + kColO + kD * st;
       int asked = 0, done = 0;   // blocks whose scores, whose P V are issued
@@ -401,9 +488,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
       const int h = f * a.G + row % a.G;
-      const int part = plan.alternate ? 2 * split + st : split;
-      const int64_t prow = (((int64_t)part * a.S + s) * a.nq_max + i) * a.H + h;
-      if (plan.parts > 1) {
+      const bool whole = !kPaged || (!alternate && pieces == 1);
+      const int64_t prow = ((int64_t)slot * 2 + st) * plan.slot_rows + row;
+      if (!whole) {
         constexpr int kChunk = kD < 32 ? kD : 32;
 #pragma unroll 1
         for (int c0 = 0; c0 < kD; c0 += kChunk) {
@@ -430,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (row_ok) {
         const float lse2 = l_run > 0.f ? m_use + log2f(l_run) : -INFINITY;
-        if (plan.parts > 1)
+        if (!whole)
           plan.part_lse[prow] = lse2;
         else if (a.lse)
           a.lse[lse_index(a, q, s, i, h)] = lse2 * kLn2;
@@ -445,55 +532,73 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of every row: out = sum_p 2^(lse_p - m) O_p / sum_p 2^(lse_p - m).
-// A warp per row; a row's parts are added in order.
+// Joins the pieces of every row: out = sum_p 2^(lse_p - m) O_p / sum_p 2^(lse_p - m).
+// A block per 32 rows of an item and head, a warp per row; a row's pieces (each
+// with both streams' halves when they alternate) are added in order.
 template <int kFmt, int kD>
-__global__ void __launch_bounds__(256) combine_kernel(const AttnArgs a, const float* part_out, const float* part_lse,
-                                                      int parts) {
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnArgs a, const Plan plan) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int64_t rows = (int64_t)a.S * a.nq_max * a.H;
-  if (row >= rows) return;
-  const int h = (int)(row % a.H), i = (int)((row / a.H) % a.nq_max), s = (int)(row / a.H / a.nq_max);
+  const int item = blockIdx.x / a.Hkv, f = blockIdx.x % a.Hkv;
+  const int pieces = plan.base[item + 1] - plan.base[item];
+  if (pieces == 0 || (!plan.alternate && pieces == 1)) return;  // no rows, or written by their CTA
+  const int s = item / plan.pairs, t0 = (item % plan.pairs) * 2 * plan.tokens;
   const Seq q = seq_of(a, s);
-  if (i >= q.nq) return;
-  float m = -INFINITY;
-  for (int p = lane; p < parts; p += 32) m = fmaxf(m, part_lse[p * rows + row]);
+  const int halves = plan.alternate ? 2 : 1, parts = halves * pieces;
+  const int64_t first = (int64_t)plan.base[item] * a.Hkv + f * pieces;
+  const int tokens = (2 / halves) * plan.tokens < q.nq - t0 ? (2 / halves) * plan.tokens : q.nq - t0;
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < tokens * a.G; r += gridDim.y * 8) {
+    const int in = r / a.G, g = r % a.G, st = in / plan.tokens, i = t0 + in, h = f * a.G + g;
+    const int at = (in - st * plan.tokens) * a.G + g;
+    auto row_of = [&](int p) {  // of part p: piece p / halves
+      return ((first + p / halves) * 2 + (halves == 2 ? (p & 1) : st)) * plan.slot_rows + at;
+    };
+    float m = -INFINITY;
+    for (int p = lane; p < parts; p += 32) m = fmaxf(m, plan.part_lse[row_of(p)]);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float base = m == -INFINITY ? 0.f : m;
-  constexpr int kE = kD / 32 > 0 ? kD / 32 : 1;  // values of a lane
-  const bool on = lane * kE < kD;
-  float acc[kE] = {}, sum = 0.f;
-  for (int p = 0; p < parts; ++p) {
-    const float l = part_lse[p * rows + row];
-    const float w = ex2(l - base);
-    sum += w;
-    if (on && w > 0.f) {
-      const float* src = part_out + (p * rows + row) * kD + lane * kE;
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float base = m == -INFINITY ? 0.f : m;
+    constexpr int kE = kD / 32 > 0 ? kD / 32 : 1;  // values of a lane
+    const bool on = lane * kE < kD;
+    float acc[kE] = {}, sum = 0.f;
+    for (int p0 = 0; p0 < parts; p0 += 32) {
+      const float wl = p0 + lane < parts ? ex2(plan.part_lse[row_of(p0 + lane)] - base) : 0.f;
+      const int n = parts - p0 < 32 ? parts - p0 : 32;
+#pragma unroll 4
+      for (int p = 0; p < n; ++p) {
+        const float w = __shfl_sync(0xffffffffu, wl, p);
+        sum += w;
+        if (on) {
+          const float* src = plan.part_out + row_of(p0 + p) * kD + lane * kE;
+          float t[kE];
+          if constexpr (kE == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            t[0] = v.x;
+            t[1] = v.y;
+            t[2] = v.z;
+            t[3] = v.w;
+          } else {
 #pragma unroll
-      for (int e = 0; e < kE; ++e) acc[e] = fmaf(w, src[e], acc[e]);
+            for (int e = 0; e < kE; ++e) t[e] = src[e];
+          }
+#pragma unroll
+          for (int e = 0; e < kE; ++e) acc[e] = fmaf(w, t[e], acc[e]);
+        }
+      }
     }
-  }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  if (on) {
-    uint16_t* o = static_cast<uint16_t*>(a.out) + ((q.q0 + i) * a.H + h) * (int64_t)kD + lane * kE;
-    if constexpr (kE == 1) {
-      o[0] = (uint16_t)pack2<kFmt>(acc[0] * inv, 0.f);
-    } else {
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    if (on) {
+      uint16_t* o = static_cast<uint16_t*>(a.out) + ((q.q0 + i) * a.H + h) * (int64_t)kD + lane * kE;
+      if constexpr (kE == 1) {
+        o[0] = (uint16_t)pack2<kFmt>(acc[0] * inv, 0.f);
+      } else {
 #pragma unroll
-      for (int e = 0; e < kE; e += 2)
-        *reinterpret_cast<uint32_t*>(o + e) = pack2<kFmt>(acc[e] * inv, acc[e + 1] * inv);
+        for (int e = 0; e < kE; e += 2)
+          *reinterpret_cast<uint32_t*>(o + e) = pack2<kFmt>(acc[e] * inv, acc[e + 1] * inv);
+      }
     }
+    if (lane == 0 && a.lse) a.lse[lse_index(a, q, s, i, h)] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
   }
-  if (lane == 0 && a.lse) a.lse[lse_index(a, q, s, i, h)] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
-}
-
-template <int kFmt, int kD>
-int combine(const AttnArgs& a, const float* po, const float* pl, int parts, cudaStream_t stream) {
-  const int64_t rows = (int64_t)a.S * a.nq_max * a.H;
-  combine_kernel<kFmt, kD><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(a, po, pl, parts);
-  return cudaGetLastError() == cudaSuccess ? LONGNET_OK : LONGNET_ERR_CUDA;
 }
 
 template <int kFmt, int kD>
@@ -510,10 +615,13 @@ int launch_typed(const AttnArgs& a, const Plan& plan, cudaStream_t stream) {
     cudaGetLastError();
     return LONGNET_ERR_CUDA;
   }
-  const int64_t pairs = plan.alternate ? 1 : ((int64_t)a.nq_max + 2 * plan.tokens - 1) / (2 * plan.tokens);
-  fn<<<dim3((unsigned)(pairs * plan.splits), (unsigned)(a.S * a.Hkv)), kThreads, LL::kSmem, stream>>>(a, maps, plan);
-  if (cudaGetLastError() != cudaSuccess) return LONGNET_ERR_CUDA;
-  return plan.parts > 1 ? combine<kFmt, kD>(a, plan.part_out, plan.part_lse, plan.parts, stream) : LONGNET_OK;
+  const dim3 grid = plan.items ? dim3((unsigned)plan.grid) : dim3((unsigned)plan.pairs, (unsigned)(a.S * a.Hkv));
+  int rc = launch_after(fn, grid, kThreads, LL::kSmem, stream, a, maps, plan);
+  if (rc || !plan.items) return rc;
+  // four rows a warp, at most
+  const int rows = (plan.alternate ? a.nq_max : 2 * plan.tokens) * a.G;
+  return launch_after(join_kernel<kFmt, kD>, dim3((unsigned)(plan.items * a.Hkv), (unsigned)((rows + 31) / 32)), 256, 0,
+                      stream, a, plan);
 }
 
 }  // namespace wt
@@ -529,45 +637,41 @@ bool window_tc_supports(const AttnArgs& a) {
        : (a.D == 16 ? FN<tc::kFmtBF16, 16>(__VA_ARGS__) : a.D == 32 ? FN<tc::kFmtBF16, 32>(__VA_ARGS__) \
           : a.D == 64 ? FN<tc::kFmtBF16, 64>(__VA_ARGS__) : FN<tc::kFmtBF16, 128>(__VA_ARGS__)))
 
-// The split of one call.  A contiguous call is never split (its row tiles fill
-// the GPU); a paged one is when its row tiles leave SMs idle: enough splits to
-// fill them once, of at least eight blocks each at the cache's capacity.
+// A contiguous call is never cut along the keys (its row tiles fill the GPU,
+// and training sequences are of one length); a paged one is when its row tiles
+// would not keep every SM busy twice over.
 WindowTcPlan window_tc_plan(const AttnArgs& a) {
   WindowTcPlan p;
   memset(&p, 0, sizeof(p));
   p.tokens = wt::kTile / a.G;
-  p.splits = 1;
-  p.parts = 1;
-  if (!a.cu_q) return p;
-  p.alternate = a.nq_max <= p.tokens;
-  const int64_t cap_blocks = (((int64_t)a.max_pages << a.page_shift) + wt::kBlk - 1) / wt::kBlk;
-  // blocks a row tile can visit
-  const int64_t reach = a.window ? ((int64_t)a.window + a.sinks + p.tokens * 2) / wt::kBlk + 2 : cap_blocks;
-  const int64_t blocks = reach < cap_blocks ? reach : cap_blocks;
-  const int64_t pairs = p.alternate ? 1 : ((int64_t)a.nq_max + 2 * p.tokens - 1) / (2 * p.tokens);
-  const int64_t ctas = pairs * a.S * a.Hkv;
-  int64_t splits = ctas >= 148 ? 1 : 148 / ctas;
-  if (splits > blocks / 8) splits = blocks / 8;
-  if (splits < 1) splits = 1;
-  if (splits > 64) splits = 64;
-  p.splits = (int)splits;
-  p.parts = (int)(p.alternate ? 2 * splits : splits);
+  p.alternate = a.cu_q && a.nq_max <= p.tokens && a.S <= wt::kMaxItems;
+  p.pairs = p.alternate ? 1 : (int)(((int64_t)a.nq_max + 2 * p.tokens - 1) / (2 * p.tokens));
+  const int64_t items = (int64_t)p.pairs * a.S;
+  if (!a.cu_q || items > wt::kMaxItems || (!p.alternate && items * a.Hkv >= 2 * wt::kSms)) return p;
+  p.items = (int)items;
+  p.grid = (int)(items * a.Hkv > wt::kSms ? items * a.Hkv : wt::kSms);
+  p.slot_rows = p.alternate ? a.nq_max * a.G : wt::kTile;
   return p;
 }
 
+namespace {
+int64_t round64(int64_t floats) { return (floats + 63) / 64 * 64; }  // 256 bytes
+}  // namespace
+
 int64_t window_tc_part_floats(const AttnArgs& a, const WindowTcPlan& p) {
-  return p.parts > 1 ? (int64_t)p.parts * a.S * a.nq_max * a.H * (a.D + 1) : 0;
+  if (!p.items) return 0;
+  const int64_t rows = (int64_t)p.grid * 2 * p.slot_rows;
+  return round64(p.items + 1) + round64(rows) + round64(rows * a.D);
 }
 
-int launch_window_fwd_tc(const AttnArgs& a, float* parts, cudaStream_t stream) {
+int launch_window_fwd_tc(const AttnArgs& a, float* workspace, cudaStream_t stream) {
   WindowTcPlan p = window_tc_plan(a);
-  p.part_out = parts;
-  p.part_lse = parts ? parts + (int64_t)p.parts * a.S * a.nq_max * a.H * a.D : nullptr;
+  if (p.items) {
+    p.base = reinterpret_cast<int*>(workspace);
+    p.part_lse = workspace + round64(p.items + 1);
+    p.part_out = p.part_lse + round64((int64_t)p.grid * 2 * p.slot_rows);
+  }
   return LN_TC_BY(wt::launch_typed, a, p, stream);
-}
-
-int launch_combine(const AttnArgs& a, const float* part_out, const float* part_lse, int parts, cudaStream_t stream) {
-  return LN_TC_BY(wt::combine, a, part_out, part_lse, parts, stream);
 }
 
 }  // namespace longnet

@@ -12,14 +12,19 @@
 
 namespace longnet {
 
-// How a forward call is cut.  tokens: tokens of a 128-row tile; alternate: one
-// row tile per key/value head, whose blocks the two streams take in turn;
-// splits: CTAs that share a row tile's blocks; parts: partial results of a
-// row, 1 when the kernel writes out itself.
+// How a forward call is cut.  tokens: of a 128-row tile; pairs: row-tile pairs
+// of the longest sequence (1 when alternate); alternate: one row tile per
+// key/value head, whose blocks the two streams take in turn.  items = 0: a CTA
+// per (sequence, head, pair).  Else the items, (sequence, pair) for one head,
+// are cut into pieces of at most a run of blocks each, one CTA per piece, and
+// the pieces' results, in slots of slot_rows rows, are joined by a second
+// kernel.
 struct WindowTcPlan {
-  int tokens, splits, alternate, parts;
-  float* part_out;  // [parts, S, nq_max, H, D]
-  float* part_lse;  // [parts, S, nq_max, H], log2 domain
+  int tokens, pairs, alternate;
+  int items, grid, slot_rows;
+  int* base;        // [items + 1] pieces before each item (of one head)
+  float* part_out;  // [grid, slots of a piece, slot_rows, D]
+  float* part_lse;  // [grid, slots of a piece, slot_rows], log2 domain
 };
 
 bool window_tc_supports(const AttnArgs& a);
@@ -30,7 +35,6 @@ int launch_weights_tc(const AttnArgs& a, float* weights, cudaStream_t stream);
 bool window_bwd_tc_supports(const AttnArgs& a);
 int window_bwd_tc_tile(int64_t D);  // keys of a work item of the key-centric kernel
 int launch_window_bwd_tc(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream);
-int launch_combine(const AttnArgs& a, const float* part_out, const float* part_lse, int parts, cudaStream_t stream);
 
 namespace wt {
 using namespace tc;
@@ -276,6 +280,27 @@ __device__ __forceinline__ void zero_rows(uint8_t* dst, int rows, int keep, int 
           make_uint4(0, 0, 0, 0);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
+}
+
+template <typename... P, typename... V>
+int launch_after(void (*fn)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, V&&... args) {
+  // programmatic dependent launch: the kernel's set-up overlaps the end of the
+  // launch before it, whose results it waits for (griddepcontrol.wait)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fn, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return LONGNET_ERR_CUDA;
+  }
+  return LONGNET_OK;
 }
 
 // [T, H, D] as (d, h, t): a box is one panel of G heads by `tokens` tokens.
