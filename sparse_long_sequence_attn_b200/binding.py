@@ -497,18 +497,24 @@ def dilated_attention(q, k, v, patterns, causal: bool = True, qk_norm: bool = Fa
     return DilatedAttnFunction.apply(q, k, v, patterns, causal, qk_norm, xpos)
 
 
+_functions = {}
+
+
 def _call(name: str, t: torch.Tensor, stream, *args) -> None:
     """Call the library with t's device current; the stream (default: torch's
     current stream there) is the last argument.  Raises LongNetError on a
     non-zero status."""
     at = t.get_device()
-    handle = (torch.cuda.current_stream(at) if stream is None else stream).cuda_stream or None
-    fn = getattr(load_library(), name)
-    if at == torch.cuda.current_device():
-        rc = fn(*args, handle)
+    # the current stream's handle without a Stream object around it (2 us a call)
+    handle = torch._C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(load_library(), name)
+    if at == torch._C._cuda_getDevice():
+        rc = fn(*args, handle or None)
     else:
         with torch.cuda.device(at):
-            rc = fn(*args, handle)
+            rc = fn(*args, handle or None)
     if rc != LONGNET_OK:
         raise LongNetError(rc, name)
 

@@ -609,12 +609,8 @@ int launch_typed(const AttnArgs& a, float* workspace, float* weights, cudaStream
   int stages = (112 * 1024 - fixed) / LL::kStageBytes;
   if (stages > 8) stages = 8;
   const int smem = fixed + stages * LL::kStageBytes;
-  auto fn = decode_kernel<kFmt, kD>;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024) != cudaSuccess) {
-    cudaGetLastError();
-    return LONGNET_ERR_CUDA;
-  }
-  int rc = launch_after(fn, dim3((unsigned)ctas_of(a)), kThreads, smem, stream, A, maps, stages);
+  if (!opt_in_smem<decode_kernel<kFmt, kD>>(112 * 1024)) return LONGNET_ERR_CUDA;
+  int rc = launch_after(decode_kernel<kFmt, kD>, dim3((unsigned)ctas_of(a)), kThreads, smem, stream, A, maps, stages);
   if (rc) return rc;
   const int64_t pairs = (int64_t)a.S * a.Hkv;
   // pairs cut into many pieces (few pairs over the CTAs) are joined by eight

@@ -243,13 +243,9 @@ int launch_typed(const AttnArgs& a, float* weights, cudaStream_t stream) {
   if (!enc) return LONGNET_ERR_CUDA;
   const int tok = kTile / a.G;
   if (!encode_q(enc, &maps.m[0], a.q, a, tok) || !encode_kv(enc, &maps.m[1], a.k, a, kTile)) return LONGNET_ERR_CUDA;
-  auto fn = weights_kernel<kFmt, kD>;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, LL::kSmem) != cudaSuccess) {
-    cudaGetLastError();
-    return LONGNET_ERR_CUDA;
-  }
+  if (!opt_in_smem<weights_kernel<kFmt, kD>>(LL::kSmem)) return LONGNET_ERR_CUDA;
   const int64_t tiles = (((int64_t)a.max_pages << a.page_shift) + kTile - 1) / kTile;
-  fn<<<dim3((unsigned)tiles, (unsigned)(a.S * a.Hkv)), kThreads, LL::kSmem, stream>>>(a, maps, weights, tok);
+  weights_kernel<kFmt, kD><<<dim3((unsigned)tiles, (unsigned)(a.S * a.Hkv)), kThreads, LL::kSmem, stream>>>(a, maps, weights, tok);
   return cudaGetLastError() == cudaSuccess ? LONGNET_OK : LONGNET_ERR_CUDA;
 }
 

@@ -18,7 +18,8 @@
 //                  rows are 64 / G tokens by the G query heads that share the
 //                  keys, so shared heads sum in the accumulators.
 //   query-centric  a CTA holds two tiles of 128 packed query rows (Q, dout) and
-//                  streams 64-key blocks (K, V): S, dP, then dQ += dS K.
+//                  streams 64-key blocks (K, V): S, dP, then dQ += dS K.  It runs
+//                  first and computes delta on the way.
 // Two score slots (S and dP, 64 columns each) in TMEM, each with a softmax
 // warpgroup of its own: the tensor cores fill one while the other's P and dS
 // are made.  Query-centric, and key-centric up to D = 64, a slot belongs to one
@@ -130,6 +131,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kDescHi = LL::kDescHi;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // the next launch may be scheduled; and what the one before wrote (key-centric:
+  // delta) is read only from here on
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int s = blockIdx.y / a.Hkv, f = blockIdx.y % a.Hkv;
   const int N = a.nq_max, G = a.G, tok = plan.tokens;
   // ---- the CTA's tiles and the streamed rows
@@ -430,10 +435,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t0 = first + st * tok, i = t0 + row / G, h = f * G + row % G;
     const bool row_ok = kKeys ? j < N : row < tok * G && i < N;
     float lse2 = 0.f, delta = 0.f;
-    if (!kKeys && row_ok) {
-      const int64_t idx = ((int64_t)s * a.H + h) * N + i;
-      lse2 = a.lse[idx] * kLog2e;
-      delta = g.delta[idx];
+    if (!kKeys) {
+      // delta of the warp's rows, a row by kRow16 lanes (16 bytes each), kept
+      // by the row's lane and left for the key-centric kernel
+      constexpr int kRow16 = kD / 8, kRows = 32 / kRow16;
+      const int64_t elem = row_ok ? (((int64_t)s * N + i) * a.H + h) * kD : -1;
+      const int c = lane % kRow16;
+#pragma unroll 4
+      for (int r0 = 0; r0 < 32; r0 += kRows) {
+        const int r = r0 + lane / kRow16;
+        const int64_t at = __shfl_sync(0xffffffffu, elem, r);
+        float d = 0.f;
+        if (at >= 0) {
+          const uint4 u = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.out) + at)[c];
+          const uint4 v = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.dout) + at)[c];
+          const uint32_t us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float u0, u1, v0, v1;
+            unpack2<kFmt>(us[e], u0, u1);
+            unpack2<kFmt>(vs[e], v0, v1);
+            d = fmaf(u0, v0, fmaf(u1, v1, d));
+          }
+        }
+#pragma unroll
+        for (int o = kRow16 / 2; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        // row r0 + k's sum is in lanes k kRow16..
+        const float mine = __shfl_sync(0xffffffffu, d, (lane % kRows) * kRow16);
+        if (lane / kRows == r0 / kRows) delta = mine;
+      }
+      if (row_ok) {
+        const int64_t idx = ((int64_t)s * a.H + h) * N + i;
+        lse2 = a.lse[idx] * kLog2e;
+        g.delta[idx] = delta;
+      }
     }
     const uint64_t sc2 = f32x2(a.scale_log2, a.scale_log2);
     const uint64_t nl_row = f32x2(-lse2, -lse2), nd_row = f32x2(-delta, -delta);
@@ -569,22 +604,18 @@ int launch_typed(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream)
       !encode_rows(enc, &mq.t[0], a.q, a, pq.tokens) || !encode_rows(enc, &mq.t[1], g.dout, a, pq.tokens) ||
       !encode_kv(enc, &mq.b[0], a.k, a, kBlk) || !encode_kv(enc, &mq.b[1], a.v, a, kBlk))
     return LONGNET_ERR_CUDA;
-  auto fk = bwd_kernel<kFmt, kD, true>;
-  auto fq = bwd_kernel<kFmt, kD, false>;
-  if (cudaFuncSetAttribute(fk, cudaFuncAttributeMaxDynamicSharedMemorySize, LK::kSmem) != cudaSuccess ||
-      cudaFuncSetAttribute(fq, cudaFuncAttributeMaxDynamicSharedMemorySize, LQ::kSmem) != cudaSuccess) {
-    cudaGetLastError();
+  if (!opt_in_smem<bwd_kernel<kFmt, kD, true>>(LK::kSmem) || !opt_in_smem<bwd_kernel<kFmt, kD, false>>(LQ::kSmem))
     return LONGNET_ERR_CUDA;
-  }
-  int rc = launch_window_delta(a, g, stream);
-  if (rc) return rc;
   const int64_t items = ((int64_t)a.nq_max + LK::kTiles * kTile - 1) / (LK::kTiles * kTile) +
                         (int64_t)pk.far.sink_tiles * pk.far.chunks;
-  fk<<<dim3((unsigned)items, (unsigned)(a.S * a.Hkv)), kThreads, LK::kSmem, stream>>>(a, g, mk, pk);
-  if (cudaGetLastError() != cudaSuccess) return LONGNET_ERR_CUDA;
   const int64_t pairs = ((int64_t)a.nq_max + 2 * pq.tokens - 1) / (2 * pq.tokens);
-  fq<<<dim3((unsigned)pairs, (unsigned)(a.S * a.Hkv)), kThreads, LQ::kSmem, stream>>>(a, g, mq, pq);
-  if (cudaGetLastError() != cudaSuccess) return LONGNET_ERR_CUDA;
+  // dq first: it leaves delta for dk and dv
+  int rc = launch_after(bwd_kernel<kFmt, kD, false>, dim3((unsigned)pairs, (unsigned)(a.S * a.Hkv)), kThreads, LQ::kSmem,
+                        stream, a, g, mq, pq);
+  if (rc) return rc;
+  rc = launch_after(bwd_kernel<kFmt, kD, true>, dim3((unsigned)items, (unsigned)(a.S * a.Hkv)), kThreads, LK::kSmem,
+                    stream, a, g, mk, pk);
+  if (rc) return rc;
   return launch_far_reduce(a, g, pk.far, stream);
 }
 

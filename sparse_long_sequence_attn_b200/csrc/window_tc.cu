@@ -610,11 +610,9 @@ int launch_typed(const AttnArgs& a, const Plan& plan, cudaStream_t stream) {
   if (!encode_q(enc, &maps.m[0], a.q, a, plan.tokens) || !encode_kv(enc, &maps.m[1], a.k, a, kBlk) ||
       !encode_kv(enc, &maps.m[2], a.v, a, kBlk))
     return LONGNET_ERR_CUDA;
-  auto fn = a.cu_q ? fwd_kernel<kFmt, kD, true> : fwd_kernel<kFmt, kD, false>;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, LL::kSmem) != cudaSuccess) {
-    cudaGetLastError();
+  if (!(a.cu_q ? opt_in_smem<fwd_kernel<kFmt, kD, true>>(LL::kSmem) : opt_in_smem<fwd_kernel<kFmt, kD, false>>(LL::kSmem)))
     return LONGNET_ERR_CUDA;
-  }
+  auto fn = a.cu_q ? fwd_kernel<kFmt, kD, true> : fwd_kernel<kFmt, kD, false>;
   const dim3 grid = plan.items ? dim3((unsigned)plan.grid) : dim3((unsigned)plan.pairs, (unsigned)(a.S * a.Hkv));
   int rc = launch_after(fn, grid, kThreads, LL::kSmem, stream, a, maps, plan);
   if (rc || !plan.items) return rc;

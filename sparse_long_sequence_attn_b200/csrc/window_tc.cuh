@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "attn_args.cuh"
 #include "tc_ptx.cuh"
 
@@ -280,6 +282,25 @@ __device__ __forceinline__ void zero_rows(uint8_t* dst, int rows, int keep, int 
           make_uint4(0, 0, 0, 0);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
+}
+
+// Opts a kernel in to its shared memory, once per device (fn's instantiations
+// have a flag each).
+template <auto fn>
+bool opt_in_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return false;
+  }
+  if ((done.load(std::memory_order_acquire) >> dev) & 1) return true;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  done.fetch_or((uint64_t)1 << dev, std::memory_order_release);
+  return true;
 }
 
 template <typename... P, typename... V>
