@@ -7,9 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "attn_args.cuh"
+#include "launch_util.cuh"
 #include "tc_ptx.cuh"
 
 namespace longnet {
@@ -282,46 +281,6 @@ __device__ __forceinline__ void zero_rows(uint8_t* dst, int rows, int keep, int 
           make_uint4(0, 0, 0, 0);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
-}
-
-// Opts a kernel in to its shared memory, once per device (fn's instantiations
-// have a flag each).
-template <auto fn>
-bool opt_in_smem(int bytes) {
-  static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
-    cudaGetLastError();
-    return false;
-  }
-  if ((done.load(std::memory_order_acquire) >> dev) & 1) return true;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  done.fetch_or((uint64_t)1 << dev, std::memory_order_release);
-  return true;
-}
-
-template <typename... P, typename... V>
-int launch_after(void (*fn)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, V&&... args) {
-  // programmatic dependent launch: the kernel's set-up overlaps the end of the
-  // launch before it, whose results it waits for (griddepcontrol.wait)
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fn, args...) != cudaSuccess) {
-    cudaGetLastError();
-    return LONGNET_ERR_CUDA;
-  }
-  return LONGNET_OK;
 }
 
 // [T, H, D] as (d, h, t): a box is one panel of G heads by `tokens` tokens.
