@@ -130,21 +130,56 @@ struct WindowBwdArgs {
   float* delta;
   float* partial;
 };
-// Key tiles (of window_tile(impl) keys) holding sinks take the queries past
-// their window in `chunks` further work items, each summed on its own.
-struct FarPlan {
-  int tile;         // keys of a tile
-  int sink_tiles;   // tiles with far work
-  int chunk;        // queries of a far item
-  int chunks;       // far items of the first tile (the most any has)
+// How dk and dv are cut into work items, one CTA each: a tile of keys by a
+// range of the queries that see it.  A tile's near queries (those its window
+// reaches) are cut into `near` ranges where the tiles alone would leave SMs
+// idle; a tile holding sinks has far queries past its window, in ranges of
+// `chunk`.  A tile with more than one item gets a partial (a slot) from each,
+// which launch_key_reduce adds in order.
+struct KeyPlan {
+  int tile, tiles;   // keys of a tile, tiles
+  int near;          // near items of a tile
+  int sink_tiles;    // tiles with far items
+  int chunk, chunks; // queries of a far item; far items of a tile
+  __host__ __device__ int items() const { return sink_tiles * chunks + tiles * near; }
+  // slots of the tiles before t, of one (batch, head)
+  __host__ __device__ int slot_of(int t) const {
+    return t <= sink_tiles ? t * (near + chunks) : sink_tiles * (near + chunks) + (near > 1 ? (t - sink_tiles) * near : 0);
+  }
+  __host__ __device__ int slots() const { return slot_of(tiles); }
+  __host__ __device__ int reduced() const { return near > 1 ? tiles : sink_tiles; }  // tiles with partials
 };
-FarPlan far_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, int64_t sinks, int tile);
-int64_t far_partial_floats(const FarPlan& f, int64_t S, int64_t Hkv, int64_t D);
+// One item: queries [i0, i1) (none when i0 >= i1) for the tile, into a slot, or
+// straight into dk and dv (slot -1).
+struct KeyItem {
+  int tile, i0, i1, slot;
+};
+__device__ __forceinline__ KeyItem key_item(const AttnArgs& a, const KeyPlan& k, int x) {
+  KeyItem it;
+  const int N = a.nq_max, fars = k.sink_tiles * k.chunks;
+  const bool far = x < fars;  // far items first: they are as long as any
+  const int part = far ? x % k.chunks : (x - fars) % k.near;
+  it.tile = far ? x / k.chunks : (x - fars) / k.near;
+  const int first = it.tile * k.tile;
+  // the near queries end where the window of the tile's last key does, or, for
+  // a tile with sinks whose far queries have no items, with the sequence
+  const int64_t reach = (int64_t)first + k.tile - 1 + a.window;
+  const int end = reach >= N || (first < a.sinks && it.tile >= k.sink_tiles) ? N : (int)reach;
+  const int len = far ? k.chunk : (end - first + k.near - 1) / k.near;
+  const int64_t i0 = (int64_t)(far ? end : first) + (int64_t)part * len, stop = far ? N : end;
+  it.i0 = i0 < stop ? (int)i0 : (int)stop;
+  it.i1 = i0 + len < stop ? (int)(i0 + len) : (int)stop;
+  it.slot = k.near > 1 || it.tile < k.sink_tiles ? k.slot_of(it.tile) + (far ? k.near + part : part) : -1;
+  return it;
+}
+KeyPlan key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, int64_t sinks, int tile, int min_blocks,
+                 int ctas);
+int64_t key_partial_floats(const KeyPlan& k, int64_t S, int64_t Hkv, int64_t D);
+constexpr int kSimtKeyTile = 64, kSimtMinBlocks = 2, kSimtCtas = 296;  // of key_plan, for the SIMT family
 int launch_window_bwd_simt(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream);
-// The last steps both families share: delta = <dout, out>, and the far
-// partials of the sink tiles summed in order into dk and dv.
+// delta = <dout, out> of every row, and the last step both families share.
 int launch_window_delta(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream);
-int launch_far_reduce(const AttnArgs& a, const WindowBwdArgs& g, const FarPlan& f, cudaStream_t stream);
+int launch_key_reduce(const AttnArgs& a, const WindowBwdArgs& g, const KeyPlan& k, cudaStream_t stream);
 
 int launch_paged_append(const AttnArgs& a, const void* k_tok, const void* v_tok, float* weights, cudaStream_t stream);
 

@@ -70,7 +70,7 @@ struct __align__(64) BMaps {
 
 struct BPlan {
   int tokens;    // of a tile (query-centric) or of a block (key-centric)
-  FarPlan far;
+  KeyPlan key;
 };
 
 struct Run {
@@ -141,29 +141,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   int first;                // key-centric: first key; query-centric: first token
   int i0 = 0, cnt = 0;      // key-centric: first streamed token; blocks
   int i1 = 0;               // key-centric: end of the streamed tokens
-  int far = -1, ftile = 0;  // key-centric: far item and its tile, or -1 and the tile
+  int slot_no = -1;         // key-centric: the item's slot
   BlockList bl = {0, 0, 0};
   if (kKeys) {
-    const int tiles = (N + kTiles * kTile - 1) / (kTiles * kTile);
-    far = (int)blockIdx.x - plan.far.sink_tiles * plan.far.chunks;  // far items first: they are as long as any
-    if (far < 0) {
-      const int item = blockIdx.x;
-      ftile = item / plan.far.chunks;
-      far = item % plan.far.chunks;
-    } else {
-      ftile = far;
-      far = -1;
-    }
-    if (ftile >= tiles) return;
-    first = ftile * kTiles * kTile;
-    const int64_t reach = (int64_t)first + kTiles * kTile - 1 + a.window;
-    const int near = reach >= N || (first < a.sinks && ftile >= plan.far.sink_tiles) ? N : (int)reach;
-    i0 = first;
-    i1 = near;
-    if (far >= 0) {
-      i0 = near + far * plan.far.chunk;
-      i1 = i0 + plan.far.chunk < N ? i0 + plan.far.chunk : N;
-    }
+    const KeyItem it = key_item(a, plan.key, blockIdx.x);
+    first = it.tile * kTiles * kTile;
+    i0 = it.i0;
+    i1 = it.i1;
+    slot_no = it.slot;
     cnt = i1 > i0 ? (i1 - i0 + tok - 1) / tok : 0;
   } else {
     first = ((int)gridDim.x - 1 - (int)blockIdx.x) * 2 * tok;  // the longest first
@@ -520,9 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const bool any = kTiles == 2 ? done > 0 : cnt > 0;
     if (ok && any) ok = wt.wait_warp(bar_acc + st, 0);
+    // (a tile that met no block is still written below: not before its load landed)
+    if (ok && cnt > 0) ok = wt.wait_warp(bar_tile, 0);
     if (ok) {
       tc_fence_after();
-      const bool partial = kKeys && ftile < plan.far.sink_tiles;
+      const bool partial = kKeys && slot_no >= 0;
       // key-centric with two tiles: a warpgroup writes both gradients of its
       // tile; with one tile, the first dV and the second dK
 #pragma unroll 1
@@ -538,11 +525,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           store_rows<kFmt, kD>(tile_ptr(kTiles == 2 ? st : 0, w), acc, any, sc, 32 * (warp & 3), lane, dst, row_ok);
           continue;
         }
-        const int slot_no = far < 0 ? 0 : 1 + far;
-        // [S Hkv][sink tile][slot][dK, dV][tile rows][D]
-        float* part = g.partial + ((((int64_t)blockIdx.y * plan.far.sink_tiles + ftile) * (plan.far.chunks + 1) + slot_no) * 2 +
-                                   (w == 0 ? 1 : 0)) * (int64_t)(kTiles * kTile * kD) +
-                      (int64_t)(j - first) * kD;
+        // [S Hkv][slot][dK, dV][tile rows][D]
+        float* part = g.partial + (((int64_t)blockIdx.y * plan.key.slots() + slot_no) * 2 + (w == 0 ? 1 : 0)) *
+                                      (int64_t)(kTiles * kTile * kD) + (int64_t)(j - first) * kD;
+        if constexpr (kD >= 64) {
+          store_rows_f32<kD>(tile_ptr(kTiles == 2 ? st : 0, w), acc, any, sc, 32 * (warp & 3), lane, part);
+          continue;
+        }
         constexpr int kChunk = kD < 32 ? kD : 32;
 #pragma unroll 1
         for (int c0 = 0; c0 < kD; c0 += kChunk) {
@@ -597,7 +586,8 @@ int launch_typed(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream)
   pq.tokens = kTile / a.G;
   using LK = B<kD, true>;
   using LQ = B<kD, false>;
-  pk.far = pq.far = far_plan(a.S, a.nq_max, a.H, a.Hkv, a.window, a.sinks, LK::kTiles * kTile);
+  pk.key = pq.key =
+      key_plan(a.S, a.nq_max, a.H, a.Hkv, a.window, a.sinks, LK::kTiles * kTile, kTcMinBlocks, kTcCtas);
   BMaps mk, mq;
   if (!encode_kv(enc, &mk.t[0], a.k, a, kTile) || !encode_kv(enc, &mk.t[1], a.v, a, kTile) ||
       !encode_rows(enc, &mk.b[0], a.q, a, pk.tokens) || !encode_rows(enc, &mk.b[1], g.dout, a, pk.tokens) ||
@@ -606,17 +596,15 @@ int launch_typed(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream)
     return LONGNET_ERR_CUDA;
   if (!opt_in_smem<bwd_kernel<kFmt, kD, true>>(LK::kSmem) || !opt_in_smem<bwd_kernel<kFmt, kD, false>>(LQ::kSmem))
     return LONGNET_ERR_CUDA;
-  const int64_t items = ((int64_t)a.nq_max + LK::kTiles * kTile - 1) / (LK::kTiles * kTile) +
-                        (int64_t)pk.far.sink_tiles * pk.far.chunks;
   const int64_t pairs = ((int64_t)a.nq_max + 2 * pq.tokens - 1) / (2 * pq.tokens);
   // dq first: it leaves delta for dk and dv
   int rc = launch_after(bwd_kernel<kFmt, kD, false>, dim3((unsigned)pairs, (unsigned)(a.S * a.Hkv)), kThreads, LQ::kSmem,
                         stream, a, g, mq, pq);
   if (rc) return rc;
-  rc = launch_after(bwd_kernel<kFmt, kD, true>, dim3((unsigned)items, (unsigned)(a.S * a.Hkv)), kThreads, LK::kSmem,
+  rc = launch_after(bwd_kernel<kFmt, kD, true>, dim3((unsigned)pk.key.items(), (unsigned)(a.S * a.Hkv)), kThreads, LK::kSmem,
                     stream, a, g, mk, pk);
   if (rc) return rc;
-  return launch_far_reduce(a, g, pk.far, stream);
+  return launch_key_reduce(a, g, pk.key, stream);
 }
 
 }  // namespace wb

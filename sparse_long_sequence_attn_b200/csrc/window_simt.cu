@@ -387,11 +387,9 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a, const Wi
   }
 }
 
-// dk, dv of a tile of 64 keys.  Blocks past the tiles' own are the far items
-// of the sink tiles: the queries past the tile's window, in chunks, each into
-// a partial of its own (far_reduce adds them in order).
+// dk, dv of a tile of 64 keys over one item's queries.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a, const WindowBwdArgs g, const FarPlan fp) {
+__global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a, const WindowBwdArgs g, const KeyPlan kp) {
   extern __shared__ __align__(16) float sm[];
   float* sK = sm;
   float* sV = sm + L<D>::kTile;
@@ -402,20 +400,8 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a, const W
   __shared__ float s_lse[kT], s_delta[kT];
   const int s = blockIdx.y / a.Hkv, f = blockIdx.y % a.Hkv;
   const Seq q = seq_of(a, s);
-  const int tiles = (a.nq_max + kT - 1) / kT;
-  const int far = (int)blockIdx.x - tiles;  // far item, or the tile itself when negative
-  const int tile = far < 0 ? (int)blockIdx.x : far / fp.chunks;
-  const int j0 = tile * kT;
-  // queries whose window reaches the tile: [j0, near); all later ones where
-  // the tile holds sinks and no far items take them
-  const int64_t reach = (int64_t)j0 + kT - 1 + a.window;
-  const int near = reach >= q.nq || (j0 < a.sinks && tile >= fp.sink_tiles) ? q.nq : (int)reach;
-  int i0 = j0, i1 = near;
-  if (far >= 0) {
-    i0 = near + (far % fp.chunks) * fp.chunk;
-    i1 = i0 + fp.chunk < q.nq ? i0 + fp.chunk : q.nq;
-    // an item past the last query still writes its (zero) partial
-  }
+  const KeyItem it = key_item(a, kp, blockIdx.x);
+  const int j0 = it.tile * kT, i0 = it.i0, i1 = it.i1;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   auto krow = [&](int r) -> int64_t { return j0 + r < q.kv ? kv_row(a, q, s, f, j0 + r) : -1; };
   load_rows<T, D>(sK, static_cast<const T*>(a.k), krow);
@@ -452,15 +438,12 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a, const W
     accumulate<D>(sP, sO, ty, tx, dv);
     accumulate<D>(sS, sQ, ty, tx, dk);
   }
-  const bool partial = tile < fp.sink_tiles;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int j = j0 + 4 * ty + r;
-    if (partial) {
-      // slot 0 the tile's own, slot 1 + c far item c: [S Hkv][tile][slot][2][kT][D]
-      const int slot = far < 0 ? 0 : 1 + far % fp.chunks;
-      float* p = g.partial + (((((int64_t)blockIdx.y * fp.sink_tiles + tile) * (fp.chunks + 1) + slot) * 2) * kT +
-                              4 * ty + r) * D;
+    if (it.slot >= 0) {
+      // [S Hkv][slot][dk, dv][kT][D]
+      float* p = g.partial + ((((int64_t)blockIdx.y * kp.slots() + it.slot) * 2) * kT + 4 * ty + r) * D;
 #pragma unroll
       for (int c = 0; c < L<D>::kC; ++c) {
         p[L<D>::col(tx, c)] = dk[r][c] * a.scale;
@@ -477,22 +460,34 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a, const W
   }
 }
 
-// dk and dv of the sink tiles: their partials added in slot order (the order
-// is fixed, so the result does not change from run to run).
+// dk and dv of the tiles with partials, added in slot order (the order is
+// fixed, so the result does not change from run to run).
 template <typename T>
-__global__ void __launch_bounds__(256) far_reduce_kernel(const AttnArgs a, const WindowBwdArgs g, const FarPlan fp) {
-  const int sf = blockIdx.y / fp.sink_tiles, tile = blockIdx.y % fp.sink_tiles;
+__global__ void __launch_bounds__(256) key_reduce_kernel(const AttnArgs a, const WindowBwdArgs g, const KeyPlan kp) {
+  const int sf = blockIdx.z, tile = blockIdx.y;
   const int s = sf / a.Hkv, f = sf % a.Hkv;
-  const int per = fp.tile * a.D;  // values of one gradient's tile
-  const int e = blockIdx.x * 256 + threadIdx.x;
+  const int per = kp.tile * a.D;  // values of one gradient's tile
+  const int e = (blockIdx.x * 256 + threadIdx.x) * 4;
   if (e >= 2 * per) return;
-  const float* p = g.partial + ((int64_t)sf * fp.sink_tiles + tile) * (fp.chunks + 1) * 2 * per + e;
-  float acc = 0.f;
-  for (int c = 0; c <= fp.chunks; ++c) acc += p[(int64_t)c * 2 * per];
+  const int s0 = kp.slot_of(tile), s1 = kp.slot_of(tile + 1);
+  const float* p = g.partial + ((int64_t)sf * kp.slots() + s0) * 2 * per + e;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = 0; c < s1 - s0; ++c) {
+    const float4 x = *reinterpret_cast<const float4*>(p + (int64_t)c * 2 * per);
+    acc.x += x.x;
+    acc.y += x.y;
+    acc.z += x.z;
+    acc.w += x.w;
+  }
   const int which = e / per, r = (e % per) / a.D, d = e % a.D;
-  const int j = tile * fp.tile + r;
-  if (j < a.nq_max)
-    static_cast<T*>(which ? g.dv : g.dk)[(((int64_t)s * a.nq_max + j) * a.Hkv + f) * a.D + d] = from_f<T>(acc);
+  const int j = tile * kp.tile + r;
+  if (j >= a.nq_max) return;
+  T* o = static_cast<T*>(which ? g.dv : g.dk) + (((int64_t)s * a.nq_max + j) * a.Hkv + f) * a.D + d;
+  o[0] = from_f<T>(acc.x);
+  o[1] = from_f<T>(acc.y);
+  o[2] = from_f<T>(acc.z);
+  o[3] = from_f<T>(acc.w);
 }
 
 bool set_smem(const void* fn, int bytes) {
@@ -526,18 +521,17 @@ template <typename T, int D>
 int bwd(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t st) {
   int rc = launch_window_delta(a, g, st);
   if (rc) return rc;
-  const FarPlan fp = far_plan(a.S, a.nq_max, a.H, a.Hkv, a.window, a.sinks, kT);
+  const KeyPlan kp = key_plan(a.S, a.nq_max, a.H, a.Hkv, a.window, a.sinks, kSimtKeyTile, kSimtMinBlocks, kSimtCtas);
   const int smem_q = (4 * L<D>::kTile + kT * kPS) * 4, smem_k = smem_q + kT * kPS * 4;
   auto fq = dq_kernel<T, D>;
   auto fk = dkv_kernel<T, D>;
   if (!set_smem((const void*)fq, smem_q) || !set_smem((const void*)fk, smem_k)) return LONGNET_ERR_CUDA;
-  const int64_t items = (a.nq_max + kT - 1) / kT + (int64_t)fp.sink_tiles * fp.chunks;
-  fk<<<dim3((unsigned)items, (unsigned)(a.S * a.Hkv)), kThreads, smem_k, st>>>(a, g, fp);
+  fk<<<dim3((unsigned)kp.items(), (unsigned)(a.S * a.Hkv)), kThreads, smem_k, st>>>(a, g, kp);
   if ((rc = ok_launch())) return rc;
   const int64_t tiles = ((int64_t)a.nq_max * a.G + kT - 1) / kT;
   fq<<<dim3((unsigned)tiles, (unsigned)(a.S * a.Hkv)), kThreads, smem_q, st>>>(a, g);
   if ((rc = ok_launch())) return rc;
-  return launch_far_reduce(a, g, fp, st);
+  return launch_key_reduce(a, g, kp, st);
 }
 template <typename T, int D>
 int delta(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t st) {
@@ -571,44 +565,54 @@ int launch_window_delta(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t 
   return LN_BY_TYPE(ws::delta, a, g, stream);
 }
 
-int launch_far_reduce(const AttnArgs& a, const WindowBwdArgs& g, const FarPlan& f, cudaStream_t stream) {
-  if (f.sink_tiles == 0) return LONGNET_OK;
-  const dim3 grid((unsigned)((2 * f.tile * a.D + 255) / 256), (unsigned)((int64_t)a.S * a.Hkv * f.sink_tiles));
+int launch_key_reduce(const AttnArgs& a, const WindowBwdArgs& g, const KeyPlan& k, cudaStream_t stream) {
+  if (k.reduced() == 0) return LONGNET_OK;
+  const dim3 grid((unsigned)((2 * k.tile * a.D / 4 + 255) / 256), (unsigned)k.reduced(), (unsigned)(a.S * a.Hkv));
   if (a.dtype == LONGNET_DTYPE_F32)
-    ws::far_reduce_kernel<float><<<grid, 256, 0, stream>>>(a, g, f);
+    ws::key_reduce_kernel<float><<<grid, 256, 0, stream>>>(a, g, k);
   else if (a.dtype == LONGNET_DTYPE_BF16)
-    ws::far_reduce_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, g, f);
+    ws::key_reduce_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, g, k);
   else
-    ws::far_reduce_kernel<__half><<<grid, 256, 0, stream>>>(a, g, f);
+    ws::key_reduce_kernel<__half><<<grid, 256, 0, stream>>>(a, g, k);
   return ws::ok_launch();
 }
 
-// A sink tile's far queries, about as many per item as its window holds (so
-// an item costs what an ordinary tile does), at least 4 tiles' worth and at
-// most 64 items.  With more than 16 sink tiles there are enough of them to
-// fill the GPU without: each then takes all its queries itself.
-FarPlan far_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, int64_t sinks, int tile) {
-  FarPlan f = {tile, 0, 0, 0};
-  // tiles with sinks and queries past their window
+// A far item has about as many queries as a tile's window holds (so it costs
+// what an ordinary tile does), at least 4 tiles' worth, at most 64 items a
+// tile.  With more than 16 sink tiles there are enough of them to fill the GPU
+// without: each then takes all its queries itself.  Near ranges: so many
+// that there are about `ctas` items, of at least min_blocks blocks of 64 query
+// rows each.
+KeyPlan key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, int64_t sinks, int tile,
+                 int min_blocks, int ctas) {
+  KeyPlan k = {tile, (int)((N + tile - 1) / tile), 1, 0, 0, 0};
+  if (window > N) window = N;
   if (sinks > N) sinks = N;
-  if (sinks <= 0 || window >= N) return f;
+  const int64_t reach = tile + window < N ? tile + window : N;
+  const int64_t blocks = reach * (H / Hkv) / 64;
+  int64_t near = ctas / (k.tiles * S * Hkv);
+  if (near > blocks / min_blocks) near = blocks / min_blocks;
+  if (near > 16) near = 16;
+  if (near > 1) k.near = (int)near;
+  // tiles with sinks and queries past their window
   int64_t t = (sinks + tile - 1) / tile;
   const int64_t past = N - (tile - 1 + window);  // queries past the first tile's window
-  if (past <= 0) return f;
+  if (t <= 0 || past <= 0) return k;
   const int64_t has = (past + tile - 1) / tile;  // tiles that have any
   if (t > has) t = has;
-  if (t > 16) return f;
-  int64_t chunk = window + tile;
-  if (chunk < 4 * tile) chunk = 4 * tile;
+  if (t > 16) return k;
+  int64_t chunk = (window + tile) / k.near;
+  if (chunk < 4 * tile / k.near) chunk = 4 * tile / k.near;
+  if (chunk < 64) chunk = 64;
   if ((past + chunk - 1) / chunk > 64) chunk = (past + 63) / 64;
-  f.sink_tiles = (int)t;
-  f.chunk = (int)chunk;
-  f.chunks = (int)((past + chunk - 1) / chunk);
-  return f;
+  k.sink_tiles = (int)t;
+  k.chunk = (int)chunk;
+  k.chunks = (int)((past + chunk - 1) / chunk);
+  return k;
 }
 
-int64_t far_partial_floats(const FarPlan& f, int64_t S, int64_t Hkv, int64_t D) {
-  return S * Hkv * f.sink_tiles * (int64_t)(f.chunks + 1) * 2 * f.tile * D;
+int64_t key_partial_floats(const KeyPlan& k, int64_t S, int64_t Hkv, int64_t D) {
+  return S * Hkv * k.slots() * 2 * (int64_t)k.tile * D;
 }
 
 }  // namespace longnet

@@ -484,6 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++done;
     }
     if (ok && done > 0) ok = wt.wait_warp(bar_o + st, 0);
+    // (a tile that met no block is still written below: not before its load landed)
+    if (ok && cnt > 0) ok = wt.wait_warp(bar_q, 0);
     if (ok && ta < tb) {
       tc_fence_after();
       const float inv = l_run > 0.f ? 1.f / l_run : 0.f;

@@ -35,6 +35,7 @@ int launch_window_fwd_tc(const AttnArgs& a, float* parts, cudaStream_t stream);
 int launch_weights_tc(const AttnArgs& a, float* weights, cudaStream_t stream);
 bool window_bwd_tc_supports(const AttnArgs& a);
 int window_bwd_tc_tile(int64_t D);  // keys of a work item of the key-centric kernel
+constexpr int kTcMinBlocks = 8, kTcCtas = 148;  // of key_plan, for the tcgen05 family
 int launch_window_bwd_tc(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream);
 
 namespace wt {
@@ -177,6 +178,37 @@ __device__ __forceinline__ void store_rows(uint8_t* tile, uint32_t acc, bool any
     const int r = r0 + lane / kRow16, c = lane % kRow16;
     const uint64_t to = __shfl_sync(0xffffffffu, mine, r);
     if ((mask >> r) & 1) reinterpret_cast<uint4*>(to)[c] = *at(row0 + r, c);
+  }
+}
+
+// The same rows as fp32 to consecutive global rows of kD floats (dst: the
+// lane's), 32 columns at a time through 128-byte rows of `tile` (16 KB).
+template <int kD>
+__device__ __forceinline__ void store_rows_f32(uint8_t* tile, uint32_t acc, bool any, float scale, int row0, int lane,
+                                               float* dst) {
+  float* first = dst - (int64_t)lane * kD;  // the warp's row 0
+#pragma unroll 1
+  for (int c0 = 0; c0 < kD; c0 += 32) {
+    uint32_t rr[32];
+    if (any) {
+      LN_TMEM_LD32(acc + c0, rr);
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) rr[c] = 0;
+    }
+    auto at = [&](int r, int c) { return reinterpret_cast<float4*>(tile + (row0 + r) * 128 + ((c ^ (r & 7)) << 4)); };
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      *at(lane, c) = make_float4(__uint_as_float(rr[4 * c]) * scale, __uint_as_float(rr[4 * c + 1]) * scale,
+                                 __uint_as_float(rr[4 * c + 2]) * scale, __uint_as_float(rr[4 * c + 3]) * scale);
+    __syncwarp();
+#pragma unroll
+    for (int r0 = 0; r0 < 32; r0 += 4) {
+      const int r = r0 + lane / 8, c = lane % 8;
+      *reinterpret_cast<float4*>(first + (int64_t)r * kD + c0 + 4 * c) = *at(r, c);
+    }
+    __syncwarp();
   }
 }
 
