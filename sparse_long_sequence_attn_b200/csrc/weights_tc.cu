@@ -10,8 +10,8 @@
 //
 // A CTA holds a tile of 128 keys of one key/value head and streams blocks of
 // 128 packed query rows (128 / G tokens by G heads) with their lse.  Two
-// 128-column score buffers in TMEM, a warpgroup each, take alternate blocks;
-// two CTAs share an SM.
+// warpgroups take alternate blocks, each with two 128-column score buffers in
+// TMEM, so that a block's scores are there when the one before is summed.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -30,20 +30,51 @@ using namespace wt;
 
 constexpr int kThreads = 320;
 constexpr int kTma = 8, kMma = 9;  // warps
-constexpr uint32_t kTmemCols = 256;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSlots = 4;  // score buffers
 
 template <int kD>
 struct L : Panels<kD> {
   static constexpr int kTileBytes = kTile * kD * 2;
   static constexpr int kStageBytes = kTileBytes + 1024;  // a block of query rows, then their -lse
-  static constexpr int kStages = 2;
+  static constexpr int kStages = kD == 128 ? 5 : 6;
   static constexpr int kBars = kTileBytes + kStages * kStageBytes;
-  // at least 80 KB, so that no third CTA (without TMEM columns left) shares an SM
-  static constexpr int kSmem = kBars + 1024 + 1024 > 80 * 1024 ? kBars + 1024 + 1024 : 80 * 1024;
+  // one CTA per SM: its TMEM columns are all of the SM's
+  static constexpr int kSmem = kBars + 1024 + 1024 > 120 * 1024 ? kBars + 1024 + 1024 : 120 * 1024;
 };
 
+// acc += the sum over 128 columns of 2^(s scale log2(e) - lse log2(e)), of those
+// in [lo, hi) with kMask.
+template <bool kMask>
+__device__ __forceinline__ void sum_block(uint32_t s_col, const float* sl, uint64_t sc2, int lo, int hi,
+                                          uint64_t (&acc)[2]) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    uint32_t sr[32];
+    LN_TMEM_LD32(s_col + 32 * w, sr);
+    tmem_wait_ld();
+    const uint32_t keep = below(hi - 32 * w) & ~below(lo - 32 * w);
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+      const float4 l4 = *reinterpret_cast<const float4*>(sl + 32 * w + c);
+      float x[4];
+      f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sc2, f32x2(l4.x, l4.y)), x[0],
+                  x[1]);
+      f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sc2, f32x2(l4.z, l4.w)),
+                  x[2], x[3]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = ex2(x[e]);
+        if (kMask) x[e] = (keep >> (c + e)) & 1 ? x[e] : 0.f;
+      }
+      acc[0] = add_f32x2(acc[0], f32x2(x[0], x[1]));
+      acc[1] = add_f32x2(acc[1], f32x2(x[2], x[3]));
+    }
+  }
+}
+
 template <int kFmt, int kD>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     weights_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Maps maps, float* weights, int tok) {
   using LL = L<kD>;
   constexpr int kPanels = LL::kPanels, kPanelBytes = kTile * LL::kRowBytes, S = LL::kStages;
@@ -70,21 +101,21 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint64_t* bar_k = bars;
   uint64_t* bar_full = bars + 1;       // [S]
   uint64_t* bar_empty = bars + 1 + S;  // [S] the block's scores done, and read
-  uint64_t* bar_s = bars + 1 + 2 * S;  // [2] scores in TMEM
-  uint64_t* bar_r = bar_s + 2;         // [2] scores read
-  uint64_t* bar_drain = bar_s + 4;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_s + 5);
+  uint64_t* bar_s = bars + 1 + 2 * S;  // [kSlots] scores in TMEM
+  uint64_t* bar_r = bar_s + kSlots;    // [kSlots] scores read
+  uint64_t* bar_drain = bar_s + 2 * kSlots;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_s + 2 * kSlots + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* s_sum = reinterpret_cast<float*>(smem + LL::kBars + 256);  // [128]
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(bar_k, 1);
     for (int i = 0; i < S; ++i) {
       mbar_init(bar_full + i, 32);        // the loading warp's lanes, and the TMA bytes
       mbar_init(bar_empty + i, 1 + 128);  // the scores' commit, and the threads that read the -lse
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
       mbar_init(bar_s + i, 1);
       mbar_init(bar_r + i, 128);
     }
@@ -102,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   Waiter wt{abort_flag, a.status, kWaitLimitNs};
   float sum = 0.f;
 
@@ -111,34 +142,50 @@ __global__ void __launch_bounds__(kThreads, 2)
     bool ok = true;
     load_pages<kD>(a, q, s, f, j0, kTile, &maps.m[1], smem, bar_k, lane);
     if (lane == 0) mbar_arrive(bar_k);
+    // -lse (log2 domain) of a block's rows, fetched a block ahead (their
+    // latency would otherwise stand between the loads)
+    // (loaded from a valid address in any case: a load under a condition is
+    // waited for where the condition ends)
+    float l2[4];
+    int c_tok[4], c_head[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      c_tok[e] = (lane + 32 * e) / G;
+      c_head[e] = f * G + (lane + 32 * e) % G;
+    }
+    auto fetch = [&](int n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = i0 + n * tok + c_tok[e];
+        l2[e] = a.lse[(q.q0 + (i < i1 ? i : i0)) * a.H + c_head[e]];
+      }
+    };
+    fetch(0);
     int issued = 0;
     for (int n = 0; n < cnt && ok; ++n) {
       const int st = n % S;
       if (n >= S) ok = wt.wait_warp(bar_empty + st, ((n / S) - 1) & 1);
       if (!ok) break;
       uint8_t* stage = sStage + st * LL::kStageBytes;
-      const int at = i0 + n * tok;
       if (lane == 0) {
         mbar_expect_tx(bar_full + st, (uint32_t)(kPanels * tok * G * LL::kRowBytes));
 #pragma unroll
         for (int pn = 0; pn < kPanels; ++pn)
           tma_load_3d(stage + pn * kPanelBytes, &maps.m[0], bar_full + st, LL::kPanelElems * pn, f * G,
-                      (int)(q.q0 + at));
+                      (int)(q.q0 + i0 + n * tok));
       }
       float* sl = reinterpret_cast<float*>(stage + LL::kTileBytes);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int c = lane + 32 * e, i = at + c / G;
-        sl[c] = c < tok * G && i < i1 ? -a.lse[(q.q0 + i) * a.H + f * G + c % G] * kLog2e : 0.f;
-      }
+      for (int e = 0; e < 4; ++e) sl[lane + 32 * e] = -l2[e] * kLog2e;  // (not looked at past the block's rows)
       __syncwarp();  // the bytes are expected before the phase can complete
       mbar_arrive(bar_full + st);
+      fetch(n + 1);
       issued = n + 1;
     }
     // drain: every issued load has landed before the CTA may exit
     if (lane == 0) {
       if (!mbar_wait(bar_k, 0, kWaitLimitNs)) record_status(a.status, kStatusTimeout);
-      for (int n = issued > S ? issued - S : 0; n < issued && ok; ++n)
+      for (int n = issued > S ? issued - S : 0; n < issued; ++n)
         if (!mbar_wait(bar_full + (n % S), (n / S) & 1, kWaitLimitNs)) {
           record_status(a.status, kStatusTimeout);
           break;
@@ -146,35 +193,33 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   } else if (warp == kMma) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
-      constexpr uint32_t kIdS = idesc_f16kind(kTile, kTile, false, kFmt);
-      const uint32_t k_lo = smem_u32(smem) >> 4;
-      bool ok = wt.wait(bar_k, 0);
-      for (int n = 0; n < cnt && ok; ++n) {
-        ok = wt.wait(bar_full + n % S, (n / S) & 1);
-        if (ok && n >= 2) ok = wt.wait(bar_r + (n & 1), ((n >> 1) - 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t q_lo = smem_u32(sStage + (n % S) * LL::kStageBytes) >> 4;
+    constexpr uint32_t kIdS = idesc_f16kind(kTile, kTile, false, kFmt);
+    const uint32_t leader = elect_leader();
+    const uint32_t k_lo = (smem_u32(smem) >> 4) | (1u << 16), ring_lo = smem_u32(sStage) >> 4;
+    bool ok = wt.wait_warp(bar_k, 0);
+    for (int n = 0; n < cnt && ok; ++n) {
+      ok = wt.wait_warp(bar_full + n % S, (n / S) & 1);
+      if (ok && n >= kSlots) ok = wt.wait_warp(bar_r + n % kSlots, (n / kSlots - 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t q_lo = (ring_lo + (n % S) * (LL::kStageBytes >> 4)) | (1u << 16);
 #pragma unroll
-        for (int pn = 0; pn < kPanels; ++pn)
+      for (int pn = 0; pn < kPanels; ++pn)
 #pragma unroll
-          for (int kk = 0; kk < LL::kPanelElems / 16; ++kk)
-            mma_ss(tmem + kTile * (n & 1), desc_from(((k_lo + pn * (kPanelBytes >> 4)) | (1u << 16)) + kk * 2, kDescHi),
-                   desc_from(((q_lo + pn * (kPanelBytes >> 4)) | (1u << 16)) + kk * 2, kDescHi), kIdS,
-                   (pn > 0 || kk > 0) ? 1u : 0u);
-        tc_commit(bar_s + (n & 1));
-        tc_commit(bar_empty + n % S);
-      }
-      // drain: all issued MMAs complete before TMEM is released
-      tc_commit(bar_drain);
-      if (!mbar_wait(bar_drain, 0, kWaitLimitNs)) record_status(a.status, kStatusTimeout);
+        for (int kk = 0; kk < LL::kPanelElems / 16; ++kk)
+          mma_ss_if(leader, tmem + kTile * (n % kSlots), desc_from(k_lo + pn * (kPanelBytes >> 4) + kk * 2, kDescHi),
+                    desc_from(q_lo + pn * (kPanelBytes >> 4) + kk * 2, kDescHi), kIdS, (pn > 0 || kk > 0) ? 1u : 0u);
+      tc_commit_if(leader, bar_s + n % kSlots);
+      tc_commit_if(leader, bar_empty + n % S);
     }
+    // drain: all issued MMAs complete before TMEM is released
+    tc_commit_if(leader, bar_drain);
+    if (!mbar_wait(bar_drain, 0, kWaitLimitNs)) record_status(a.status, kStatusTimeout);
   } else {
     // ------------------------------------------------------------ exponentials and sums
     const int wg = warp >> 2;
     const int j = j0 + 32 * (warp & 3) + lane;  // TMEM lane = key
-    const uint32_t s_col = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kTile * wg;
+    const uint32_t s_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint64_t sc2 = f32x2(a.scale_log2, a.scale_log2);
     uint64_t acc[2] = {0, 0};
     bool ok = true;
@@ -189,31 +234,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int hi = (a.window == 0 || j < a.sinks || to > n_tok ? n_tok : to < 0 ? 0 : (int)to) * G;
       const bool whole = __all_sync(0xffffffffu, lo == 0 && hi == kTile);
       ok = wt.wait_warp(bar_full + st, (n / S) & 1);
-      if (ok) ok = wt.wait_warp(bar_s + wg, (n >> 1) & 1);
+      if (ok) ok = wt.wait_warp(bar_s + n % kSlots, (n / kSlots) & 1);
       if (!ok) break;
       tc_fence_after();
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t sr[32];
-        LN_TMEM_LD32(s_col + 32 * w, sr);
-        tmem_wait_ld();
-        const uint32_t keep = below(hi - 32 * w) & ~below(lo - 32 * w);
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 l4 = *reinterpret_cast<const float4*>(sl + 32 * w + c);
-          float x[4];
-          f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sc2, f32x2(l4.x, l4.y)),
-                      x[0], x[1]);
-          f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sc2, f32x2(l4.z, l4.w)),
-                      x[2], x[3]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = whole || ((keep >> (c + e)) & 1) ? ex2(x[e]) : 0.f;
-          acc[0] = add_f32x2(acc[0], f32x2(x[0], x[1]));
-          acc[1] = add_f32x2(acc[1], f32x2(x[2], x[3]));
-        }
-      }
+      const uint32_t s_col = s_lane + kTile * (n % kSlots);
+      if (whole)
+        sum_block<false>(s_col, sl, sc2, lo, hi, acc);
+      else
+        sum_block<true>(s_col, sl, sc2, lo, hi, acc);
       tc_fence_before();
-      mbar_arrive(bar_r + wg);
+      mbar_arrive(bar_r + n % kSlots);
       mbar_arrive(bar_empty + st);
     }
     float t0, t1;

@@ -255,18 +255,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         kKeys ? f : f * G, first + st * (kKeys ? kTile : tok), s);
     }
     // key-centric: -lse (log2 domain) and -delta of a block's rows, fetched a
-    // block ahead (their latency would otherwise stand between the loads);
-    // zero where there is no row
+    // block ahead (their latency would otherwise stand between the loads)
     float l2[2] = {0.f, 0.f}, dl[2] = {0.f, 0.f};
     const int c_tok[2] = {lane / G, (lane + 32) / G}, c_head[2] = {lane % G, (lane + 32) % G};
+    // (loaded from a valid address in any case: a load under a condition is
+    // waited for where the condition ends)
     auto fetch = [&](int n) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = i0 + n * tok + c_tok[e];
-        const bool in = n < cnt && c_tok[e] < tok && i < N;
-        const int64_t idx = ((int64_t)s * a.H + f * G + c_head[e]) * N + i;
-        l2[e] = in ? a.lse[idx] : 0.f;
-        dl[e] = in ? g.delta[idx] : 0.f;
+        const int64_t idx = ((int64_t)s * a.H + f * G + c_head[e]) * N + (i < N ? i : N - 1);
+        l2[e] = a.lse[idx];
+        dl[e] = g.delta[idx];
       }
     };
     if (kKeys) fetch(0);
