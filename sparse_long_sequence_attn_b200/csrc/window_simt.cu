@@ -59,20 +59,44 @@ __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat
 template <>
 __device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
 
-// 64 rows of D elements into shared memory as fp32; off(r) is the row's
-// element offset, negative for a row of zeros.
+// 64 rows of D elements on their way to shared memory: fetched into registers
+// (16 bytes at a time; off(r) is a row's element offset, negative for a row of
+// zeros), then stored as fp32.  A block is fetched while the one before is
+// computed.
+template <typename T, int D>
+struct Fetch {
+  static constexpr int kVec = 16 / sizeof(T);  // elements of a 16-byte load
+  static constexpr int kChunks = D / kVec;
+  static constexpr int kAll = kT * kChunks, kN = (kAll + kThreads - 1) / kThreads;
+  uint4 x[kN];
+  template <typename Off>
+  __device__ __forceinline__ void get(const T* src, Off off) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int e = threadIdx.x + i * kThreads;
+      const int64_t o = kAll % kThreads == 0 || e < kAll ? off(e / kChunks) : -1;
+      x[i] = o < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src + o + (e % kChunks) * kVec);
+    }
+  }
+  __device__ __forceinline__ void put(float* dst) const {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int e = threadIdx.x + i * kThreads;
+      if (kAll % kThreads != 0 && e >= kAll) continue;
+      T t[kVec];
+      *reinterpret_cast<uint4*>(t) = x[i];
+      float* o = dst + (e / kChunks) * L<D>::kStride + (e % kChunks) * kVec;
+#pragma unroll
+      for (int j = 0; j < kVec; j += 4)
+        *reinterpret_cast<float4*>(o + j) = make_float4(to_f<T>(t[j]), to_f<T>(t[j + 1]), to_f<T>(t[j + 2]), to_f<T>(t[j + 3]));
+    }
+  }
+};
 template <typename T, int D, typename Off>
 __device__ __forceinline__ void load_rows(float* dst, const T* src, Off off) {
-  constexpr int kVec = 16 / sizeof(T);  // elements of a 16-byte load
-  constexpr int kChunks = D / kVec;
-  for (int e = threadIdx.x; e < kT * kChunks; e += kThreads) {
-    const int r = e / kChunks, c = (e % kChunks) * kVec;
-    const int64_t o = off(r);
-    T x[kVec];
-    *reinterpret_cast<uint4*>(x) = o < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src + o + c);
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) dst[r * L<D>::kStride + c + i] = to_f<T>(x[i]);
-  }
+  Fetch<T, D> f;
+  f.get(src, off);
+  f.put(dst);
 }
 
 // acc[r][c] = <A row 4 ty + r, B row tx + 16 c>
@@ -168,8 +192,9 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) float sm[];
   float* sQ = sm;
-  float* sKV = sm + L<D>::kTile;
-  float* sP = sm + 2 * L<D>::kTile;
+  float* sK = sm + L<D>::kTile;
+  float* sV = sm + 2 * L<D>::kTile;
+  float* sP = sm + 3 * L<D>::kTile;
   Rows R;
   R.s = blockIdx.y / a.Hkv;
   R.f = blockIdx.y % a.Hkv;
@@ -190,14 +215,23 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a) {
     x[r] = 4 * ty + r < R.n ? R.pos(4 * ty + r) : -1;
   }
   const BlockList bl = blocks_of<kT>(a, R.pos(0), R.pos(R.n - 1));
-  for (int n = 0; n < bl.count; ++n) {
+  Fetch<T, D> fk, fv;
+  auto fetch = [&](int n) {
     const int j0 = bl.at(n) * kT;
     auto row = [&](int r) -> int64_t { return j0 + r < R.q.kv ? kv_row(a, R.q, R.s, R.f, j0 + r) : -1; };
+    fk.get(static_cast<const T*>(a.k), row);
+    fv.get(static_cast<const T*>(a.v), row);
+  };
+  if (bl.count > 0) fetch(0);
+  for (int n = 0; n < bl.count; ++n) {
+    const int j0 = bl.at(n) * kT;
     __syncthreads();
-    load_rows<T, D>(sKV, static_cast<const T*>(a.k), row);
+    fk.put(sK);
+    fv.put(sV);
     __syncthreads();
+    if (n + 1 < bl.count) fetch(n + 1);
     float s[4][4];
-    dots<D>(sQ, sKV, ty, tx, s);
+    dots<D>(sQ, sK, ty, tx, s);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       float mx = -INFINITY;
@@ -222,9 +256,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a) {
       for (int c = 0; c < L<D>::kC; ++c) acc[r][c] *= corr;
     }
     __syncthreads();
-    load_rows<T, D>(sKV, static_cast<const T*>(a.v), row);
-    __syncthreads();
-    accumulate<D>(sP, sKV, ty, tx, acc);
+    accumulate<D>(sP, sV, ty, tx, acc);
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -356,13 +388,21 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a, const Wi
     x[r] = in ? R.pos(i) : -1;
   }
   const BlockList bl = blocks_of<kT>(a, R.pos(0), R.pos(R.n - 1));
-  for (int n = 0; n < bl.count; ++n) {
+  Fetch<T, D> fk, fv;
+  auto fetch = [&](int n) {
     const int j0 = bl.at(n) * kT;
     auto row = [&](int r) -> int64_t { return j0 + r < R.q.kv ? kv_row(a, R.q, R.s, R.f, j0 + r) : -1; };
+    fk.get(static_cast<const T*>(a.k), row);
+    fv.get(static_cast<const T*>(a.v), row);
+  };
+  if (bl.count > 0) fetch(0);
+  for (int n = 0; n < bl.count; ++n) {
+    const int j0 = bl.at(n) * kT;
     __syncthreads();
-    load_rows<T, D>(sK, static_cast<const T*>(a.k), row);
-    load_rows<T, D>(sV, static_cast<const T*>(a.v), row);
+    fk.put(sK);
+    fv.put(sV);
     __syncthreads();
+    if (n + 1 < bl.count) fetch(n + 1);
     float s[4][4], dp[4][4];
     dots<D>(sQ, sK, ty, tx, s);
     dots<D>(sO, sV, ty, tx, dp);
@@ -407,18 +447,33 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a, const W
   load_rows<T, D>(sK, static_cast<const T*>(a.k), krow);
   load_rows<T, D>(sV, static_cast<const T*>(a.v), krow);
   float dk[4][L<D>::kC] = {}, dv[4][L<D>::kC] = {};
-  for (int r0 = i0 * a.G; r0 < i1 * a.G; r0 += kT) {
-    Rows R{q, s, f, a.G, r0, i1 * a.G - r0 < kT ? i1 * a.G - r0 : kT};
+  Fetch<T, D> fq, fo;
+  float l2 = 0.f, dl = 0.f;  // of row threadIdx.x
+  auto rows_at = [&](int r0) { return Rows{q, s, f, a.G, r0, i1 * a.G - r0 < kT ? i1 * a.G - r0 : kT}; };
+  auto fetch = [&](int r0) {
+    const Rows R = rows_at(r0);
     auto qrow = [&](int r) { return r < R.n ? R.elem(r, a.H, D) : -1; };
+    fq.get(static_cast<const T*>(a.q), qrow);
+    fo.get(static_cast<const T*>(g.dout), qrow);
+    const int r = threadIdx.x;
+    if (r < R.n) {
+      const int64_t at = lse_index(a, q, s, R.token(r), R.head(r));
+      l2 = a.lse[at] * kLog2e;
+      dl = g.delta[at];
+    }
+  };
+  if (i0 < i1) fetch(i0 * a.G);
+  for (int r0 = i0 * a.G; r0 < i1 * a.G; r0 += kT) {
+    const Rows R = rows_at(r0);
     __syncthreads();
-    load_rows<T, D>(sQ, static_cast<const T*>(a.q), qrow);
-    load_rows<T, D>(sO, static_cast<const T*>(g.dout), qrow);
-    for (int r = threadIdx.x; r < kT; r += kThreads) {
-      const int64_t at = r < R.n ? lse_index(a, q, s, R.token(r), R.head(r)) : 0;
-      s_lse[r] = r < R.n ? a.lse[at] * kLog2e : 0.f;
-      s_delta[r] = r < R.n ? g.delta[at] : 0.f;
+    fq.put(sQ);
+    fo.put(sO);
+    if (threadIdx.x < kT) {
+      s_lse[threadIdx.x] = l2;
+      s_delta[threadIdx.x] = dl;
     }
     __syncthreads();
+    if (r0 + kT < i1 * a.G) fetch(r0 + kT);
     float st[4][4], dp[4][4];
     dots<D>(sK, sQ, ty, tx, st);
     dots<D>(sV, sO, ty, tx, dp);
@@ -501,7 +556,7 @@ int ok_launch() { return cudaGetLastError() == cudaSuccess ? LONGNET_OK : LONGNE
 
 template <typename T, int D>
 int fwd(const AttnArgs& a, cudaStream_t st) {
-  const int smem = (2 * L<D>::kTile + kT * kPS) * 4;
+  const int smem = (3 * L<D>::kTile + kT * kPS) * 4;
   auto fn = fwd_kernel<T, D>;
   if (!set_smem((const void*)fn, smem)) return LONGNET_ERR_CUDA;
   const int64_t tiles = ((int64_t)a.nq_max * a.G + kT - 1) / kT;
