@@ -1,12 +1,21 @@
 // The backward of the sliding-window attention on the tensor cores (tcgen05),
 // bf16 and fp16, D = 16, 32, 64 or 128.
 //
-// Mathematics.  With P = e^{s - lse} and delta = <dout, out> (from the forward's
-// rounded out, as the call gets it), dS = P (dout V^T - delta):
+// Mathematics.  With P = e^{s - lse} and delta = <dout, out>, dS = P (dout V^T -
+// delta):
 //   dV = P^T dout, dK = dS^T Q / sqrt(D), dQ = dS K / sqrt(D).
 // P and dS are computed in fp32 and rounded to the input format for their
 // products (the tensor cores take 16-bit operands); every sum is fp32 and each
-// gradient is rounded once, when it is written.
+// gradient is rounded once, when it is written.  Two measures against what the
+// roundings cost:
+//   - delta from the forward's out carries that tensor's rounding, which shows
+//     in dS where few keys are seen (and dout V^T - delta nearly cancels).  Up
+//     to kExactKeys visible keys, delta is summed as P dout V^T in fp32 instead,
+//     by a first pass over the same blocks (relative error of dq and dk at a
+//     window of 64: 2.6e-3 -> 2.35e-3, where the plain 32-bit form rounded once
+//     has 1.7e-3);
+//   - in fp16, P is rounded as 2^8 P, since a weight of one in thousands of keys
+//     is below that format's normal range; dV is scaled back at the end.
 //
 // Design.  Two kernels, so that no gradient row is summed by two CTAs and no
 // atomics are needed (the same bits every run), at the price of computing the
@@ -68,8 +77,11 @@ struct __align__(64) BMaps {
   CUtensorMap t[2], b[2];  // the tiles' two tensors, the blocks' two
 };
 
+constexpr int kExactKeys = 512;
+
 struct BPlan {
   int tokens;    // of a tile (query-centric) or of a block (key-centric)
+  int exact;     // query-centric: delta by a pass of its own
   KeyPlan key;
 };
 
@@ -80,7 +92,11 @@ struct Run {
 
 // P and dS of 32 streamed rows for this thread's tile row, packed in pairs:
 // P = 2^(s scale log2(e) - lse log2(e)), dS = P (dP - delta); 0 where keep has
-// no bit.
+// no bit.  Key-centric in fp16, P is 2^8 P (its lse says so) and dP and delta
+// come times 2^-8.
+template <int kFmt>
+constexpr float kPScale = kFmt == kFmtF16 ? 256.f : 1.f;
+
 template <int kFmt, bool kKeys, bool kMask>
 __device__ __forceinline__ void p_ds_half(const uint32_t (&sr)[32], const uint32_t (&dr)[32], const float* nl_col,
                                           const float* nd_col, uint64_t nl_row, uint64_t nd_row, uint64_t sc2,
@@ -105,8 +121,10 @@ __device__ __forceinline__ void p_ds_half(const uint32_t (&sr)[32], const uint32
       f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[c + e]), __uint_as_float(sr[c + e + 1])), sc2, nl[e / 2]), x0,
                   x1);
       float p0 = ex2(x0), p1 = ex2(x1), d0, d1;
-      f32x2_split(mul_f32x2(f32x2(p0, p1),
-                            add_f32x2(f32x2(__uint_as_float(dr[c + e]), __uint_as_float(dr[c + e + 1])), nd[e / 2])),
+      const uint64_t dp = f32x2(__uint_as_float(dr[c + e]), __uint_as_float(dr[c + e + 1]));
+      constexpr float kDown = kKeys ? 1.f / kPScale<kFmt> : 1.f;
+      f32x2_split(mul_f32x2(f32x2(p0, p1), kDown == 1.f ? add_f32x2(dp, nd[e / 2])
+                                                        : fma_f32x2(dp, f32x2(kDown, kDown), nd[e / 2])),
                   d0, d1);
       if (kMask) {
         const bool v0 = (keep >> (c + e)) & 1, v1 = (keep >> (c + e + 1)) & 1;
@@ -238,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   Waiter wt{abort_flag, a.status, kWaitLimitNs};
+  const int passes = !kKeys && plan.exact ? 2 : 1;  // over the blocks; the first of two sums delta
   auto tile_ptr = [&](int st, int which) { return smem + (st * 2 + which) * LL::kTileBytes; };
 
   if (warp == kTma) {
@@ -271,12 +290,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (kKeys) fetch(0);
     int issued = 0;
-    for (int n = 0; n < cnt && ok; ++n) {
+    for (int n = 0; n < passes * cnt && ok; ++n) {
       const int st = n % S;
       if (n >= S) ok = wt.wait_warp(bar_empty + st, ((n / S) - 1) & 1);
       if (!ok) break;
       uint8_t* stage = sStage + st * LL::kStageBytes;
-      const int at = kKeys ? i0 + n * tok : bl.at(n) * kBlk;
+      const int at = kKeys ? i0 + n * tok : bl.at(n < cnt ? n : n - cnt) * kBlk;
       if (lane == 0) {
         mbar_expect_tx(bar_full + st,
                        (uint32_t)(2 * (kKeys ? kPanels * tok * G * LL::kRowBytes : LL::kBlkBytes)));
@@ -291,8 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* sl = reinterpret_cast<float*>(stage + 2 * LL::kBlkBytes);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          sl[lane + 32 * e] = -l2[e] * kLog2e;
-          sl[kBlk + lane + 32 * e] = -dl[e];
+          sl[lane + 32 * e] = fmaf(-l2[e], kLog2e, kFmt == kFmtF16 ? 8.f : 0.f);
+          sl[kBlk + lane + 32 * e] = -dl[e] * (1.f / kPScale<kFmt>);
         }
       }
       __syncwarp();  // the bytes are expected before the phase can complete
@@ -358,18 +377,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = wt.wait_warp(bar_tile, 0);
       if (kTiles == 2) {
         int stage = 0, phase = 0, done = 0;
-        for (int n = 0; n < cnt && ok; ++n) {
+        for (int m = 0; m < passes * cnt && ok; ++m) {
+          const bool sum = m < (passes - 1) * cnt;  // the pass for delta
+          const int n = m < cnt ? m : m - cnt;
           // (a block that only the other tile uses is released once it is
           // there, so that this warp stays within a ring of the other)
           ok = wt.wait_warp(bar_full + stage, phase);
           if (!ok) break;
           if (r.has(n)) {
             scores(stage, st);
+            if (sum) tc_commit_if(leader, bar_empty + stage);
             ok = wt.wait_warp(bar_p + st, done & 1);
             if (!ok) break;
-            grads(stage, st, done == 0);
-            tc_commit_if(leader, bar_empty + stage);
-            if (++done == r.count) tc_commit_if(leader, bar_acc + st);
+            ++done;
+            if (!sum) {
+              const int first_of_pass = (passes - 1) * r.count;
+              grads(stage, st, done == first_of_pass + 1);
+              tc_commit_if(leader, bar_empty + stage);
+              if (done == first_of_pass + r.count) tc_commit_if(leader, bar_acc + st);
+            }
           } else {
             mbar_arrive_if(leader, bar_empty + stage);
           }
@@ -420,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t0 = first + st * tok, i = t0 + row / G, h = f * G + row % G;
     const bool row_ok = kKeys ? j < N : row < tok * G && i < N;
     float lse2 = 0.f, delta = 0.f;
-    if (!kKeys) {
+    if (!kKeys && passes == 1) {
       // delta of the warp's rows, a row by kRow16 lanes (16 bytes each), kept
       // by the row's lane and left for the key-centric kernel
       constexpr int kRow16 = kD / 8, kRows = 32 / kRow16;
@@ -449,40 +475,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mine = __shfl_sync(0xffffffffu, d, (lane % kRows) * kRow16);
         if (lane / kRows == r0 / kRows) delta = mine;
       }
-      if (row_ok) {
-        const int64_t idx = ((int64_t)s * a.H + h) * N + i;
-        lse2 = a.lse[idx] * kLog2e;
-        g.delta[idx] = delta;
-      }
     }
+    const int64_t stat = ((int64_t)s * a.H + h) * N + i;  // of lse and delta
+    if (!kKeys && row_ok) lse2 = a.lse[stat] * kLog2e;
     const uint64_t sc2 = f32x2(a.scale_log2, a.scale_log2);
-    const uint64_t nl_row = f32x2(-lse2, -lse2), nd_row = f32x2(-delta, -delta);
+    const uint64_t nl_row = f32x2(-lse2, -lse2);
     const Run r = run_of(st);
     int done = 0;
     bool ok = true;
+    // query-centric: the columns of block n that this row sees, as bits
+    auto seen = [&](int n, uint32_t& keep0, uint32_t& keep1) {
+      const int j0 = bl.at(n) * kBlk;
+      const int hi = row_ok ? i - j0 + 1 : 0, lo = i - j0 - a.window + 1, sk = a.sinks - j0;
+      keep0 = below(hi) & (~below(lo) | below(sk));
+      keep1 = below(hi - 32) & (~below(lo - 32) | below(sk - 32));
+    };
+    if (!kKeys && passes == 2) {
+      // delta = sum of P dP over the row
+      uint64_t acc = 0;
+      for (int n = r.begin; n < r.end && ok; ++n) {
+        ok = wt.wait_warp(bar_s + st, done & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t keep[2];
+        seen(n, keep[0], keep[1]);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t sr[32], dr[32];
+          LN_TMEM_LD32(slot + 32 * hf, sr);
+          LN_TMEM_LD32(slot + 64 + 32 * hf, dr);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            float x0, x1;
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sc2, nl_row), x0, x1);
+            const bool v0 = (keep[hf] >> c) & 1, v1 = (keep[hf] >> (c + 1)) & 1;
+            // (an unseen pair's dP may be anything, where a row is no token's)
+            acc = fma_f32x2(f32x2(v0 ? ex2(x0) : 0.f, v1 ? ex2(x1) : 0.f),
+                            f32x2(v0 ? __uint_as_float(dr[c]) : 0.f, v1 ? __uint_as_float(dr[c + 1]) : 0.f), acc);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(bar_p + st);
+        ++done;
+      }
+      float d0, d1;
+      f32x2_split(acc, d0, d1);
+      delta = d0 + d1;
+    }
+    if (!kKeys && row_ok) g.delta[stat] = delta;  // the key-centric kernel's
+    const uint64_t nd_row = f32x2(-delta, -delta);
     for (int n = r.begin; n < r.end && ok; n += r.step) {
       const float* sl = reinterpret_cast<const float*>(sStage + (n % S) * LL::kStageBytes + 2 * LL::kBlkBytes);
-      // the columns [lo, hi) that pair with this row, and below sk
-      int lo, hi, sk;
+      uint32_t keep0, keep1;  // the columns that pair with this row, as bits
       if (kKeys) {
         const int b0 = i0 + n * tok;
         const int n_tok = i1 - b0 < tok ? i1 - b0 : tok;
         const int from = j - b0, to = j + a.window - b0;  // tokens
-        lo = (from < 0 ? 0 : from > kBlk ? kBlk : from) * G;
-        hi = (j < a.sinks || to > n_tok ? n_tok : to < 0 ? 0 : to) * G;
-        sk = 0;
+        const int lo = (from < 0 ? 0 : from > kBlk ? kBlk : from) * G;
+        const int hi = (j < a.sinks || to > n_tok ? n_tok : to < 0 ? 0 : to) * G;
+        keep0 = below(hi) & ~below(lo);
+        keep1 = below(hi - 32) & ~below(lo - 32);
       } else {
-        const int j0 = bl.at(n) * kBlk;
-        hi = row_ok ? i - j0 + 1 : 0;
-        lo = i - j0 - a.window + 1;
-        sk = a.sinks - j0;
+        seen(n, keep0, keep1);
       }
       if (kKeys) ok = wt.wait_warp(bar_full + n % S, (n / S) & 1);
       if (ok) ok = wt.wait_warp(bar_s + st, done & 1);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t keep0 = below(hi) & (~below(lo) | below(sk));
-      const uint32_t keep1 = below(hi - 32) & (~below(lo - 32) | below(sk - 32));
       const bool whole = __all_sync(0xffffffffu, (keep0 & keep1) == 0xffffffffu);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
@@ -516,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int w = 0; w < (kKeys ? 2 : 1); ++w) {
         if (kTiles == 1 && w != st) continue;
         // w = 0: dV or dQ, w = 1: dK
-        const float sc = kKeys && w == 0 ? 1.f : a.scale;
+        const float sc = kKeys && w == 0 ? 1.f / kPScale<kFmt> : a.scale;
         const uint32_t acc = tmem + lane_base + kColAcc + (kTiles == 2 ? (kKeys ? 2 : 1) * kD * st : 0) + w * kD;
         uint16_t* dst = kKeys ? static_cast<uint16_t*>(w == 0 ? g.dv : g.dk) + (((int64_t)s * N + j) * a.Hkv + f) * kD
                               : static_cast<uint16_t*>(g.dq) + (((int64_t)s * N + i) * a.H + h) * kD;
@@ -584,6 +644,8 @@ int launch_typed(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream)
   BPlan pk, pq;
   pk.tokens = kBlk / a.G;
   pq.tokens = kTile / a.G;
+  pk.exact = 0;
+  pq.exact = (int64_t)a.window + a.sinks <= kExactKeys || a.nq_max <= kExactKeys;
   using LK = B<kD, true>;
   using LQ = B<kD, false>;
   pk.key = pq.key =
