@@ -632,20 +632,22 @@ int launch_key_reduce(const AttnArgs& a, const WindowBwdArgs& g, const KeyPlan& 
   return ws::ok_launch();
 }
 
-// A far item has about as many queries as a tile's window holds (so it costs
-// what an ordinary tile does), at least 4 tiles' worth, at most 64 items a
-// tile.  With more than 16 sink tiles there are enough of them to fill the GPU
-// without: each then takes all its queries itself.  Near ranges: so many
-// that there are about `ctas` items, of at least min_blocks blocks of 64 query
-// rows each.
+// Near ranges: so many that there are about `ctas` items, of at least min_blocks
+// blocks of 64 query rows each, at most 16 a tile.  (Not to even out the last
+// wave of many tiles: every tile then has partials, and adding them took 83 us
+// for 16K tokens of 8 heads at D = 128, more than the wave.)  A far item has
+// about as many queries as a near one, up to half as many more where the items
+// then fit the waves that the tiles need anyway, and at least 64; a tile has at
+// most 64.  With more than 16 sink tiles there are enough of them to fill the
+// GPU without: each then takes all its queries itself.
 KeyPlan key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, int64_t sinks, int tile,
                  int min_blocks, int ctas) {
   KeyPlan k = {tile, (int)((N + tile - 1) / tile), 1, 0, 0, 0};
   if (window > N) window = N;
   if (sinks > N) sinks = N;
-  const int64_t reach = tile + window < N ? tile + window : N;
+  const int64_t pairs = S * Hkv, reach = tile + window < N ? tile + window : N;
   const int64_t blocks = reach * (H / Hkv) / 64;
-  int64_t near = ctas / (k.tiles * S * Hkv);
+  int64_t near = ctas / (k.tiles * pairs);
   if (near > blocks / min_blocks) near = blocks / min_blocks;
   if (near > 16) near = 16;
   if (near > 1) k.near = (int)near;
@@ -659,10 +661,14 @@ KeyPlan key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, i
   int64_t chunk = (window + tile) / k.near;
   if (chunk < 4 * tile / k.near) chunk = 4 * tile / k.near;
   if (chunk < 64) chunk = 64;
-  if ((past + chunk - 1) / chunk > 64) chunk = (past + 63) / 64;
+  int64_t n = (past + chunk - 1) / chunk;
+  if (n > 64) n = 64;
+  const int64_t fewest = (2 * past + 3 * chunk - 1) / (3 * chunk), items = pairs * k.tiles * k.near;
+  const int64_t room = ((items + ctas - 1) / ctas * ctas - items) / (pairs * t);
+  if (room >= fewest && room < n) n = room;
   k.sink_tiles = (int)t;
-  k.chunk = (int)chunk;
-  k.chunks = (int)((past + chunk - 1) / chunk);
+  k.chunk = (int)((past + n - 1) / n);
+  k.chunks = (int)((past + k.chunk - 1) / k.chunk);
   return k;
 }
 
