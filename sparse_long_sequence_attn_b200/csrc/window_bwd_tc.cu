@@ -35,6 +35,12 @@
 // of two tiles that share every streamed block; key-centric at D = 128 the
 // accumulators of one tile fill the rest of TMEM, and the slots take
 // alternate blocks.
+// The compute warps are held up by what they read from shared memory: a column's
+// -lse and -delta, the same for all 32 lanes, cost a load's full bandwidth (512
+// bytes of registers for 16).  Key-centric up to D = 64 they are therefore added
+// by the tensor cores: the tiles get a further 16 operand columns, constants,
+// and the blocks three parts of each number in the input format (24 bits or
+// more of it), which makes the scores s - lse / scale and dP - delta.
 // Warps 0-3 and 4-7 compute, warp 8 loads (TMA; its lanes fetch lse and
 // delta), warps 9 and 10 issue, one for each tile (one tile: warp 9 alone, as
 // both slots add to the same accumulators).  Every wait is bounded.
@@ -65,10 +71,16 @@ struct B : Panels<kD> {
   static constexpr int kTiles = kKeys && kD > 64 ? 1 : 2;
   static constexpr int kTileBytes = kTile * kD * 2;
   static constexpr int kBlkBytes = kBlk * kD * 2;
-  static constexpr int kStageBytes = 2 * kBlkBytes + (kKeys ? 1024 : 0);  // two blocks, then -lse and -delta
+  // Key-centric up to D = 64, -lse and -delta come into the scores as one more
+  // step of the products (kFold), from extra operand columns; at D = 128 the
+  // compute warps add them from shared memory.
+  static constexpr bool kFold = kKeys && kD <= 64;
+  static constexpr int kFoldBytes = kFold ? kTile * 32 : 0;  // the tiles' extra columns: 128 rows of 16
+  static constexpr int kStageBytes = 2 * kBlkBytes + (kFold ? 2 * kBlk * 32 : kKeys ? 1024 : 0);  // two blocks, then these
   static constexpr int kStages = kD == 128 ? (kKeys ? 4 : 3) : 6;
   static constexpr int kStage0 = kTiles * 2 * kTileBytes;
-  static constexpr int kBars = kStage0 + kStages * kStageBytes;
+  static constexpr int kFold0 = kStage0 + kStages * kStageBytes;
+  static constexpr int kBars = kFold0 + kFoldBytes;
   // one CTA per SM at every D: its TMEM columns are all of the SM's
   static constexpr int kSmem = kBars + 512 + 1024 > 120 * 1024 ? kBars + 512 + 1024 : 120 * 1024;
 };
@@ -96,6 +108,48 @@ struct Run {
 // come times 2^-8.
 template <int kFmt>
 constexpr float kPScale = kFmt == kFmtF16 ? 256.f : 1.f;
+
+// x as three parts of the input format whose sum, times the tiles' constant
+// kUnit, is x to 2^-24 or better.  fp16: kUnit 256 keeps parts of |x| up to 1.6e7
+// in range, and what is lost below its range under 1e-5.
+template <int kFmt>
+constexpr float kUnit = kFmt == kFmtF16 ? 256.f : 1.f;
+template <int kFmt>
+__device__ __forceinline__ uint4 three_parts(float x) {
+  x *= 1.f / kUnit<kFmt>;
+  float hi, mid, none;
+  unpack2<kFmt>(pack2<kFmt>(x, 0.f), hi, none);
+  unpack2<kFmt>(pack2<kFmt>(x - hi, 0.f), mid, none);
+  return make_uint4(pack2<kFmt>(hi, mid), pack2<kFmt>(x - hi - mid, 0.f), 0u, 0u);
+}
+// Byte of 16-byte chunk c of row r of the extra columns (32-byte rows and swizzle).
+__device__ __forceinline__ int fold_at(int r, int c) { return r * 32 + ((c ^ ((r >> 2) & 1)) << 4); }
+
+// The same with -lse and -delta already in sr (times the softmax scale) and dr.
+template <int kFmt, bool kMask>
+__device__ __forceinline__ void p_ds_folded(const uint32_t (&sr)[32], const uint32_t (&dr)[32], uint64_t sc2,
+                                            uint32_t keep, uint32_t (&pk)[16], uint32_t (&dk)[16]) {
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) {
+    float x0, x1;
+    const uint64_t s2 = f32x2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+    // fp16: 2^8 P for dV, P for dS
+    f32x2_split(kPScale<kFmt> == 1.f ? mul_f32x2(s2, sc2) : fma_f32x2(s2, sc2, f32x2(8.f, 8.f)), x0, x1);
+    float p0 = ex2(x0), p1 = ex2(x1), d0, d1;
+    uint64_t pp = f32x2(p0, p1);
+    if (kPScale<kFmt> != 1.f) pp = mul_f32x2(pp, f32x2(1.f / kPScale<kFmt>, 1.f / kPScale<kFmt>));
+    f32x2_split(mul_f32x2(pp, f32x2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1]))), d0, d1);
+    if (kMask) {
+      const bool v0 = (keep >> c) & 1, v1 = (keep >> (c + 1)) & 1;
+      p0 = v0 ? p0 : 0.f;
+      p1 = v1 ? p1 : 0.f;
+      d0 = v0 ? d0 : 0.f;
+      d1 = v1 ? d1 : 0.f;
+    }
+    pk[c / 2] = pack2<kFmt>(p0, p1);
+    dk[c / 2] = pack2<kFmt>(d0, d1);
+  }
+}
 
 template <int kFmt, bool kKeys, bool kMask>
 __device__ __forceinline__ void p_ds_half(const uint32_t (&sr)[32], const uint32_t (&dr)[32], const float* nl_col,
@@ -233,6 +287,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
+  if (LL::kFold) {
+    // the tiles' extra columns, three constants and zeros, and the blocks'
+    // second chunk of theirs, zeros
+    const uint32_t one = pack2<kFmt>(kUnit<kFmt>, kUnit<kFmt>);
+    for (int e = threadIdx.x; e < kTile * 2; e += kThreads)
+      *reinterpret_cast<uint4*>(smem + LL::kFold0 + fold_at(e >> 1, e & 1)) =
+          (e & 1) ? make_uint4(0, 0, 0, 0) : make_uint4(one, one & 0xffffu, 0, 0);
+    for (int e = threadIdx.x; e < S * 2 * kBlk; e += kThreads)
+      *reinterpret_cast<uint4*>(sStage + (e / (2 * kBlk)) * LL::kStageBytes + 2 * LL::kBlkBytes +
+                                (e / kBlk % 2) * kBlk * 32 + fold_at(e % kBlk, 1)) = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
   if (kKeys && tok * G < kBlk) {
     // rows of a block that no token has: zeros, as the products read them
     const int rows = kBlk - tok * G, chunks = LL::kRowBytes / 16;
@@ -306,7 +372,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_4d(stage + w * LL::kBlkBytes + pn * kBlkPanel, &maps.b[w], bar_full + st, LL::kPanelElems * pn,
                         kKeys ? f * G : f, at, s);
       }
-      if (kKeys) {
+      if (LL::kFold) {
+        uint8_t* fold = stage + 2 * LL::kBlkBytes;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          *reinterpret_cast<uint4*>(fold + fold_at(lane + 32 * e, 0)) = three_parts<kFmt>(-l2[e] / a.scale);
+          *reinterpret_cast<uint4*>(fold + kBlk * 32 + fold_at(lane + 32 * e, 0)) = three_parts<kFmt>(-dl[e]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      } else if (kKeys) {
         float* sl = reinterpret_cast<float*>(stage + 2 * LL::kBlkBytes);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -354,6 +428,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_ss_if(leader, tmem + 128 * slot + 64 * w, desc_from(t_lo[w] + pn * (kTilePanel >> 4) + kk * 2, kDescHi),
                         desc_from(b_lo + w * (LL::kBlkBytes >> 4) + pn * (kBlkPanel >> 4) + kk * 2, kDescHi), kIdScore,
                         (pn > 0 || kk > 0) ? 1u : 0u);
+        if (LL::kFold) {
+          constexpr uint32_t kHi = (uint32_t)(8 * 32 >> 4) | (1u << 14) | (6u << 29);  // 32-byte rows and swizzle
+          const uint32_t fa = (smem_u32(smem + LL::kFold0) >> 4) | (1u << 16);
+          const uint32_t fb = b_lo + (2 * LL::kBlkBytes >> 4);
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            mma_ss_if(leader, tmem + 128 * slot + 64 * w, desc_from(fa, kHi), desc_from(fb + w * (kBlk * 32 >> 4), kHi),
+                      kIdScore, 1u);
+        }
         tc_commit_if(leader, bar_s + slot);
       };
       // the gradient products of the block in `stage`, P and dS in slot `slot`
@@ -539,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         seen(n, keep0, keep1);
       }
-      if (kKeys) ok = wt.wait_warp(bar_full + n % S, (n / S) & 1);
+      if (kKeys && !LL::kFold) ok = wt.wait_warp(bar_full + n % S, (n / S) & 1);  // for what sl holds
       if (ok) ok = wt.wait_warp(bar_s + st, done & 1);
       if (!ok) break;
       tc_fence_after();
@@ -550,7 +633,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         LN_TMEM_LD32(slot + 32 * hf, sr);
         LN_TMEM_LD32(slot + 64 + 32 * hf, dr);
         tmem_wait_ld();
-        if (whole)
+        if (LL::kFold) {
+          if (whole)
+            p_ds_folded<kFmt, false>(sr, dr, sc2, 0, pk, dk);
+          else
+            p_ds_folded<kFmt, true>(sr, dr, sc2, hf ? keep1 : keep0, pk, dk);
+        } else if (whole)
           p_ds_half<kFmt, kKeys, false>(sr, dr, sl + 32 * hf, sl + kBlk + 32 * hf, nl_row, nd_row, sc2, 0, pk, dk);
         else
           p_ds_half<kFmt, kKeys, true>(sr, dr, sl + 32 * hf, sl + kBlk + 32 * hf, nl_row, nd_row, sc2,
