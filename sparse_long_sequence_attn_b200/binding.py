@@ -6,7 +6,9 @@ library is missing, loading raises: there is no fallback of any kind.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from typing import Sequence, Tuple
 
@@ -500,6 +502,11 @@ def dilated_attention(q, k, v, patterns, causal: bool = True, qk_norm: bool = Fa
 _functions = {}
 
 
+def _on(stream):
+    """Allocations and calls of one entry point on `stream`, when one is given."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _call(name: str, t: torch.Tensor, stream, *args) -> None:
     """Call the library with t's device current; the stream (default: torch's
     current stream there) is the last argument.  Raises LongNetError on a
@@ -549,6 +556,7 @@ def longnet_window_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o
           int(impl))
 
 
+@functools.lru_cache(maxsize=1024)
 def longnet_window_bwd_workspace_bytes(B: int, N: int, H: int, Hkv: int, D: int, window: int, sinks: int,
                                        dtype: torch.dtype) -> int:
     """Device workspace bytes longnet_window_attn_bwd needs."""
@@ -585,9 +593,10 @@ def window_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, 
     """Allocate out (and lse) with torch and run longnet_window_attn_fwd.
     Returns (out, lse)."""
     B, N, H, _ = q.shape
-    out = torch.empty_like(q)
-    lse = torch.empty((B, H, N), device=q.device, dtype=torch.float32) if want_lse else None
-    longnet_window_attn_fwd(q, k, v, out, lse, window, sinks, impl, stream)
+    with _on(stream):
+        out = torch.empty_like(q)
+        lse = torch.empty((B, H, N), device=q.device, dtype=torch.float32) if want_lse else None
+        longnet_window_attn_fwd(q, k, v, out, lse, window, sinks, impl, stream)
     return out, lse
 
 
@@ -596,10 +605,11 @@ def window_attn_bwd(q, k, v, out, lse, dout, window: int, sinks: int = 0, impl: 
     """Allocate dq, dk, dv (and the workspace) with torch and run the backward
     matching window_attn.  Returns (dq, dk, dv)."""
     B, N, H, D = q.shape
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    ws = torch.empty(longnet_window_bwd_workspace_bytes(B, N, H, k.shape[2], D, window, sinks, q.dtype),
-                     dtype=torch.uint8, device=q.device)
-    longnet_window_attn_bwd(q, k, v, out, lse, dout.contiguous(), dq, dk, dv, window, sinks, ws, impl, stream)
+    with _on(stream):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        ws = torch.empty(longnet_window_bwd_workspace_bytes(B, N, H, k.shape[2], D, window, sinks, q.dtype),
+                         dtype=torch.uint8, device=q.device)
+        longnet_window_attn_bwd(q, k, v, out, lse, dout.contiguous(), dq, dk, dv, window, sinks, ws, impl, stream)
     return dq, dk, dv
 
 
@@ -657,6 +667,7 @@ def paged_append(k_tok: torch.Tensor, v_tok: torch.Tensor, k_pages: torch.Tensor
           table.data_ptr(), T, S, Hkv, D, n_pages, page, max_pages, _dtype_code(k_tok))
 
 
+@functools.lru_cache(maxsize=1024)
 def longnet_paged_workspace_bytes(S: int, max_q: int, H: int, Hkv: int, D: int, page: int, max_pages: int,
                                   window: int, sinks: int, dtype: torch.dtype, weights: bool = False) -> int:
     """Device workspace bytes longnet_paged_attn_fwd needs."""
@@ -691,16 +702,18 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, cu
     LongNetError on a non-zero status."""
     n_pages, page, Hkv, D, S, max_pages = _cache_sizes(k_pages, table)
     T, H, dt = q.shape[0], q.shape[1], q.dtype
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if lse is None else lse
+    if out is None or lse is None or workspace is None:
+        with _on(stream):
+            out = torch.empty_like(q) if out is None else out
+            lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if lse is None else lse
+            if workspace is None:
+                workspace = paged_workspace(q, k_pages, table, max_q, window, sinks, weights is not None)
     _check(q, ("q", q, (T, H, D), dt), ("k_pages", k_pages, k_pages.shape, dt),
            ("v_pages", v_pages, k_pages.shape, dt), ("out", out, (T, H, D), dt), ("lse", lse, (T, H), torch.float32),
            ("cu_q", cu_q, (S + 1,), torch.int32), ("kv_len", kv_len, (S,), torch.int32),
            ("table", table, table.shape, torch.int32))
     if weights is not None:
         _check(q, ("weights", weights, (S, Hkv, max_pages * page), torch.float32))
-    if workspace is None:
-        workspace = paged_workspace(q, k_pages, table, max_q, window, sinks, weights is not None)
     _check(q, ("workspace", workspace, workspace.shape, workspace.dtype))
     _call("longnet_paged_attn_fwd", q, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
           lse.data_ptr(), None if weights is None else weights.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
@@ -728,9 +741,11 @@ def cache_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, weights: torch.Ten
            ("k_out", k_out, (n_out, page, Hkv, D), dt), ("v_out", v_out, (n_out, page, Hkv, D), dt),
            ("weights", weights, (S, Hkv, max_pages * page), torch.float32), ("kv_len", kv_len, (S,), torch.int32),
            ("table", table, table.shape, torch.int32), ("new_table", new_table, (S, max_out), torch.int32))
-    kept = torch.empty((S, Hkv, max(int(budget), 0)), dtype=torch.int32, device=at)
-    new_len = torch.empty((S,), dtype=torch.int32, device=at)
-    new_weights = torch.empty((S, Hkv, max_out * page), dtype=torch.float32, device=at)
+    with _on(stream):
+        # (a budget out of range is refused by the library)
+        kept = torch.empty((S, Hkv, min(max(int(budget), 0), max_out * page)), dtype=torch.int32, device=at)
+        new_len = torch.empty((S,), dtype=torch.int32, device=at)
+        new_weights = torch.empty((S, Hkv, max_out * page), dtype=torch.float32, device=at)
     _call("longnet_cache_evict", k_pages, stream, k_pages.data_ptr(), v_pages.data_ptr(), weights.data_ptr(),
           kv_len.data_ptr(), table.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), new_weights.data_ptr(),
           new_len.data_ptr(), kept.data_ptr(), new_table.data_ptr(), S, Hkv, D, n_pages, page, max_pages, n_out,

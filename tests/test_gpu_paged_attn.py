@@ -28,6 +28,12 @@ CASES = {
     "chunks, group of 7, sinks past a block": ([(90, 1100)], 7, 1, 32, 16, 64, 140),
     "long chunk over a long cache": ([(140, 6000)], 2, 1, 64, 256, 0, 0),
     "more tokens than keys": ([(5, 3), (40, 8)], 2, 1, 64, 16, 0, 0),
+    "no new tokens": ([(0, 100), (0, 0)], 4, 2, 64, 16, 0, 0),
+    "wider groups than a tile": ([(2, 300), (1, 20)], 130, 1, 32, 16, 0, 0),
+    "group of a whole tile": ([(3, 200), (1, 90)], 128, 1, 64, 32, 50, 2),
+    "many short sequences": ([(1 + i % 3, 3 + i % 40) for i in range(330)], 20, 1, 16, 8, 0, 0),
+    "very many sequences": ([(1, 1 + i % 17) for i in range(2100)], 1, 1, 16, 8, 0, 0),
+    "window, long cache, few tokens": ([(6, 9000), (2, 4000)], 8, 1, 128, 64, 3000, 5),
 }
 
 
@@ -62,7 +68,10 @@ def families(dtype):
 def refused(impl, case, dtype, more=0):
     """The few-token family takes at most 16 query rows per key/value head."""
     seqs, H, Hkv = CASES[case][:3]
-    return impl == bd.LONGNET_IMPL_DECODE and (max(n for n, _ in seqs) + more) * (H // Hkv) > 16
+    if impl == bd.LONGNET_IMPL_TCGEN05:
+        return H // Hkv > 128
+    return impl == bd.LONGNET_IMPL_DECODE and ((max(1, *(n for n, _ in seqs)) + more) * (H // Hkv) > 16
+                                               or len(seqs) > 2048)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
@@ -71,11 +80,12 @@ def test_attention_and_weights(case, dtype):
     cache, q, nq, cu, window, sinks = setup(case, dtype)
     out, lse, w, b_out = paged_reference(cache, q, nq, window, sinks)
     n = sum(nq)
+    top = max(1, *nq)
     for impl in families(dtype):
         if refused(impl, case, dtype):
             continue
-        for max_q in (max(nq), max(nq) + 3):
-            if refused(impl, case, dtype, max_q - max(nq)):
+        for max_q in (top, top + 3):
+            if refused(impl, case, dtype, max_q - top):
                 with pytest.raises(bd.LongNetError):
                     attend(cache, q, cu, max_q, window, sinks, impl)
                 continue
@@ -86,13 +96,13 @@ def test_attention_and_weights(case, dtype):
             assert bool((got[n:] == 7).all()) and bool((got_lse[n:] == 7).all()), "rows of no sequence were written"
         start = torch.rand(w.shape, device="cuda")
         weights = start.clone()
-        again, again_lse = attend(cache, q, cu, max(nq), window, sinks, impl, weights)
+        again, again_lse = attend(cache, q, cu, top, window, sinks, impl, weights)
         assert bd.longnet_last_device_status() == 0
         within(f"out with weights {impl}", again[:n], out[:n], b_out[:n])
         # a weight is a sum of e^{s - lse} in fp32
         within(f"weights {impl}", weights, start.double() + w, 1e-4 * w + 1e-6)
         twice = start.clone()
-        attend(cache, q, cu, max(nq), window, sinks, impl, twice)
+        attend(cache, q, cu, top, window, sinks, impl, twice)
         assert torch.equal(weights, twice), "the same inputs gave other bits"
 
 
@@ -316,3 +326,63 @@ def test_no_tokens_at_all():
     bd.paged_append(q[:, :1].contiguous(), q[:, :1].contiguous(), cache.k_pages, cache.v_pages, cu, cache.kv_len,
                     cache.table)
     assert bd.longnet_last_device_status() == 0
+
+
+def test_pages_past_two_to_the_31_elements():
+    """The last pages of a pool whose offsets do not fit 32 bits."""
+    Hkv, D, page, H = 8, 128, 256, 16
+    n_pages = 2 ** 31 // (Hkv * D * page) + 12
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB")
+    lens, nq = [700, 300], [3, 1]
+    cache = Cache(lens, page, Hkv, D, BF16, 11, wide=4)
+    k_pages = torch.empty((n_pages, page, Hkv, D), dtype=BF16, device="cuda")
+    v_pages = torch.empty_like(k_pages)
+    small = cache.k_pages.shape[0]
+    k_pages[-small:], v_pages[-small:] = cache.k_pages, cache.v_pages
+    table = torch.where(cache.table >= 0, cache.table + (n_pages - small), cache.table)
+    q = torch.randn((4, H, D), device="cuda").to(BF16)
+    cu = torch.tensor([0, 3, 4], dtype=torch.int32, device="cuda")
+    out, lse, w, b = paged_reference(cache, q, nq, 0, 0)
+    k_tok = torch.cat([cache.k[0][-3:], cache.k[1][-1:]]).contiguous()
+    v_tok = torch.cat([cache.v[0][-3:], cache.v[1][-1:]]).contiguous()
+    for s in range(2):  # what the append has to bring back
+        for x in range(lens[s] - nq[s], lens[s]):
+            k_pages[int(table[s, x // page]), x % page] = 0
+    bd.paged_append(k_tok, v_tok, k_pages, v_pages, cu, cache.kv_len, table)
+    for impl in families(BF16):
+        weights = torch.zeros_like(w, dtype=torch.float32)
+        got, _ = bd.paged_attn(q, k_pages, v_pages, cu, cache.kv_len, table, 3, weights=weights, impl=impl)
+        within(f"out {impl}", got, out, b)
+        within(f"weights {impl}", weights, w, 1e-4 * w + 1e-6)
+    new_table = n_pages - small - torch.tensor([[1, 2], [3, 4]], dtype=torch.int32, device="cuda")
+    kept, new_len, _ = bd.cache_evict(k_pages, v_pages, w.float(), cache.kv_len, table, k_pages, v_pages, new_table, 400, 4,
+                                      50)
+    assert bd.longnet_last_device_status() == 0 and new_len.tolist() == [400, 300]
+    for s in range(2):
+        n = int(new_len[s])
+        j = torch.arange(n, device="cuda")
+        for f in (0, Hkv - 1):
+            got = k_pages[new_table[s].long()[j // page], j % page, f]
+            assert torch.equal(got, cache.k[s][kept[s, f, :n].long(), f])
+
+
+def test_two_calls_at_once():
+    """Two streams, each with its own workspace, give what one after the other gives."""
+    cache, q, nq, cu, _, _ = setup("chunks", BF16)
+    d_cache, d_q, d_nq, d_cu, _, _ = setup("single tokens, long", BF16)
+    want = attend(cache, q, cu, 257, 0, 0, AUTO)
+    d_want = attend(d_cache, d_q, d_cu, 1, 0, 0, AUTO)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(5):
+        with torch.cuda.stream(streams[0]):
+            a = attend(cache, q, cu, 257, 0, 0, AUTO)
+        with torch.cuda.stream(streams[1]):
+            b = attend(d_cache, d_q, d_cu, 1, 0, 0, AUTO)
+        got.append((a, b))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert torch.equal(a[0], want[0]) and torch.equal(b[0], d_want[0])

@@ -30,6 +30,10 @@ SHAPES = [
     (1, 520, 24, 1, 32, 250, 0),
     (1, 1000, 1, 1, 128, 1000, 0),
     (1, 2600, 1, 1, 64, 40, 2600),
+    (2, 70, 80, 1, 16, 30, 3),    # more shared heads than a streamed block has rows
+    (1, 40, 130, 1, 32, 17, 0),   # and than a tile has
+    (2, 1030, 8, 4, 64, 515, 1),
+    (1, 5000, 2, 1, 32, 70, 300),
 ]
 
 
@@ -171,3 +175,34 @@ def test_scores_far_apart(scale):
     # a score's fp32 error grows with the score: |s| FP32 / 4 beside the bound of its unit size
     within("out", out, ref[0], bound[0] + 1e-5 * scale * 4)
     within("lse", lse, ref[1], bound[1] + 1e-6 * ref[1].abs())
+
+
+def test_given_stream():
+    """Outputs and workspaces belong to the stream that the call is given."""
+    q, k, v, dout = inputs(1, 400, 4, 2, 64, BF16, 3)
+    want = run(q, k, v, dout, 60, 2, AUTO)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        out, lse = bd.window_attn(q, k, v, 60, 2, stream=side)
+        grads = bd.window_attn_bwd(q, k, v, out, lse, dout, 60, 2, stream=side)
+        junk = [torch.full_like(q, 9.0) for _ in range(4)]  # what the freed workspace must not be given to meanwhile
+    side.synchronize()
+    del junk
+    assert all(torch.equal(a, b) for a, b in zip((out, lse, *grads), want))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_backward_of_scores_far_apart(dtype, D):
+    """Scores of some hundreds: lse is far from 0, and one or two keys take a row."""
+    scale = 20.0
+    q, k, v, dout = inputs(1, 300, 4, 2, D, dtype, 7)
+    q = (q.float() * scale).to(dtype)
+    ref, bound = window_reference(q, k, v, dout, 120, 8)
+    got = run(q, k, v, dout, 120, 8, AUTO)
+    # a score of |s| <= 6 sqrt(D) scale / 4 carries its fp32 error, 2^-22 of it at most, into P, which
+    # the products with terms of up to 5 (v, dout) or 5 scale (q) then spread over a row's or key's terms
+    slack = 2.0 ** -22 * 6 * D ** 0.5 * scale / 4 * 5 * 5 * D ** 0.5
+    for name, a, r, b in zip(("out", "lse", "dq", "dk", "dv"), got, ref, bound):
+        within(name, a, r, b + (1e-6 * r.abs() if name == "lse" else slack * (scale if name == "dk" else 1)))
