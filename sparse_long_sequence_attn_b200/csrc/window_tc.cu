@@ -492,7 +492,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int h = f * a.G + row % a.G;
       const bool whole = !kPaged || (!alternate && pieces == 1);
       const int64_t prow = ((int64_t)slot * 2 + st) * plan.slot_rows + row;
-      if (!whole) {
+      if (!whole && kD >= 64 && !alternate) {
+        if constexpr (kD >= 64)  // (a slot has 128 rows of this stream)
+          store_rows_f32<kD>(sQ + st * LL::kQBytes, o_col, done > 0, inv, 32 * (warp & 3), lane,
+                             plan.part_out + prow * kD);
+      } else if (!whole) {
         constexpr int kChunk = kD < 32 ? kD : 32;
 #pragma unroll 1
         for (int c0 = 0; c0 < kD; c0 += kChunk) {
