@@ -175,7 +175,8 @@ __device__ __forceinline__ KeyItem key_item(const AttnArgs& a, const KeyPlan& k,
 KeyPlan key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, int64_t sinks, int tile, int min_blocks,
                  int ctas);
 int64_t key_partial_floats(const KeyPlan& k, int64_t S, int64_t Hkv, int64_t D);
-constexpr int kSimtKeyTile = 64, kSimtMinBlocks = 2, kSimtCtas = 296;  // of key_plan, for the SIMT family
+// the SIMT family's
+KeyPlan simt_key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, int64_t sinks);
 int launch_window_bwd_simt(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream);
 // delta = <dout, out> of every row, and the last step both families share.
 int launch_window_delta(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream);

@@ -77,7 +77,7 @@ int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 int64_t bwd_workspace(int64_t B, int64_t N, int64_t H, int64_t Hkv, int64_t D, int64_t window, int64_t sinks) {
   window = window < N ? window : N;
   sinks = sinks < N ? sinks : N;
-  const KeyPlan ks = key_plan(B, N, H, Hkv, window, sinks, kSimtKeyTile, kSimtMinBlocks, kSimtCtas);
+  const KeyPlan ks = simt_key_plan(B, N, H, Hkv, window, sinks);
   const KeyPlan kt = key_plan(B, N, H, Hkv, window, sinks, window_bwd_tc_tile(D), kTcMinBlocks, kTcCtas);
   const int64_t simt = key_partial_floats(ks, B, Hkv, D), tc = key_partial_floats(kt, B, Hkv, D);
   return round256(4 * B * N * H) + round256(4 * (simt > tc ? simt : tc));

@@ -9,11 +9,11 @@
 // delta = <dout, out>: P = e^{s - lse}, dS = P (dout V^T - delta),
 // dQ = dS K / sqrt(D), dK = dS^T Q / sqrt(D), dV = P^T dout.
 //
-// Layout.  A CTA of 16 x 16 threads owns 64 rows (packed query rows, or keys)
-// and streams 64-row blocks of the other side through shared memory as fp32;
-// a thread holds a 4 x 4 piece of the 64 x 64 scores and a 4 x D/16 piece of
-// the accumulators, so every value read from shared memory feeds four
-// multiply-adds.  Rows are padded by four floats, which keeps the 16-byte
+// Layout.  A CTA of 16 x 16 threads owns 16 RT rows (packed query rows, or keys;
+// RT = 4, or 1 for small problems) and streams 64-row blocks of the other
+// side through shared memory as fp32; a thread holds an RT x 4 piece of the
+// scores and an RT x D/16 piece of the accumulators, so that at RT = 4 every
+// value read from shared memory feeds four multiply-adds.  Rows are padded by four floats, which keeps the 16-byte
 // reads of 8 lanes in different banks.  The bound is the fp32 pipe (no TF32:
 // fp32 inputs keep fp32 products).
 #include <cuda_bf16.h>
@@ -30,6 +30,7 @@ namespace ws {
 constexpr int kT = 64;        // rows of a tile, keys of a block
 constexpr int kThreads = 256;
 constexpr int kPS = kT + 4;   // row stride of a score tile
+constexpr int kSms = 148;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -59,15 +60,15 @@ __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat
 template <>
 __device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
 
-// 64 rows of D elements on their way to shared memory: fetched into registers
+// ROWS rows of D elements on their way to shared memory: fetched into registers
 // (16 bytes at a time; off(r) is a row's element offset, negative for a row of
 // zeros), then stored as fp32.  A block is fetched while the one before is
 // computed.
-template <typename T, int D>
+template <typename T, int D, int ROWS = kT>
 struct Fetch {
   static constexpr int kVec = 16 / sizeof(T);  // elements of a 16-byte load
   static constexpr int kChunks = D / kVec;
-  static constexpr int kAll = kT * kChunks, kN = (kAll + kThreads - 1) / kThreads;
+  static constexpr int kAll = ROWS * kChunks, kN = (kAll + kThreads - 1) / kThreads;
   uint4 x[kN];
   template <typename Off>
   __device__ __forceinline__ void get(const T* src, Off off) {
@@ -92,31 +93,30 @@ struct Fetch {
     }
   }
 };
-template <typename T, int D, typename Off>
+template <typename T, int D, int ROWS = kT, typename Off>
 __device__ __forceinline__ void load_rows(float* dst, const T* src, Off off) {
-  Fetch<T, D> f;
+  Fetch<T, D, ROWS> f;
   f.get(src, off);
   f.put(dst);
 }
 
-// acc[r][c] = <A row 4 ty + r, B row tx + 16 c>
-template <int D>
-__device__ __forceinline__ void dots(const float* A, const float* B, int ty, int tx, float (&acc)[4][4]) {
+// acc[r][c] = <A row RT ty + r, B row tx + 16 c>
+template <int D, int RT>
+__device__ __forceinline__ void dots(const float* A, const float* B, int ty, int tx, float (&acc)[RT][4]) {
   constexpr int ST = L<D>::kStride;
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+  for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
 #pragma unroll 4
   for (int d = 0; d < D; d += 4) {
-    float4 x[4], y[4];
+    float4 x[RT], y[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      x[r] = *reinterpret_cast<const float4*>(A + (4 * ty + r) * ST + d);
-      y[r] = *reinterpret_cast<const float4*>(B + (tx + 16 * r) * ST + d);
-    }
+    for (int r = 0; r < RT; ++r) x[r] = *reinterpret_cast<const float4*>(A + (RT * ty + r) * ST + d);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < 4; ++r) y[r] = *reinterpret_cast<const float4*>(B + (tx + 16 * r) * ST + d);
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         acc[r][c] = fmaf(x[r].x, y[c].x, acc[r][c]);
@@ -127,17 +127,17 @@ __device__ __forceinline__ void dots(const float* A, const float* B, int ty, int
   }
 }
 
-// acc[r][c] += sum_j P[4 ty + r][j] X[j][col c]
-template <int D>
+// acc[r][c] += sum_j P[RT ty + r][j] X[j][col c]
+template <int D, int RT>
 __device__ __forceinline__ void accumulate(const float* P, const float* X, int ty, int tx,
-                                           float (&acc)[4][L<D>::kC]) {
+                                           float (&acc)[RT][L<D>::kC]) {
   constexpr int ST = L<D>::kStride, C = L<D>::kC, V = L<D>::kV;
 #pragma unroll 2
   for (int j = 0; j < kT; j += 4) {
-    float p[4][4];
+    float p[RT][4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float4 t = *reinterpret_cast<const float4*>(P + (4 * ty + r) * kPS + j);
+    for (int r = 0; r < RT; ++r) {
+      const float4 t = *reinterpret_cast<const float4*>(P + (RT * ty + r) * kPS + j);
       p[r][0] = t.x;
       p[r][1] = t.y;
       p[r][2] = t.z;
@@ -162,7 +162,7 @@ __device__ __forceinline__ void accumulate(const float* P, const float* X, int t
 #pragma unroll
         for (int u = 0; u < V; ++u)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[r][c0 + u] = fmaf(p[r][i], x[u], acc[r][c0 + u]);
+          for (int r = 0; r < RT; ++r) acc[r][c0 + u] = fmaf(p[r][i], x[u], acc[r][c0 + u]);
       }
   }
 }
@@ -188,31 +188,32 @@ struct Rows {
   __device__ int64_t elem(int r, int H, int D) const { return ((q.q0 + token(r)) * H + head(r)) * (int64_t)D; }
 };
 
-template <typename T, int D>
+template <typename T, int D, int RT>
 __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a) {
+  constexpr int kR = 16 * RT;  // rows of the tile
   extern __shared__ __align__(16) float sm[];
   float* sQ = sm;
-  float* sK = sm + L<D>::kTile;
-  float* sV = sm + 2 * L<D>::kTile;
-  float* sP = sm + 3 * L<D>::kTile;
+  float* sK = sm + kR * L<D>::kStride;
+  float* sV = sK + L<D>::kTile;
+  float* sP = sV + L<D>::kTile;
   Rows R;
   R.s = blockIdx.y / a.Hkv;
   R.f = blockIdx.y % a.Hkv;
   R.q = seq_of(a, R.s);
   R.G = a.G;
-  R.r0 = (gridDim.x - 1 - blockIdx.x) * kT;  // the longest rows first
+  R.r0 = (gridDim.x - 1 - blockIdx.x) * kR;  // the longest rows first
   R.n = R.q.nq * a.G - R.r0;
   if (R.n <= 0) return;
-  if (R.n > kT) R.n = kT;
+  if (R.n > kR) R.n = kR;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  load_rows<T, D>(sQ, static_cast<const T*>(a.q), [&](int r) { return r < R.n ? R.elem(r, a.H, D) : -1; });
-  float acc[4][L<D>::kC] = {}, m[4], l[4];
-  int x[4];
+  load_rows<T, D, kR>(sQ, static_cast<const T*>(a.q), [&](int r) { return r < R.n ? R.elem(r, a.H, D) : -1; });
+  float acc[RT][L<D>::kC] = {}, m[RT], l[RT];
+  int x[RT];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
+  for (int r = 0; r < RT; ++r) {
     m[r] = -INFINITY;
     l[r] = 0.f;
-    x[r] = 4 * ty + r < R.n ? R.pos(4 * ty + r) : -1;
+    x[r] = RT * ty + r < R.n ? R.pos(RT * ty + r) : -1;
   }
   const BlockList bl = blocks_of<kT>(a, R.pos(0), R.pos(R.n - 1));
   Fetch<T, D> fk, fv;
@@ -230,10 +231,10 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a) {
     fv.put(sV);
     __syncthreads();
     if (n + 1 < bl.count) fetch(n + 1);
-    float s[4][4];
-    dots<D>(sQ, sK, ty, tx, s);
+    float s[RT][4];
+    dots<D, RT>(sQ, sK, ty, tx, s);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < RT; ++r) {
       float mx = -INFINITY;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -249,18 +250,18 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a) {
       for (int c = 0; c < 4; ++c) {
         const float p = exp2f(s[r][c] - base);
         sum += p;
-        sP[(4 * ty + r) * kPS + tx + 16 * c] = p;
+        sP[(RT * ty + r) * kPS + tx + 16 * c] = p;
       }
       l[r] = l[r] * corr + sum16(sum);
 #pragma unroll
       for (int c = 0; c < L<D>::kC; ++c) acc[r][c] *= corr;
     }
     __syncthreads();
-    accumulate<D>(sP, sV, ty, tx, acc);
+    accumulate<D, RT>(sP, sV, ty, tx, acc);
   }
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int i = 4 * ty + r;
+  for (int r = 0; r < RT; ++r) {
+    const int i = RT * ty + r;
     if (i >= R.n) continue;
     const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
     T* o = static_cast<T*>(a.out) + R.elem(i, a.H, D);
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const AttnArgs a, flo
     }
     __syncthreads();
     float st[4][4];
-    dots<D>(sK, sQ, ty, tx, st);
+    dots<D, 4>(sK, sQ, ty, tx, st);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int col = tx + 16 * c;
@@ -355,32 +356,33 @@ __global__ void __launch_bounds__(256) delta_kernel(const AttnArgs a, const T* o
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int RT>
 __global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a, const WindowBwdArgs g) {
+  constexpr int kR = 16 * RT;  // rows of the tile
   extern __shared__ __align__(16) float sm[];
   float* sQ = sm;
-  float* sO = sm + L<D>::kTile;
-  float* sK = sm + 2 * L<D>::kTile;
-  float* sV = sm + 3 * L<D>::kTile;
-  float* sS = sm + 4 * L<D>::kTile;
+  float* sO = sm + kR * L<D>::kStride;
+  float* sK = sO + kR * L<D>::kStride;
+  float* sV = sK + L<D>::kTile;
+  float* sS = sV + L<D>::kTile;
   Rows R;
   R.s = blockIdx.y / a.Hkv;
   R.f = blockIdx.y % a.Hkv;
   R.q = seq_of(a, R.s);
   R.G = a.G;
-  R.r0 = (gridDim.x - 1 - blockIdx.x) * kT;
+  R.r0 = (gridDim.x - 1 - blockIdx.x) * kR;
   R.n = R.q.nq * a.G - R.r0;
   if (R.n <= 0) return;
-  if (R.n > kT) R.n = kT;
+  if (R.n > kR) R.n = kR;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   auto qrow = [&](int r) { return r < R.n ? R.elem(r, a.H, D) : -1; };
-  load_rows<T, D>(sQ, static_cast<const T*>(a.q), qrow);
-  load_rows<T, D>(sO, static_cast<const T*>(g.dout), qrow);
-  float acc[4][L<D>::kC] = {}, lse2[4], delta[4];
-  int x[4];
+  load_rows<T, D, kR>(sQ, static_cast<const T*>(a.q), qrow);
+  load_rows<T, D, kR>(sO, static_cast<const T*>(g.dout), qrow);
+  float acc[RT][L<D>::kC] = {}, lse2[RT], delta[RT];
+  int x[RT];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int i = 4 * ty + r;
+  for (int r = 0; r < RT; ++r) {
+    const int i = RT * ty + r;
     const bool in = i < R.n;
     const int64_t at = in ? lse_index(a, R.q, R.s, R.token(i), R.head(i)) : 0;
     lse2[r] = in ? a.lse[at] * kLog2e : 0.f;
@@ -403,23 +405,23 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a, const Wi
     fv.put(sV);
     __syncthreads();
     if (n + 1 < bl.count) fetch(n + 1);
-    float s[4][4], dp[4][4];
-    dots<D>(sQ, sK, ty, tx, s);
-    dots<D>(sO, sV, ty, tx, dp);
+    float s[RT][4], dp[RT][4];
+    dots<D, RT>(sQ, sK, ty, tx, s);
+    dots<D, RT>(sO, sV, ty, tx, dp);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const float p =
             sees(a, x[r], j0 + tx + 16 * c) ? exp2f(fmaf(s[r][c], a.scale_log2, -lse2[r])) : 0.f;
-        sS[(4 * ty + r) * kPS + tx + 16 * c] = p * (dp[r][c] - delta[r]);
+        sS[(RT * ty + r) * kPS + tx + 16 * c] = p * (dp[r][c] - delta[r]);
       }
     __syncthreads();
-    accumulate<D>(sS, sK, ty, tx, acc);
+    accumulate<D, RT>(sS, sK, ty, tx, acc);
   }
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int i = 4 * ty + r;
+  for (int r = 0; r < RT; ++r) {
+    const int i = RT * ty + r;
     if (i >= R.n) continue;
     T* o = static_cast<T*>(g.dq) + R.elem(i, a.H, D);
 #pragma unroll
@@ -427,26 +429,27 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a, const Wi
   }
 }
 
-// dk, dv of a tile of 64 keys over one item's queries.
-template <typename T, int D>
+// dk, dv of a tile of 16 RT keys over one item's queries.
+template <typename T, int D, int RT>
 __global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a, const WindowBwdArgs g, const KeyPlan kp) {
+  constexpr int kR = 16 * RT;
   extern __shared__ __align__(16) float sm[];
   float* sK = sm;
-  float* sV = sm + L<D>::kTile;
-  float* sQ = sm + 2 * L<D>::kTile;
-  float* sO = sm + 3 * L<D>::kTile;
-  float* sP = sm + 4 * L<D>::kTile;
-  float* sS = sP + kT * kPS;
+  float* sV = sm + kR * L<D>::kStride;
+  float* sQ = sV + kR * L<D>::kStride;
+  float* sO = sQ + L<D>::kTile;
+  float* sP = sO + L<D>::kTile;
+  float* sS = sP + kR * kPS;
   __shared__ float s_lse[kT], s_delta[kT];
   const int s = blockIdx.y / a.Hkv, f = blockIdx.y % a.Hkv;
   const Seq q = seq_of(a, s);
   const KeyItem it = key_item(a, kp, blockIdx.x);
-  const int j0 = it.tile * kT, i0 = it.i0, i1 = it.i1;
+  const int j0 = it.tile * kR, i0 = it.i0, i1 = it.i1;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   auto krow = [&](int r) -> int64_t { return j0 + r < q.kv ? kv_row(a, q, s, f, j0 + r) : -1; };
-  load_rows<T, D>(sK, static_cast<const T*>(a.k), krow);
-  load_rows<T, D>(sV, static_cast<const T*>(a.v), krow);
-  float dk[4][L<D>::kC] = {}, dv[4][L<D>::kC] = {};
+  load_rows<T, D, kR>(sK, static_cast<const T*>(a.k), krow);
+  load_rows<T, D, kR>(sV, static_cast<const T*>(a.v), krow);
+  float dk[RT][L<D>::kC] = {}, dv[RT][L<D>::kC] = {};
   Fetch<T, D> fq, fo;
   float l2 = 0.f, dl = 0.f;  // of row threadIdx.x
   auto rows_at = [&](int r0) { return Rows{q, s, f, a.G, r0, i1 * a.G - r0 < kT ? i1 * a.G - r0 : kT}; };
@@ -474,35 +477,35 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a, const W
     }
     __syncthreads();
     if (r0 + kT < i1 * a.G) fetch(r0 + kT);
-    float st[4][4], dp[4][4];
-    dots<D>(sK, sQ, ty, tx, st);
-    dots<D>(sV, sO, ty, tx, dp);
+    float st[RT][4], dp[RT][4];
+    dots<D, RT>(sK, sQ, ty, tx, st);
+    dots<D, RT>(sV, sO, ty, tx, dp);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int col = tx + 16 * c;
       const int x = col < R.n ? R.pos(col) : -1;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
+      for (int r = 0; r < RT; ++r) {
         const float p =
-            sees(a, x, j0 + 4 * ty + r) ? exp2f(fmaf(st[r][c], a.scale_log2, -s_lse[col])) : 0.f;
-        sP[(4 * ty + r) * kPS + col] = p;
-        sS[(4 * ty + r) * kPS + col] = p * (dp[r][c] - s_delta[col]);
+            sees(a, x, j0 + RT * ty + r) ? exp2f(fmaf(st[r][c], a.scale_log2, -s_lse[col])) : 0.f;
+        sP[(RT * ty + r) * kPS + col] = p;
+        sS[(RT * ty + r) * kPS + col] = p * (dp[r][c] - s_delta[col]);
       }
     }
     __syncthreads();
-    accumulate<D>(sP, sO, ty, tx, dv);
-    accumulate<D>(sS, sQ, ty, tx, dk);
+    accumulate<D, RT>(sP, sO, ty, tx, dv);
+    accumulate<D, RT>(sS, sQ, ty, tx, dk);
   }
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int j = j0 + 4 * ty + r;
+  for (int r = 0; r < RT; ++r) {
+    const int j = j0 + RT * ty + r;
     if (it.slot >= 0) {
-      // [S Hkv][slot][dk, dv][kT][D]
-      float* p = g.partial + ((((int64_t)blockIdx.y * kp.slots() + it.slot) * 2) * kT + 4 * ty + r) * D;
+      // [S Hkv][slot][dk, dv][kR][D]
+      float* p = g.partial + ((((int64_t)blockIdx.y * kp.slots() + it.slot) * 2) * kR + RT * ty + r) * D;
 #pragma unroll
       for (int c = 0; c < L<D>::kC; ++c) {
         p[L<D>::col(tx, c)] = dk[r][c] * a.scale;
-        p[kT * D + L<D>::col(tx, c)] = dv[r][c];
+        p[kR * D + L<D>::col(tx, c)] = dv[r][c];
       }
     } else if (j < q.kv) {
       const int64_t at = ((q.q0 + j) * a.Hkv + f) * D;
@@ -554,13 +557,38 @@ bool set_smem(const void* fn, int bytes) {
 
 int ok_launch() { return cudaGetLastError() == cudaSuccess ? LONGNET_OK : LONGNET_ERR_CUDA; }
 
+// Query tiles have 64 rows, or 16 where the GPU holds all of those at once, two
+// to an SM.  A small tile reads shared memory more often for each product, and is
+// done sooner: forward and dq of 2 x 276 tokens, one head of 128, take 64 and 74 us
+// with 64 rows, 37 and 49 with 16; of 600 tokens, 4/2 heads of 64, 42 and 50 with
+// 64, 26 and 33 with 16.  (Tiles of 32 rows lie between: 32 and 38 us; and above
+// the limit they lose, 36 us, where 94 tiles of 64 rows take 32, for dq at D = 32.)
+bool small_tiles(const AttnArgs& a) {
+  return ((int64_t)a.nq_max * a.G + 15) / 16 * a.S * a.Hkv <= 2 * kSms;
+}
+
+template <typename T, int D, int RT>
+int fwd_tiles(const AttnArgs& a, cudaStream_t st) {
+  constexpr int kR = 16 * RT;
+  const int smem = (kR * L<D>::kStride + 2 * L<D>::kTile + kR * kPS) * 4;
+  auto fn = fwd_kernel<T, D, RT>;
+  if (!set_smem((const void*)fn, smem)) return LONGNET_ERR_CUDA;
+  const int64_t tiles = ((int64_t)a.nq_max * a.G + kR - 1) / kR;
+  fn<<<dim3((unsigned)tiles, (unsigned)(a.S * a.Hkv)), kThreads, smem, st>>>(a);
+  return ok_launch();
+}
 template <typename T, int D>
 int fwd(const AttnArgs& a, cudaStream_t st) {
-  const int smem = (3 * L<D>::kTile + kT * kPS) * 4;
-  auto fn = fwd_kernel<T, D>;
+  return small_tiles(a) ? fwd_tiles<T, D, 1>(a, st) : fwd_tiles<T, D, 4>(a, st);
+}
+template <typename T, int D, int RT>
+int dq_tiles(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t st) {
+  constexpr int kR = 16 * RT;
+  const int smem = (2 * kR * L<D>::kStride + 2 * L<D>::kTile + kR * kPS) * 4;
+  auto fn = dq_kernel<T, D, RT>;
   if (!set_smem((const void*)fn, smem)) return LONGNET_ERR_CUDA;
-  const int64_t tiles = ((int64_t)a.nq_max * a.G + kT - 1) / kT;
-  fn<<<dim3((unsigned)tiles, (unsigned)(a.S * a.Hkv)), kThreads, smem, st>>>(a);
+  const int64_t tiles = ((int64_t)a.nq_max * a.G + kR - 1) / kR;
+  fn<<<dim3((unsigned)tiles, (unsigned)(a.S * a.Hkv)), kThreads, smem, st>>>(a, g);
   return ok_launch();
 }
 template <typename T, int D>
@@ -572,20 +600,24 @@ int weights_sum(const AttnArgs& a, float* w, cudaStream_t st) {
   fn<<<dim3((unsigned)tiles, (unsigned)(a.S * a.Hkv)), kThreads, smem, st>>>(a, w);
   return ok_launch();
 }
+template <typename T, int D, int RT>
+int dkv_tiles(const AttnArgs& a, const WindowBwdArgs& g, const KeyPlan& kp, cudaStream_t st) {
+  constexpr int kR = 16 * RT;
+  const int smem = (2 * kR * L<D>::kStride + 2 * L<D>::kTile + 2 * kR * kPS) * 4;
+  auto fn = dkv_kernel<T, D, RT>;
+  if (!set_smem((const void*)fn, smem)) return LONGNET_ERR_CUDA;
+  fn<<<dim3((unsigned)kp.items(), (unsigned)(a.S * a.Hkv)), kThreads, smem, st>>>(a, g, kp);
+  return ok_launch();
+}
 template <typename T, int D>
 int bwd(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t st) {
   int rc = launch_window_delta(a, g, st);
   if (rc) return rc;
-  const KeyPlan kp = key_plan(a.S, a.nq_max, a.H, a.Hkv, a.window, a.sinks, kSimtKeyTile, kSimtMinBlocks, kSimtCtas);
-  const int smem_q = (4 * L<D>::kTile + kT * kPS) * 4, smem_k = smem_q + kT * kPS * 4;
-  auto fq = dq_kernel<T, D>;
-  auto fk = dkv_kernel<T, D>;
-  if (!set_smem((const void*)fq, smem_q) || !set_smem((const void*)fk, smem_k)) return LONGNET_ERR_CUDA;
-  fk<<<dim3((unsigned)kp.items(), (unsigned)(a.S * a.Hkv)), kThreads, smem_k, st>>>(a, g, kp);
-  if ((rc = ok_launch())) return rc;
-  const int64_t tiles = ((int64_t)a.nq_max * a.G + kT - 1) / kT;
-  fq<<<dim3((unsigned)tiles, (unsigned)(a.S * a.Hkv)), kThreads, smem_q, st>>>(a, g);
-  if ((rc = ok_launch())) return rc;
+  const KeyPlan kp = simt_key_plan(a.S, a.nq_max, a.H, a.Hkv, a.window, a.sinks);
+  rc = kp.tile == 16 ? dkv_tiles<T, D, 1>(a, g, kp, st) : dkv_tiles<T, D, 4>(a, g, kp, st);
+  if (rc) return rc;
+  rc = small_tiles(a) ? dq_tiles<T, D, 1>(a, g, st) : dq_tiles<T, D, 4>(a, g, st);
+  if (rc) return rc;
   return launch_key_reduce(a, g, kp, st);
 }
 template <typename T, int D>
@@ -638,8 +670,8 @@ int launch_key_reduce(const AttnArgs& a, const WindowBwdArgs& g, const KeyPlan& 
 // for 16K tokens of 8 heads at D = 128, more than the wave.)  A far item has
 // about as many queries as a near one, up to half as many more where the items
 // then fit the waves that the tiles need anyway, and at least 64; a tile has at
-// most 64.  With more than 16 sink tiles there are enough of them to fill the
-// GPU without: each then takes all its queries itself.
+// most 64.  With more than 16 sink tiles, or 1024 sinks in smaller tiles, there
+// are enough of them to fill the GPU without: each then takes all its queries itself.
 KeyPlan key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, int64_t sinks, int tile,
                  int min_blocks, int ctas) {
   KeyPlan k = {tile, (int)((N + tile - 1) / tile), 1, 0, 0, 0};
@@ -657,7 +689,7 @@ KeyPlan key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, i
   if (t <= 0 || past <= 0) return k;
   const int64_t has = (past + tile - 1) / tile;  // tiles that have any
   if (t > has) t = has;
-  if (t > 16) return k;
+  if (t > (tile < 64 ? 1024 / tile : 16)) return k;
   int64_t chunk = (window + tile) / k.near;
   if (chunk < 4 * tile / k.near) chunk = 4 * tile / k.near;
   if (chunk < 64) chunk = 64;
@@ -670,6 +702,15 @@ KeyPlan key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, i
   k.chunk = (int)((past + n - 1) / n);
   k.chunks = (int)((past + k.chunk - 1) / k.chunk);
   return k;
+}
+
+// Tiles of 64 keys, or 16 where the items of 64 would leave half of the SMs idle
+// (dk and dv of 2 x 276 tokens, one head of 128: 82 us with tiles of 64 keys, 41
+// with 16).
+KeyPlan simt_key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, int64_t sinks) {
+  const int min_blocks = 2, ctas = 2 * ws::kSms;
+  const KeyPlan k = key_plan(S, N, H, Hkv, window, sinks, 64, min_blocks, ctas);
+  return k.items() * S * Hkv >= ws::kSms / 2 ? k : key_plan(S, N, H, Hkv, window, sinks, 16, min_blocks, ctas);
 }
 
 int64_t key_partial_floats(const KeyPlan& k, int64_t S, int64_t Hkv, int64_t D) {

@@ -206,3 +206,19 @@ def test_backward_of_scores_far_apart(dtype, D):
     slack = 2.0 ** -22 * 6 * D ** 0.5 * scale / 4 * 5 * 5 * D ** 0.5
     for name, a, r, b in zip(("out", "lse", "dq", "dk", "dv"), got, ref, bound):
         within(name, a, r, b + (1e-6 * r.abs() if name == "lse" else slack * (scale if name == "dk" else 1)))
+
+
+@pytest.mark.parametrize("shape", [
+    (1, 1578, 3, 1, 64, 90, 16),    # the largest grid of 16-row tiles with a group of 3
+    (1, 1579, 3, 1, 64, 90, 16),    # and one row past it: tiles of 64
+    (1, 2500, 2, 1, 128, 300, 70),
+    (3, 800, 4, 2, 16, 65, 700),
+    (1, 2400, 1, 1, 128, 17, 1200),  # sinks over many tiles of 16 keys
+    (1, 330, 1, 1, 64, 400, 270),
+], ids=str)
+def test_fp32_tiles_of_both_sizes(shape):
+    B, N, H, Hkv, D, window, sinks = shape
+    x = inputs(B, N, H, Hkv, D, F32, 2 + N)
+    ref, bound = window_reference(*x, window, sinks)
+    for name, a, r, b in zip(("out", "lse", "dq", "dk", "dv"), run(*x, window, sinks, AUTO), ref, bound):
+        within(name, a, r, b)
