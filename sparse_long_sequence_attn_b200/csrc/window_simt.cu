@@ -100,37 +100,83 @@ __device__ __forceinline__ void load_rows(float* dst, const T* src, Off off) {
   f.put(dst);
 }
 
-// acc[r][c] = <A row RT ty + r, B row tx + 16 c>
+// Two fp32 multiply-adds in one instruction: the pipe's rate is the same, but the
+// loads beside them find the issue slots (1500 tokens, 8 heads of 128, window 500:
+// forward 201 -> 171 us, dq 236 -> 224, dk and dv 325 -> 304).
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t r) {
+  float2 x;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x.x), "=f"(x.y) : "l"(r));
+  return x;
+}
+__device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+
+// acc[r][c] = <A row RT ty + r, B row tx + 16 c>, even and odd elements apart
 template <int D, int RT>
 __device__ __forceinline__ void dots(const float* A, const float* B, int ty, int tx, float (&acc)[RT][4]) {
   constexpr int ST = L<D>::kStride;
+  uint64_t s[RT][4];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
+    for (int c = 0; c < 4; ++c) s[r][c] = 0;
 #pragma unroll 4
   for (int d = 0; d < D; d += 4) {
-    float4 x[RT], y[4];
+    ulonglong2 x[RT], y[4];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) x[r] = *reinterpret_cast<const float4*>(A + (RT * ty + r) * ST + d);
+    for (int r = 0; r < RT; ++r) x[r] = *reinterpret_cast<const ulonglong2*>(A + (RT * ty + r) * ST + d);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) y[r] = *reinterpret_cast<const float4*>(B + (tx + 16 * r) * ST + d);
+    for (int r = 0; r < 4; ++r) y[r] = *reinterpret_cast<const ulonglong2*>(B + (tx + 16 * r) * ST + d);
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        acc[r][c] = fmaf(x[r].x, y[c].x, acc[r][c]);
-        acc[r][c] = fmaf(x[r].y, y[c].y, acc[r][c]);
-        acc[r][c] = fmaf(x[r].z, y[c].z, acc[r][c]);
-        acc[r][c] = fmaf(x[r].w, y[c].w, acc[r][c]);
+        fma2(s[r][c], x[r].x, y[c].x);
+        fma2(s[r][c], x[r].y, y[c].y);
       }
   }
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float2 t = unpack2(s[r][c]);
+      acc[r][c] = t.x + t.y;
+    }
 }
+
+// The accumulators of RT rows by a thread's columns, in pairs of columns.
+template <int D, int RT>
+struct Acc {
+  static constexpr int C = L<D>::kC, kP = (C + 1) / 2;  // at D = 16 the second of the pair is unused
+  uint64_t v[RT][kP];
+  __device__ __forceinline__ Acc() {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int c = 0; c < kP; ++c) v[r][c] = 0;
+  }
+  __device__ __forceinline__ void scale(int r, float f) {
+#pragma unroll
+    for (int c = 0; c < kP; ++c) {
+      const float2 t = unpack2(v[r][c]);
+      v[r][c] = pack2(t.x * f, t.y * f);
+    }
+  }
+  __device__ __forceinline__ float at(int r, int c) const {
+    const float2 t = unpack2(v[r][c / 2]);
+    return c % 2 ? t.y : t.x;
+  }
+};
 
 // acc[r][c] += sum_j P[RT ty + r][j] X[j][col c]
 template <int D, int RT>
-__device__ __forceinline__ void accumulate(const float* P, const float* X, int ty, int tx,
-                                           float (&acc)[RT][L<D>::kC]) {
+__device__ __forceinline__ void accumulate(const float* P, const float* X, int ty, int tx, Acc<D, RT>& acc) {
   constexpr int ST = L<D>::kStride, C = L<D>::kC, V = L<D>::kV;
 #pragma unroll 2
   for (int j = 0; j < kT; j += 4) {
@@ -147,22 +193,21 @@ __device__ __forceinline__ void accumulate(const float* P, const float* X, int t
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int c0 = 0; c0 < C; c0 += V) {
-        float x[V];
         const float* src = X + (j + i) * ST + L<D>::col(tx, c0);
+        uint64_t x[(V + 1) / 2];
         if constexpr (V == 4) {
-          const float4 t = *reinterpret_cast<const float4*>(src);
+          const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(src);
           x[0] = t.x;
           x[1] = t.y;
-          x[2] = t.z;
-          x[3] = t.w;
+        } else if constexpr (V == 2) {
+          x[0] = *reinterpret_cast<const uint64_t*>(src);
         } else {
-#pragma unroll
-          for (int u = 0; u < V; ++u) x[u] = src[u];
+          x[0] = pack2(src[0], 0.f);
         }
 #pragma unroll
-        for (int u = 0; u < V; ++u)
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-          for (int r = 0; r < RT; ++r) acc[r][c0 + u] = fmaf(p[r][i], x[u], acc[r][c0 + u]);
+          for (int u = 0; u < (V + 1) / 2; ++u) fma2(acc.v[r][c0 / 2 + u], pack2(p[r][i], p[r][i]), x[u]);
       }
   }
 }
@@ -207,7 +252,8 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a) {
   if (R.n > kR) R.n = kR;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   load_rows<T, D, kR>(sQ, static_cast<const T*>(a.q), [&](int r) { return r < R.n ? R.elem(r, a.H, D) : -1; });
-  float acc[RT][L<D>::kC] = {}, m[RT], l[RT];
+  Acc<D, RT> acc;
+  float m[RT], l[RT];
   int x[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
@@ -253,8 +299,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a) {
         sP[(RT * ty + r) * kPS + tx + 16 * c] = p;
       }
       l[r] = l[r] * corr + sum16(sum);
-#pragma unroll
-      for (int c = 0; c < L<D>::kC; ++c) acc[r][c] *= corr;
+      acc.scale(r, corr);
     }
     __syncthreads();
     accumulate<D, RT>(sP, sV, ty, tx, acc);
@@ -266,7 +311,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a) {
     const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
     T* o = static_cast<T*>(a.out) + R.elem(i, a.H, D);
 #pragma unroll
-    for (int c = 0; c < L<D>::kC; ++c) o[L<D>::col(tx, c)] = from_f<T>(acc[r][c] * inv);
+    for (int c = 0; c < L<D>::kC; ++c) o[L<D>::col(tx, c)] = from_f<T>(acc.at(r, c) * inv);
     if (tx == 0 && a.lse)
       a.lse[lse_index(a, R.q, R.s, R.token(i), R.head(i))] = l[r] > 0.f ? (m[r] + log2f(l[r])) * kLn2 : -INFINITY;
   }
@@ -378,7 +423,8 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a, const Wi
   auto qrow = [&](int r) { return r < R.n ? R.elem(r, a.H, D) : -1; };
   load_rows<T, D, kR>(sQ, static_cast<const T*>(a.q), qrow);
   load_rows<T, D, kR>(sO, static_cast<const T*>(g.dout), qrow);
-  float acc[RT][L<D>::kC] = {}, lse2[RT], delta[RT];
+  Acc<D, RT> acc;
+  float lse2[RT], delta[RT];
   int x[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
@@ -425,13 +471,14 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a, const Wi
     if (i >= R.n) continue;
     T* o = static_cast<T*>(g.dq) + R.elem(i, a.H, D);
 #pragma unroll
-    for (int c = 0; c < L<D>::kC; ++c) o[L<D>::col(tx, c)] = from_f<T>(acc[r][c] * a.scale);
+    for (int c = 0; c < L<D>::kC; ++c) o[L<D>::col(tx, c)] = from_f<T>(acc.at(r, c) * a.scale);
   }
 }
 
 // dk, dv of a tile of 16 RT keys over one item's queries.
 template <typename T, int D, int RT>
-__global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a, const WindowBwdArgs g, const KeyPlan kp) {
+__global__ void __launch_bounds__(kThreads, D <= 32 ? 2 : 1)  // two to an SM: 42 -> 34 us for 997 tokens, 6/2 heads of 32
+    dkv_kernel(const AttnArgs a, const WindowBwdArgs g, const KeyPlan kp) {
   constexpr int kR = 16 * RT;
   extern __shared__ __align__(16) float sm[];
   float* sK = sm;
@@ -449,7 +496,7 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a, const W
   auto krow = [&](int r) -> int64_t { return j0 + r < q.kv ? kv_row(a, q, s, f, j0 + r) : -1; };
   load_rows<T, D, kR>(sK, static_cast<const T*>(a.k), krow);
   load_rows<T, D, kR>(sV, static_cast<const T*>(a.v), krow);
-  float dk[RT][L<D>::kC] = {}, dv[RT][L<D>::kC] = {};
+  Acc<D, RT> dk, dv;
   Fetch<T, D> fq, fo;
   float l2 = 0.f, dl = 0.f;  // of row threadIdx.x
   auto rows_at = [&](int r0) { return Rows{q, s, f, a.G, r0, i1 * a.G - r0 < kT ? i1 * a.G - r0 : kT}; };
@@ -504,15 +551,15 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const AttnArgs a, const W
       float* p = g.partial + ((((int64_t)blockIdx.y * kp.slots() + it.slot) * 2) * kR + RT * ty + r) * D;
 #pragma unroll
       for (int c = 0; c < L<D>::kC; ++c) {
-        p[L<D>::col(tx, c)] = dk[r][c] * a.scale;
-        p[kR * D + L<D>::col(tx, c)] = dv[r][c];
+        p[L<D>::col(tx, c)] = dk.at(r, c) * a.scale;
+        p[kR * D + L<D>::col(tx, c)] = dv.at(r, c);
       }
     } else if (j < q.kv) {
       const int64_t at = ((q.q0 + j) * a.Hkv + f) * D;
 #pragma unroll
       for (int c = 0; c < L<D>::kC; ++c) {
-        static_cast<T*>(g.dk)[at + L<D>::col(tx, c)] = from_f<T>(dk[r][c] * a.scale);
-        static_cast<T*>(g.dv)[at + L<D>::col(tx, c)] = from_f<T>(dv[r][c]);
+        static_cast<T*>(g.dk)[at + L<D>::col(tx, c)] = from_f<T>(dk.at(r, c) * a.scale);
+        static_cast<T*>(g.dv)[at + L<D>::col(tx, c)] = from_f<T>(dv.at(r, c));
       }
     }
   }
@@ -705,7 +752,7 @@ KeyPlan key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, i
 }
 
 // Tiles of 64 keys, or 16 where the items of 64 would leave half of the SMs idle
-// (dk and dv of 2 x 276 tokens, one head of 128: 82 us with tiles of 64 keys, 41
+// (dk and dv of 2 x 276 tokens, one head of 128: 73 us with tiles of 64 keys, 41
 // with 16).
 KeyPlan simt_key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, int64_t sinks) {
   const int min_blocks = 2, ctas = 2 * ws::kSms;
