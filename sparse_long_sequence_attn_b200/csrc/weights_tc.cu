@@ -6,7 +6,8 @@
 // S^T = K Q^T, a TMEM lane per key, and each thread sums its key's row.  No
 // second product, no exchange between threads, one addition per key and call,
 // so the result does not depend on any order.  Bound: the exponentials (16 per
-// clock and SM).
+// clock and SM: 17 us of them for three chunks of up to 1024 tokens over up to 8192
+// keys, 8/2 heads of 128, which take 37 us).
 //
 // A CTA holds a tile of 128 keys of one key/value head and streams blocks of
 // 128 packed query rows (128 / G tokens by G heads) with their lse.  Two

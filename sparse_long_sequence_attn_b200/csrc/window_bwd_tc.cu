@@ -12,8 +12,8 @@
 //     in dS where few keys are seen (and dout V^T - delta nearly cancels).  Up
 //     to kExactKeys visible keys, delta is summed as P dout V^T in fp32 instead,
 //     by a first pass over the same blocks (relative error of dq and dk at a
-//     window of 64: 2.6e-3 -> 2.35e-3, where the plain 32-bit form rounded once
-//     has 1.7e-3);
+//     window of 64: 2.6e-3 -> 2.4e-3, where the plain 32-bit form rounded once has
+//     1.7e-3);
 //   - in fp16, P is rounded as 2^8 P, since a weight of one in thousands of keys
 //     is below that format's normal range; dV is scaled back at the end.
 //
@@ -44,6 +44,11 @@
 // Warps 0-3 and 4-7 compute, warp 8 loads (TMA; its lanes fetch lse and
 // delta), warps 9 and 10 issue, one for each tile (one tile: warp 9 alone, as
 // both slots add to the same accumulators).  Every wait is bounded.
+// Bound: the compute warps' passes over S and dP (two TMEM reads, an exponential
+// and a TMEM write for each 2 x 2 D multiply-adds); the tensor cores work 20 to 42 %
+// of the cycles.  Measured, query- and key-centric: 8192 tokens, 12/4 heads of 64,
+// window 1024: 93 and 100 us; 16384 tokens, 8 heads of 128, window 4096: 489 and 498
+// us (854 TFLOP/s of the seven products).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
