@@ -17,8 +17,9 @@
 // floats, which keeps the 16-byte reads of 8 lanes in different banks.  The bound
 // is the fp32 pipe (no TF32: fp32 inputs keep fp32 products) and, for small
 // problems, a CTA's latency.  Measured, fp32, forward, dq, and dk with dv: 997
-// tokens, 6/2 heads of 32, window 200: 27, 31 and 34 us; 1500 tokens, 8 heads of 128,
+// tokens, 6/2 heads of 32, window 200: 26, 29 and 34 us; 1500 tokens, 8 heads of 128,
 // window 500: 171, 224 and 304 us (half of the pipe's rate while a CTA runs).
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -171,6 +172,13 @@ struct Acc {
       v[r][c] = pack2(t.x * f, t.y * f);
     }
   }
+  // to rows of D values
+  __device__ __forceinline__ void put(float* dst, int ty, int tx) const {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int c = 0; c < C; ++c) dst[(RT * ty + r) * D + L<D>::col(tx, c)] = at(r, c);
+  }
   __device__ __forceinline__ float at(int r, int c) const {
     const float2 t = unpack2(v[r][c / 2]);
     return c % 2 ? t.y : t.x;
@@ -226,6 +234,19 @@ __device__ __forceinline__ float max16(float x) {
   return x;
 }
 
+// A query tile's key blocks are shared by the CTAs of a cluster (1, 2, 4 or 8),
+// each with a run of them: part `rank` of `parts`.
+struct Part {
+  int rank, parts, tile;
+  __device__ Part() {
+    parts = (int)cooperative_groups::this_cluster().num_blocks();
+    rank = (int)cooperative_groups::this_cluster().block_rank();
+    tile = (gridDim.x - 1 - blockIdx.x) / parts;  // the longest rows first
+  }
+  __device__ int first(int blocks) const { return (int)((int64_t)blocks * rank / parts); }
+  __device__ int last(int blocks) const { return (int)((int64_t)blocks * (rank + 1) / parts); }
+};
+
 // A tile of packed query rows of (sequence s, key/value head f).
 struct Rows {
   Seq q;
@@ -249,7 +270,8 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a) {
   R.f = blockIdx.y % a.Hkv;
   R.q = seq_of(a, R.s);
   R.G = a.G;
-  R.r0 = (gridDim.x - 1 - blockIdx.x) * kR;  // the longest rows first
+  const Part part;
+  R.r0 = part.tile * kR;
   R.n = R.q.nq * a.G - R.r0;
   if (R.n <= 0) return;
   if (R.n > kR) R.n = kR;
@@ -272,14 +294,15 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a) {
     fk.get(static_cast<const T*>(a.k), row);
     fv.get(static_cast<const T*>(a.v), row);
   };
-  if (bl.count > 0) fetch(0);
-  for (int n = 0; n < bl.count; ++n) {
+  const int n0 = part.first(bl.count), n1 = part.last(bl.count);
+  if (n0 < n1) fetch(n0);
+  for (int n = n0; n < n1; ++n) {
     const int j0 = bl.at(n) * kT;
     __syncthreads();
     fk.put(sK);
     fv.put(sV);
     __syncthreads();
-    if (n + 1 < bl.count) fetch(n + 1);
+    if (n + 1 < n1) fetch(n + 1);
     float s[RT][4];
     dots<D, RT>(sQ, sK, ty, tx, s);
 #pragma unroll
@@ -306,6 +329,37 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a) {
     }
     __syncthreads();
     accumulate<D, RT>(sP, sV, ty, tx, acc);
+  }
+  if (part.parts > 1) {  // each CTA adds the parts of some of the rows, in order
+    auto cluster = cooperative_groups::this_cluster();
+    float* sA = sK;  // [kR][D]
+    float* sM = sK + kR * D;
+    float* sL = sM + kR;
+    __syncthreads();
+    acc.put(sA, ty, tx);
+    if (tx == 0)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        sM[RT * ty + r] = m[r];
+        sL[RT * ty + r] = l[r];
+      }
+    cluster.sync();
+    for (int e = part.rank * kThreads + threadIdx.x; e < R.n * D; e += part.parts * kThreads) {
+      const int i = e / D;
+      float top = -INFINITY, sum = 0.f, o = 0.f;
+      for (int c = 0; c < part.parts; ++c) top = fmaxf(top, cluster.map_shared_rank(sM, c)[i]);
+      const float base = top == -INFINITY ? 0.f : top;
+      for (int c = 0; c < part.parts; ++c) {
+        const float w = exp2f(cluster.map_shared_rank(sM, c)[i] - base);
+        sum = fmaf(w, cluster.map_shared_rank(sL, c)[i], sum);
+        o = fmaf(w, cluster.map_shared_rank(sA, c)[e], o);
+      }
+      static_cast<T*>(a.out)[R.elem(i, a.H, D) + e % D] = from_f<T>(o * (sum > 0.f ? 1.f / sum : 0.f));
+      if (e % D == 0 && a.lse)
+        a.lse[lse_index(a, R.q, R.s, R.token(i), R.head(i))] = sum > 0.f ? (base + log2f(sum)) * kLn2 : -INFINITY;
+    }
+    cluster.sync();  // no CTA ends while another reads its part
+    return;
   }
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
@@ -418,7 +472,8 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a, const Wi
   R.f = blockIdx.y % a.Hkv;
   R.q = seq_of(a, R.s);
   R.G = a.G;
-  R.r0 = (gridDim.x - 1 - blockIdx.x) * kR;
+  const Part part;
+  R.r0 = part.tile * kR;
   R.n = R.q.nq * a.G - R.r0;
   if (R.n <= 0) return;
   if (R.n > kR) R.n = kR;
@@ -446,14 +501,15 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a, const Wi
     fk.get(static_cast<const T*>(a.k), row);
     fv.get(static_cast<const T*>(a.v), row);
   };
-  if (bl.count > 0) fetch(0);
-  for (int n = 0; n < bl.count; ++n) {
+  const int n0 = part.first(bl.count), n1 = part.last(bl.count);
+  if (n0 < n1) fetch(n0);
+  for (int n = n0; n < n1; ++n) {
     const int j0 = bl.at(n) * kT;
     __syncthreads();
     fk.put(sK);
     fv.put(sV);
     __syncthreads();
-    if (n + 1 < bl.count) fetch(n + 1);
+    if (n + 1 < n1) fetch(n + 1);
     float s[RT][4], dp[RT][4];
     dots<D, RT>(sQ, sK, ty, tx, s);
     dots<D, RT>(sO, sV, ty, tx, dp);
@@ -467,6 +523,20 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const AttnArgs a, const Wi
       }
     __syncthreads();
     accumulate<D, RT>(sS, sK, ty, tx, acc);
+  }
+  if (part.parts > 1) {
+    auto cluster = cooperative_groups::this_cluster();
+    float* sA = sV;  // [kR][D]
+    __syncthreads();
+    acc.put(sA, ty, tx);
+    cluster.sync();
+    for (int e = part.rank * kThreads + threadIdx.x; e < R.n * D; e += part.parts * kThreads) {
+      float sum = 0.f;
+      for (int c = 0; c < part.parts; ++c) sum += cluster.map_shared_rank(sA, c)[e];
+      static_cast<T*>(g.dq)[R.elem(e / D, a.H, D) + e % D] = from_f<T>(sum * a.scale);
+    }
+    cluster.sync();
+    return;
   }
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
@@ -617,15 +687,45 @@ bool small_tiles(const AttnArgs& a) {
   return ((int64_t)a.nq_max * a.G + 15) / 16 * a.S * a.Hkv <= 2 * kSms;
 }
 
+// CTAs that share a query tile's key blocks (a cluster): doubled while the grid
+// fits two to an SM and each has a block (forward and dq of 2 x 276 tokens, one head
+// of 128: 37 and 49 us with one, 19 and 24 with 8).
+int key_parts(const AttnArgs& a, int64_t tiles, int rows) {
+  int64_t keys = a.cu_q ? (int64_t)a.max_pages << a.page_shift : a.nq_max;
+  if (a.window) {
+    const int64_t seen = (int64_t)a.window + rows / a.G + 2 + (a.sinks + kT - 1) / kT * kT;
+    if (seen < keys) keys = seen;
+  }
+  int parts = 1;
+  while (parts < 8 && tiles * a.S * a.Hkv * parts <= kSms && 2 * parts * kT <= keys + kT - 1) parts *= 2;
+  return parts;
+}
+// fn on (tiles, S Hkv) clusters of `parts` CTAs.
+template <typename... P, typename... V>
+int launch_tiles(void (*fn)(P...), const AttnArgs& a, int rows, int smem, cudaStream_t st, V&&... args) {
+  if (!set_smem((const void*)fn, smem)) return LONGNET_ERR_CUDA;
+  const int64_t tiles = ((int64_t)a.nq_max * a.G + rows - 1) / rows;
+  const int parts = key_parts(a, tiles, rows);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * parts), (unsigned)(a.S * a.Hkv));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = parts;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess) return LONGNET_OK;
+  cudaGetLastError();
+  return LONGNET_ERR_CUDA;
+}
+
 template <typename T, int D, int RT>
 int fwd_tiles(const AttnArgs& a, cudaStream_t st) {
   constexpr int kR = 16 * RT;
-  const int smem = (kR * L<D>::kStride + 2 * L<D>::kTile + kR * kPS) * 4;
-  auto fn = fwd_kernel<T, D, RT>;
-  if (!set_smem((const void*)fn, smem)) return LONGNET_ERR_CUDA;
-  const int64_t tiles = ((int64_t)a.nq_max * a.G + kR - 1) / kR;
-  fn<<<dim3((unsigned)tiles, (unsigned)(a.S * a.Hkv)), kThreads, smem, st>>>(a);
-  return ok_launch();
+  return launch_tiles(fwd_kernel<T, D, RT>, a, kR, (kR * L<D>::kStride + 2 * L<D>::kTile + kR * kPS) * 4, st, a);
 }
 template <typename T, int D>
 int fwd(const AttnArgs& a, cudaStream_t st) {
@@ -634,12 +734,7 @@ int fwd(const AttnArgs& a, cudaStream_t st) {
 template <typename T, int D, int RT>
 int dq_tiles(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t st) {
   constexpr int kR = 16 * RT;
-  const int smem = (2 * kR * L<D>::kStride + 2 * L<D>::kTile + kR * kPS) * 4;
-  auto fn = dq_kernel<T, D, RT>;
-  if (!set_smem((const void*)fn, smem)) return LONGNET_ERR_CUDA;
-  const int64_t tiles = ((int64_t)a.nq_max * a.G + kR - 1) / kR;
-  fn<<<dim3((unsigned)tiles, (unsigned)(a.S * a.Hkv)), kThreads, smem, st>>>(a, g);
-  return ok_launch();
+  return launch_tiles(dq_kernel<T, D, RT>, a, kR, (2 * kR * L<D>::kStride + 2 * L<D>::kTile + kR * kPS) * 4, st, a, g);
 }
 template <typename T, int D>
 int weights_sum(const AttnArgs& a, float* w, cudaStream_t st) {
@@ -754,13 +849,13 @@ KeyPlan key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, i
   return k;
 }
 
-// Tiles of 64 keys, or 16 where the items of 64 would leave half of the SMs idle
-// (dk and dv of 2 x 276 tokens, one head of 128: 73 us with tiles of 64 keys, 41
-// with 16).
+// Tiles of 64 keys, or 16 where the items of 64 would leave half of the SMs idle,
+// and then cut down to one block of queries (dk and dv of 2 x 276 tokens, one head of
+// 128: 73 us with tiles of 64 keys, 41 with 16, 27 so cut).
 KeyPlan simt_key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, int64_t sinks) {
-  const int min_blocks = 2, ctas = 2 * ws::kSms;
-  const KeyPlan k = key_plan(S, N, H, Hkv, window, sinks, 64, min_blocks, ctas);
-  return k.items() * S * Hkv >= ws::kSms / 2 ? k : key_plan(S, N, H, Hkv, window, sinks, 16, min_blocks, ctas);
+  const int ctas = 2 * ws::kSms;
+  const KeyPlan k = key_plan(S, N, H, Hkv, window, sinks, 64, 2, ctas);
+  return k.items() * S * Hkv >= ws::kSms / 2 ? k : key_plan(S, N, H, Hkv, window, sinks, 16, 1, ctas);
 }
 
 int64_t key_partial_floats(const KeyPlan& k, int64_t S, int64_t Hkv, int64_t D) {
