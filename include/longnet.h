@@ -432,7 +432,7 @@ int longnet_dilated_attn_bwd_ws(const void* q, const void* k, const void* v,
  *     aligned; lse: fp32 [B, H, N] or NULL.
  *   - D in {16, 32, 64, 128} (else LONGNET_ERR_UNSUPPORTED); N >= 1;
  *     window >= 1 (window >= N: plain causal attention); sinks >= 0.
- *   - B Hkv <= 65535 and N H <= 2^30, else LONGNET_ERR_UNSUPPORTED.
+ *   - H and B Hkv <= 65535, N H and B N <= 2^30, else LONGNET_ERR_UNSUPPORTED.
  *   - impl: LONGNET_IMPL_AUTO, LONGNET_IMPL_TCGEN05 (bf16 and fp16) or
  *     LONGNET_IMPL_SIMT (fp32 arithmetic, every dtype).
  *   Rows of v a query does not see may be read and multiplied by a weight of
@@ -476,7 +476,9 @@ int longnet_window_attn_bwd(const void* q, const void* k, const void* v,
  * int32, 4-byte aligned:
  *   - table [S, max_pages]: key j of sequence s lies in page
  *     table[s][j / page], slot j mod page.  Entries past a sequence's keys
- *     are not read and may hold anything.
+ *     are not read and may hold anything; those of its keys must all be
+ *     pages, also where the mask hides the keys, which may be read (and weigh
+ *     0, so they must be finite).
  *   - kv_len [S]: keys of each sequence, the new tokens' among them;
  *     0 <= kv_len <= max_pages * page.
  *   - cu_q [S + 1]: the new tokens of sequence s are the token rows

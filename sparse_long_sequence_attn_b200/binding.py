@@ -633,7 +633,12 @@ class WindowAttnFunction(torch.autograd.Function):
 
 def window_attention(q, k, v, window: int, sinks: int = 0):
     """Differentiable attention with a sliding window and sinks: out
-    [B, N, H, D], gradients through the backward."""
+    [B, N, H, D], gradients through the backward.
+
+    A step captured into a CUDA graph: let go of every output that was computed
+    eagerly from the same leaves first (warm up on a side stream, then drop it),
+    since torch adds a leaf's gradient on the stream of the leaf's live graph,
+    which a capture does not allow."""
     return WindowAttnFunction.apply(q.contiguous(), k.contiguous(), v.contiguous(), int(window), int(sinks))
 
 

@@ -222,3 +222,31 @@ def test_fp32_tiles_of_both_sizes(shape):
     ref, bound = window_reference(*x, window, sinks)
     for name, a, r, b in zip(("out", "lse", "dq", "dk", "dv"), run(*x, window, sinks, AUTO), ref, bound):
         within(name, a, r, b)
+
+
+def test_captured_training_step():
+    """Forward and backward through autograd in one graph; the eager warm-up is dropped before the capture."""
+    q, k, v, dout = inputs(2, 300, 4, 2, 64, BF16, 12)
+    leaves = [z.clone().requires_grad_() for z in (q, k, v)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        bd.window_attention(*leaves, 70, 4).backward(dout)
+    torch.cuda.current_stream().wait_stream(side)
+    for z in leaves:
+        z.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = bd.window_attention(*leaves, 70, 4)
+        out.backward(dout)
+    new = inputs(2, 300, 4, 2, 64, BF16, 13)
+    with torch.no_grad():
+        for z, n in zip((*leaves, dout), new):
+            z.copy_(n)
+    for _ in range(2):  # the second replay writes the same gradients again, it does not add to them
+        graph.replay()
+    torch.cuda.synchronize()
+    want = run(*new, 70, 4, AUTO)
+    assert torch.equal(out, want[0])
+    for z, w in zip(leaves, want[2:]):
+        assert torch.equal(z.grad, w)
