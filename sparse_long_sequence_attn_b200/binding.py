@@ -500,11 +500,12 @@ def dilated_attention(q, k, v, patterns, causal: bool = True, qk_norm: bool = Fa
 
 
 _functions = {}
+_HERE = contextlib.nullcontext()
 
 
 def _on(stream):
     """Allocations and calls of one entry point on `stream`, when one is given."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 def _call(name: str, t: torch.Tensor, stream, *args) -> None:
@@ -529,9 +530,9 @@ def _call(name: str, t: torch.Tensor, stream, *args) -> None:
 def _check(like: torch.Tensor, *wanted) -> None:
     """Tensor arguments, as (name, tensor, shape, dtype): each CUDA, on
     `like`'s device, contiguous, of this shape and dtype."""
-    at = like.get_device()
+    at = like.get_device() if like.is_cuda else None  # None: no tensor is there
     for what, t, shape, dtype in wanted:
-        if t.dtype is not dtype or t.shape != shape or t.get_device() != at or at < 0 or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != at or not t.is_contiguous():
             raise ValueError(f"{what} must be a contiguous {dtype} CUDA tensor {tuple(shape)} on {like.device}, "
                              f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
@@ -546,11 +547,18 @@ def longnet_window_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o
     one dtype (fp32/bf16/fp16); lse: contiguous fp32 [B, H, N] or None.  Raises
     LongNetError on a non-zero status."""
     B, N, H, D = q.shape
-    Hkv, dt = k.shape[2], q.dtype
-    _check(q, ("q", q, (B, N, H, D), dt), ("k", k, (B, N, Hkv, D), dt), ("v", v, (B, N, Hkv, D), dt),
-           ("out", out, (B, N, H, D), dt))
+    _check(q, ("out", out, q.shape, q.dtype))
     if lse is not None:
         _check(q, ("lse", lse, (B, H, N), torch.float32))
+    _window_fwd(q, k, v, out, lse, window, sinks, impl, stream)
+
+
+def _window_fwd(q, k, v, out, lse, window, sinks, impl, stream) -> None:
+    # out and lse are checked or of this module's making
+    B, N, H, D = q.shape
+    Hkv, dt = k.shape[2], q.dtype
+    kv = (B, N, Hkv, D)
+    _check(q, ("q", q, (B, N, H, D), dt), ("k", k, kv, dt), ("v", v, kv, dt))
     _call("longnet_window_attn_fwd", q, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
           None if lse is None else lse.data_ptr(), B, N, H, Hkv, D, int(window), int(sinks), _dtype_code(q),
           int(impl))
@@ -576,12 +584,19 @@ def longnet_window_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o
     forward's.  workspace: a CUDA tensor of at least
     longnet_window_bwd_workspace_bytes bytes, 256-byte aligned.  Raises
     LongNetError on a non-zero status."""
+    dt, kv = q.dtype, k.shape
+    _check(q, ("dq", dq, q.shape, dt), ("dk", dk, kv, dt), ("dv", dv, kv, dt),
+           ("workspace", workspace, workspace.shape, workspace.dtype))
+    _window_bwd(q, k, v, out, lse, dout, dq, dk, dv, window, sinks, workspace, impl, stream)
+
+
+def _window_bwd(q, k, v, out, lse, dout, dq, dk, dv, window, sinks, workspace, impl, stream) -> None:
+    # dq, dk, dv and the workspace are checked or of this module's making
     B, N, H, D = q.shape
     Hkv, dt = k.shape[2], q.dtype
     rows, kv = (B, N, H, D), (B, N, Hkv, D)
     _check(q, ("q", q, rows, dt), ("k", k, kv, dt), ("v", v, kv, dt), ("out", out, rows, dt),
-           ("dout", dout, rows, dt), ("dq", dq, rows, dt), ("dk", dk, kv, dt), ("dv", dv, kv, dt),
-           ("lse", lse, (B, H, N), torch.float32), ("workspace", workspace, workspace.shape, workspace.dtype))
+           ("dout", dout, rows, dt), ("lse", lse, (B, H, N), torch.float32))
     _call("longnet_window_attn_bwd", q, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
           lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, N, H, Hkv, D,
           int(window), int(sinks), _dtype_code(q), int(impl), workspace.data_ptr(),
@@ -594,9 +609,10 @@ def window_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, 
     Returns (out, lse)."""
     B, N, H, _ = q.shape
     with _on(stream):
+        # (empty_like keeps the strides of a dense q, which the call then refuses with q)
         out = torch.empty_like(q)
-        lse = torch.empty((B, H, N), device=q.device, dtype=torch.float32) if want_lse else None
-        longnet_window_attn_fwd(q, k, v, out, lse, window, sinks, impl, stream)
+        lse = q.new_empty((B, H, N), dtype=torch.float32) if want_lse else None
+        _window_fwd(q, k, v, out, lse, window, sinks, impl, stream)
     return out, lse
 
 
@@ -607,9 +623,9 @@ def window_attn_bwd(q, k, v, out, lse, dout, window: int, sinks: int = 0, impl: 
     B, N, H, D = q.shape
     with _on(stream):
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        ws = torch.empty(longnet_window_bwd_workspace_bytes(B, N, H, k.shape[2], D, window, sinks, q.dtype),
-                         dtype=torch.uint8, device=q.device)
-        longnet_window_attn_bwd(q, k, v, out, lse, dout.contiguous(), dq, dk, dv, window, sinks, ws, impl, stream)
+        ws = q.new_empty(longnet_window_bwd_workspace_bytes(B, N, H, k.shape[2], D, window, sinks, q.dtype),
+                         dtype=torch.uint8)
+        _window_bwd(q, k, v, out, lse, dout.contiguous(), dq, dk, dv, window, sinks, ws, impl, stream)
     return dq, dk, dv
 
 
@@ -689,7 +705,7 @@ def paged_workspace(q: torch.Tensor, k_pages: torch.Tensor, table: torch.Tensor,
     keeps one (a call without one allocates it with torch)."""
     n_pages, page, Hkv, D, S, max_pages = _cache_sizes(k_pages, table)
     n = longnet_paged_workspace_bytes(S, max_q, q.shape[1], Hkv, D, page, max_pages, window, sinks, q.dtype, weights)
-    return torch.empty(n, dtype=torch.uint8, device=q.device)
+    return q.new_empty(n, dtype=torch.uint8)
 
 
 def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, cu_q: torch.Tensor,
@@ -707,19 +723,22 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, cu
     LongNetError on a non-zero status."""
     n_pages, page, Hkv, D, S, max_pages = _cache_sizes(k_pages, table)
     T, H, dt = q.shape[0], q.shape[1], q.dtype
+    rows, pool = (T, H, D), (n_pages, page, Hkv, D)
+    _check(q, ("q", q, rows, dt), ("k_pages", k_pages, pool, dt), ("v_pages", v_pages, pool, dt),
+           ("cu_q", cu_q, (S + 1,), torch.int32), ("kv_len", kv_len, (S,), torch.int32),
+           ("table", table, (S, max_pages), torch.int32))
+    if weights is not None:
+        _check(q, ("weights", weights, (S, Hkv, max_pages * page), torch.float32))
     if out is None or lse is None or workspace is None:
         with _on(stream):
             out = torch.empty_like(q) if out is None else out
-            lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if lse is None else lse
+            lse = q.new_empty((T, H), dtype=torch.float32) if lse is None else lse
             if workspace is None:
-                workspace = paged_workspace(q, k_pages, table, max_q, window, sinks, weights is not None)
-    _check(q, ("q", q, (T, H, D), dt), ("k_pages", k_pages, k_pages.shape, dt),
-           ("v_pages", v_pages, k_pages.shape, dt), ("out", out, (T, H, D), dt), ("lse", lse, (T, H), torch.float32),
-           ("cu_q", cu_q, (S + 1,), torch.int32), ("kv_len", kv_len, (S,), torch.int32),
-           ("table", table, table.shape, torch.int32))
-    if weights is not None:
-        _check(q, ("weights", weights, (S, Hkv, max_pages * page), torch.float32))
-    _check(q, ("workspace", workspace, workspace.shape, workspace.dtype))
+                workspace = q.new_empty(
+                    longnet_paged_workspace_bytes(S, max_q, H, Hkv, D, page, max_pages, window, sinks, dt,
+                                                  weights is not None), dtype=torch.uint8)
+    _check(q, ("out", out, rows, dt), ("lse", lse, (T, H), torch.float32),
+           ("workspace", workspace, workspace.shape, workspace.dtype))
     _call("longnet_paged_attn_fwd", q, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
           lse.data_ptr(), None if weights is None else weights.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
           table.data_ptr(), T, S, int(max_q), H, Hkv, D, n_pages, page, max_pages, int(window), int(sinks),
@@ -741,16 +760,16 @@ def cache_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, weights: torch.Ten
     status."""
     n_pages, page, Hkv, D, S, max_pages = _cache_sizes(k_pages, table)
     n_out, _, _, _, _, max_out = _cache_sizes(k_out, new_table)
-    dt, at = k_pages.dtype, k_pages.device
+    dt = k_pages.dtype
     _check(k_pages, ("k_pages", k_pages, k_pages.shape, dt), ("v_pages", v_pages, k_pages.shape, dt),
            ("k_out", k_out, (n_out, page, Hkv, D), dt), ("v_out", v_out, (n_out, page, Hkv, D), dt),
            ("weights", weights, (S, Hkv, max_pages * page), torch.float32), ("kv_len", kv_len, (S,), torch.int32),
            ("table", table, table.shape, torch.int32), ("new_table", new_table, (S, max_out), torch.int32))
     with _on(stream):
         # (a budget out of range is refused by the library)
-        kept = torch.empty((S, Hkv, min(max(int(budget), 0), max_out * page)), dtype=torch.int32, device=at)
-        new_len = torch.empty((S,), dtype=torch.int32, device=at)
-        new_weights = torch.empty((S, Hkv, max_out * page), dtype=torch.float32, device=at)
+        kept = table.new_empty((S, Hkv, min(max(int(budget), 0), max_out * page)))
+        new_len = torch.empty_like(kv_len)
+        new_weights = weights.new_empty((S, Hkv, max_out * page))
     _call("longnet_cache_evict", k_pages, stream, k_pages.data_ptr(), v_pages.data_ptr(), weights.data_ptr(),
           kv_len.data_ptr(), table.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), new_weights.data_ptr(),
           new_len.data_ptr(), kept.data_ptr(), new_table.data_ptr(), S, Hkv, D, n_pages, page, max_pages, n_out,
