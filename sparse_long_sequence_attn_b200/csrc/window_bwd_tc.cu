@@ -29,21 +29,28 @@
 //   query-centric  a CTA holds two tiles of 128 packed query rows (Q, dout) and
 //                  streams 64-key blocks (K, V): S, dP, then dQ += dS K.  It runs
 //                  first and computes delta on the way.
-// Two score slots (S and dP, 64 columns each) in TMEM, each with a softmax
-// warpgroup of its own: the tensor cores fill one while the other's P and dS
-// are made.  Query-centric, and key-centric up to D = 64, a slot belongs to one
-// of two tiles that share every streamed block; key-centric at D = 128 the
-// accumulators of one tile fill the rest of TMEM, and the slots take
-// alternate blocks.
+// Two score slots (S and dP, 64 columns each) in TMEM, each with two compute
+// warpgroups, one for each half of a block's columns: no row statistic is
+// shared between columns, so a block's scores are worked off by 256 threads.
+// Query-centric, and key-centric up to D = 64, a slot belongs to one of two tiles
+// that share every streamed block; key-centric at D = 128 the accumulators of
+// one tile fill the rest of TMEM, and the slots take alternate blocks.
+// What the tiles' tensor work must not wait for is the arithmetic on the block
+// before.  So S of the next block is issued as soon as this one's scores are in
+// registers; P and dS go over dP's columns, and dP of the next block follows the
+// products that read them.  Query-centric up to D = 64 TMEM has room for dS
+// beside the scores, and dP comes early as well.  (All after the products of
+// the block before, with half the warps: 274 us for the step of 8192 tokens, 12/4
+// heads of 64, against 240; 1222 against 1093 for 16384 tokens, 8 heads of 128.)
 // The compute warps are held up by what they read from shared memory: a column's
 // -lse and -delta, the same for all 32 lanes, cost a load's full bandwidth (512
 // bytes of registers for 16).  Key-centric up to D = 64 they are therefore added
 // by the tensor cores: the tiles get a further 16 operand columns, constants,
 // and the blocks three parts of each number in the input format (24 bits or
 // more of it), which makes the scores s - lse / scale and dP - delta.
-// Warps 0-3 and 4-7 compute, warp 8 loads (TMA; its lanes fetch lse and
-// delta), warps 9 and 10 issue, one for each tile (one tile: warp 9 alone, as
-// both slots add to the same accumulators).  Every wait is bounded.
+// Warps 0-15 compute (slot 0, slot 1, and the same for the other half), warp 16
+// loads (TMA; its lanes fetch lse and delta), warps 17 and 18 issue, one for each
+// tile (one tile: warp 17 alone, as both slots add to the same accumulators).  Every wait is bounded.
 // Bound: the compute warps' passes over S and dP (two TMEM reads, an exponential
 // and a TMEM write for each 2 x 2 D multiply-adds); the tensor cores work 20 to 42 %
 // of the cycles.  Measured, query- and key-centric: 8192 tokens, 12/4 heads of 64,
@@ -65,10 +72,10 @@ namespace longnet {
 namespace wb {
 using namespace wt;
 
-constexpr int kThreads = 352;
-constexpr int kTma = 8, kMma = 9;  // warps
+constexpr int kThreads = 608;
+constexpr int kTma = 16, kMma = 17;  // warps
 constexpr int kBlk = 64;           // streamed rows
-constexpr uint32_t kTmemCols = 512, kColAcc = 256;
+constexpr uint32_t kTmemCols = 512, kColAcc = 256, kColDs = 384;
 
 template <int kD, bool kKeys>
 struct B : Panels<kD> {
@@ -80,6 +87,9 @@ struct B : Panels<kD> {
   // step of the products (kFold), from extra operand columns; at D = 128 the
   // compute warps add them from shared memory.
   static constexpr bool kFold = kKeys && kD <= 64;
+  // Query-centric up to D = 64, TMEM has room for dS beside the scores (two
+  // buffers a tile): both products of the next block run during this one's.
+  static constexpr bool kBeside = !kKeys && kD <= 64;
   static constexpr int kFoldBytes = kFold ? kTile * 32 : 0;  // the tiles' extra columns: 128 rows of 16
   static constexpr int kStageBytes = 2 * kBlkBytes + (kFold ? 2 * kBlk * 32 : kKeys ? 1024 : 0);  // two blocks, then these
   static constexpr int kStages = kD == 128 ? (kKeys ? 4 : 3) : 6;
@@ -273,7 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar_p = bar_s + 2;         // [2] P and dS of a slot in TMEM
   uint64_t* bar_acc = bar_s + 4;       // [2] accumulators done
   uint64_t* bar_drain = bar_s + 6;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_s + 7);
+  uint64_t* bar_ld = bar_s + 7;        // [2] scores of a slot read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_s + 9);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -285,8 +296,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_s + i, 1);
-      mbar_init(bar_p + i, 128);
+      mbar_init(bar_p + i, 256);
       mbar_init(bar_acc + i, 1);
+      mbar_init(bar_ld + i, 256);
     }
     mbar_init(bar_drain, kTiles);
     *abort_flag = 0;
@@ -420,51 +432,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t t_lo[2] = {(smem_u32(tile_ptr(st, 0)) >> 4) | (1u << 16), (smem_u32(tile_ptr(st, 1)) >> 4) | (1u << 16)};
       const uint32_t ring_lo = smem_u32(sStage) >> 4;
       const uint32_t acc = tmem + kColAcc + (kTiles == 2 ? (kKeys ? 2 : 1) * kD * st : 0);
-      // S and dP of the block in `stage` into slot `slot`
-      auto scores = [&](int stage, int slot) {
-        tc_fence_after();
+      // product w (0: S, 1: dP) of the block in `stage` into slot `slot`
+      auto score = [&](int w, int stage, int slot) {
         const uint32_t b_lo = (ring_lo + stage * (LL::kStageBytes >> 4)) | (1u << 16);
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
+        for (int pn = 0; pn < kPanels; ++pn)
 #pragma unroll
-          for (int pn = 0; pn < kPanels; ++pn)
-#pragma unroll
-            for (int kk = 0; kk < LL::kPanelElems / 16; ++kk)
-              mma_ss_if(leader, tmem + 128 * slot + 64 * w, desc_from(t_lo[w] + pn * (kTilePanel >> 4) + kk * 2, kDescHi),
-                        desc_from(b_lo + w * (LL::kBlkBytes >> 4) + pn * (kBlkPanel >> 4) + kk * 2, kDescHi), kIdScore,
-                        (pn > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < LL::kPanelElems / 16; ++kk)
+            mma_ss_if(leader, tmem + 128 * slot + 64 * w, desc_from(t_lo[w] + pn * (kTilePanel >> 4) + kk * 2, kDescHi),
+                      desc_from(b_lo + w * (LL::kBlkBytes >> 4) + pn * (kBlkPanel >> 4) + kk * 2, kDescHi), kIdScore,
+                      (pn > 0 || kk > 0) ? 1u : 0u);
         if (LL::kFold) {
           constexpr uint32_t kHi = (uint32_t)(8 * 32 >> 4) | (1u << 14) | (6u << 29);  // 32-byte rows and swizzle
           const uint32_t fa = (smem_u32(smem + LL::kFold0) >> 4) | (1u << 16);
           const uint32_t fb = b_lo + (2 * LL::kBlkBytes >> 4);
-#pragma unroll
-          for (int w = 0; w < 2; ++w)
-            mma_ss_if(leader, tmem + 128 * slot + 64 * w, desc_from(fa, kHi), desc_from(fb + w * (kBlk * 32 >> 4), kHi),
-                      kIdScore, 1u);
+          mma_ss_if(leader, tmem + 128 * slot + 64 * w, desc_from(fa, kHi), desc_from(fb + w * (kBlk * 32 >> 4), kHi),
+                    kIdScore, 1u);
         }
-        tc_commit_if(leader, bar_s + slot);
       };
-      // the gradient products of the block in `stage`, P and dS in slot `slot`
-      auto grads = [&](int stage, int slot, bool fresh) {
+      // the gradient products of item e, in `stage`; P and dS in slot `slot`
+      auto grads = [&](int stage, int slot, int e, bool fresh) {
         tc_fence_after();
         const uint32_t b0 = (ring_lo + stage * (LL::kStageBytes >> 4)) | lbo_mn, b1 = b0 + (LL::kBlkBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < kBlk / 16; ++kk) {
           const uint32_t add = fresh && kk == 0 ? 0u : 1u;
+          // 16 rows' P (8 columns) and, 16 columns on, dS; in each half of dP's columns those of its rows
+          const uint32_t p = tmem + 128 * slot + 64 + 32 * (kk >> 1) + 8 * (kk & 1);
           if (kKeys) {
             // dV += P^T dout, dK += dS^T Q
-            mma_ts_if(leader, acc, tmem + 128 * slot + kk * 8, desc_from(b1 + kk * kStep16, kDescHi), kIdGrad, add);
-            mma_ts_if(leader, acc + kD, tmem + 128 * slot + 64 + kk * 8, desc_from(b0 + kk * kStep16, kDescHi), kIdGrad,
-                      add);
+            mma_ts_if(leader, acc, p, desc_from(b1 + kk * kStep16, kDescHi), kIdGrad, add);
+            mma_ts_if(leader, acc + kD, p + 16, desc_from(b0 + kk * kStep16, kDescHi), kIdGrad, add);
           } else {
             // dQ += dS K
-            mma_ts_if(leader, acc, tmem + 128 * slot + 64 + kk * 8, desc_from(b0 + kk * kStep16, kDescHi), kIdGrad, add);
+            const uint32_t d = LL::kBeside ? tmem + kColDs + 64 * slot + 32 * (e & 1) + 8 * kk : p + 16;
+            mma_ts_if(leader, acc, d, desc_from(b0 + kk * kStep16, kDescHi), kIdGrad, add);
           }
         }
       };
       bool ok = wt.wait_warp(bar_tile, 0);
       if (kTiles == 2) {
-        int stage = 0, phase = 0, done = 0;
+        // Item e (the e-th block of the tile's run, first pass and second): its
+        // S is issued as soon as the scores before it are read, its dP then too
+        // where dS lies beside them, else after the products that read P and dS
+        // in its place.
+        const int sums = (passes - 1) * r.count, all = passes * r.count;
+        int stage = 0, phase = 0, asked = 0, used = 0, held = -1;  // held: stage of the item asked for and not used
+        auto use = [&]() {
+          ok = wt.wait_warp(bar_p + st, used & 1);
+          if (!ok) return;
+          if (used >= sums) {
+            grads(held, st, used, used == sums);
+            tc_commit_if(leader, bar_empty + held);
+            if (used == all - 1) tc_commit_if(leader, bar_acc + st);
+          }
+          ++used;
+          held = -1;
+        };
         for (int m = 0; m < passes * cnt && ok; ++m) {
           const bool sum = m < (passes - 1) * cnt;  // the pass for delta
           const int n = m < cnt ? m : m - cnt;
@@ -473,18 +497,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wt.wait_warp(bar_full + stage, phase);
           if (!ok) break;
           if (r.has(n)) {
-            scores(stage, st);
-            if (sum) tc_commit_if(leader, bar_empty + stage);
-            ok = wt.wait_warp(bar_p + st, done & 1);
+            if (asked > 0) ok = wt.wait_warp(bar_ld + st, (asked - 1) & 1);
             if (!ok) break;
-            ++done;
-            if (!sum) {
-              const int first_of_pass = (passes - 1) * r.count;
-              grads(stage, st, done == first_of_pass + 1);
-              tc_commit_if(leader, bar_empty + stage);
-              if (done == first_of_pass + r.count) tc_commit_if(leader, bar_acc + st);
+            tc_fence_after();
+            score(0, stage, st);
+            if (LL::kBeside) {
+              score(1, stage, st);
+              tc_commit_if(leader, bar_s + st);
             }
+            if (held >= 0) use();
+            if (!ok) break;
+            if (!LL::kBeside) {
+              score(1, stage, st);
+              tc_commit_if(leader, bar_s + st);
+            }
+            if (sum) tc_commit_if(leader, bar_empty + stage);
+            ++asked;
+            held = stage;
           } else {
+            if (held >= 0) use();
+            if (!ok) break;
             mbar_arrive_if(leader, bar_empty + stage);
           }
           if (++stage == S) {
@@ -492,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             phase ^= 1;
           }
         }
+        if (ok && held >= 0) use();
       } else {
         // a block's scores are issued before the P and dS of the one before
         // are waited for
@@ -500,12 +533,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n < cnt) {
             ok = wt.wait_warp(bar_full + stage, phase);
             if (!ok) break;
-            scores(stage, n & 1);
+            tc_fence_after();
+            score(0, stage, n & 1);
+            score(1, stage, n & 1);
+            tc_commit_if(leader, bar_s + (n & 1));
           }
           if (n > 0) {
             ok = wt.wait_warp(bar_p + ((n - 1) & 1), ((n - 1) >> 1) & 1);
             if (!ok) break;
-            grads(before, (n - 1) & 1, n == 1);
+            grads(before, (n - 1) & 1, n - 1, n == 1);
             tc_commit_if(leader, bar_empty + before);
           }
           before = stage;
@@ -525,10 +561,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ P, dS and the epilogue
-    const int st = warp >> 2;
-    const int row = 32 * (warp & 3) + lane;  // TMEM lane = tile row
+    const int st = (warp >> 2) & 1, hf = warp >> 3;  // slot, half of the block's columns
+    const int row = 32 * (warp & 3) + lane;          // TMEM lane = tile row
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t slot = tmem + lane_base + 128 * st;
+    const uint32_t slot = tmem + lane_base + 128 * st + 32 * hf;
     // key-centric: this thread's key; query-centric: its token and head
     const int j = first + (kTiles == 2 ? st * kTile : 0) + row;
     const int t0 = first + st * tok, i = t0 + row / G, h = f * G + row % G;
@@ -571,12 +607,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Run r = run_of(st);
     int done = 0;
     bool ok = true;
-    // query-centric: the columns of block n that this row sees, as bits
-    auto seen = [&](int n, uint32_t& keep0, uint32_t& keep1) {
-      const int j0 = bl.at(n) * kBlk;
+    // query-centric: the columns of this half of block n that the row sees, as bits
+    auto seen = [&](int n) {
+      const int j0 = bl.at(n) * kBlk + 32 * hf;
       const int hi = row_ok ? i - j0 + 1 : 0, lo = i - j0 - a.window + 1, sk = a.sinks - j0;
-      keep0 = below(hi) & (~below(lo) | below(sk));
-      keep1 = below(hi - 32) & (~below(lo - 32) | below(sk - 32));
+      return below(hi) & (~below(lo) | below(sk));
     };
     if (!kKeys && passes == 2) {
       // delta = sum of P dP over the row
@@ -585,72 +620,80 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wt.wait_warp(bar_s + st, done & 1);
         if (!ok) break;
         tc_fence_after();
-        uint32_t keep[2];
-        seen(n, keep[0], keep[1]);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t sr[32], dr[32];
-          LN_TMEM_LD32(slot + 32 * hf, sr);
-          LN_TMEM_LD32(slot + 64 + 32 * hf, dr);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            float x0, x1;
-            f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sc2, nl_row), x0, x1);
-            const bool v0 = (keep[hf] >> c) & 1, v1 = (keep[hf] >> (c + 1)) & 1;
-            // (an unseen pair's dP may be anything, where a row is no token's)
-            acc = fma_f32x2(f32x2(v0 ? ex2(x0) : 0.f, v1 ? ex2(x1) : 0.f),
-                            f32x2(v0 ? __uint_as_float(dr[c]) : 0.f, v1 ? __uint_as_float(dr[c + 1]) : 0.f), acc);
-          }
-        }
+        const uint32_t keep = seen(n);
+        uint32_t sr[32], dr[32];
+        LN_TMEM_LD32(slot, sr);
+        LN_TMEM_LD32(slot + 64, dr);
+        tmem_wait_ld();
         tc_fence_before();
+        mbar_arrive(bar_ld + st);
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          float x0, x1;
+          f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sc2, nl_row), x0, x1);
+          const bool v0 = (keep >> c) & 1, v1 = (keep >> (c + 1)) & 1;
+          // (an unseen pair's dP may be anything, where a row is no token's)
+          acc = fma_f32x2(f32x2(v0 ? ex2(x0) : 0.f, v1 ? ex2(x1) : 0.f),
+                          f32x2(v0 ? __uint_as_float(dr[c]) : 0.f, v1 ? __uint_as_float(dr[c + 1]) : 0.f), acc);
+        }
         mbar_arrive(bar_p + st);
         ++done;
       }
       float d0, d1;
       f32x2_split(acc, d0, d1);
-      delta = d0 + d1;
+      // the other half's sum comes through TMEM, in accumulators not yet in use
+      const uint32_t swap = tmem + lane_base + kColAcc + kD * st;
+      asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(swap + hf), "f"(d0 + d1) : "memory");
+      tmem_wait_st();
+      tc_fence_before();
+      asm volatile("bar.sync %0, 256;" ::"r"(1 + st) : "memory");  // the slot's two warpgroups, also after a timeout
+      tc_fence_after();
+      float other;
+      asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(other) : "r"(swap + (hf ^ 1)));
+      tmem_wait_ld();
+      asm volatile("" : "+f"(other));  // used after the wait only
+      tc_fence_before();
+      delta = hf ? other + (d0 + d1) : (d0 + d1) + other;
     }
-    if (!kKeys && row_ok) g.delta[stat] = delta;  // the key-centric kernel's
+    if (!kKeys && row_ok && hf == 0) g.delta[stat] = delta;  // the key-centric kernel's
     const uint64_t nd_row = f32x2(-delta, -delta);
     for (int n = r.begin; n < r.end && ok; n += r.step) {
       const float* sl = reinterpret_cast<const float*>(sStage + (n % S) * LL::kStageBytes + 2 * LL::kBlkBytes);
-      uint32_t keep0, keep1;  // the columns that pair with this row, as bits
+      uint32_t keep;  // the half's columns that pair with this row, as bits
       if (kKeys) {
         const int b0 = i0 + n * tok;
         const int n_tok = i1 - b0 < tok ? i1 - b0 : tok;
         const int from = j - b0, to = j + a.window - b0;  // tokens
         const int lo = (from < 0 ? 0 : from > kBlk ? kBlk : from) * G;
         const int hi = (j < a.sinks || to > n_tok ? n_tok : to < 0 ? 0 : to) * G;
-        keep0 = below(hi) & ~below(lo);
-        keep1 = below(hi - 32) & ~below(lo - 32);
+        keep = below(hi - 32 * hf) & ~below(lo - 32 * hf);
       } else {
-        seen(n, keep0, keep1);
+        keep = seen(n);
       }
       if (kKeys && !LL::kFold) ok = wt.wait_warp(bar_full + n % S, (n / S) & 1);  // for what sl holds
       if (ok) ok = wt.wait_warp(bar_s + st, done & 1);
       if (!ok) break;
       tc_fence_after();
-      const bool whole = __all_sync(0xffffffffu, (keep0 & keep1) == 0xffffffffu);
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t sr[32], dr[32], pk[16], dk[16];
-        LN_TMEM_LD32(slot + 32 * hf, sr);
-        LN_TMEM_LD32(slot + 64 + 32 * hf, dr);
-        tmem_wait_ld();
-        if (LL::kFold) {
-          if (whole)
-            p_ds_folded<kFmt, false>(sr, dr, sc2, 0, pk, dk);
-          else
-            p_ds_folded<kFmt, true>(sr, dr, sc2, hf ? keep1 : keep0, pk, dk);
-        } else if (whole)
-          p_ds_half<kFmt, kKeys, false>(sr, dr, sl + 32 * hf, sl + kBlk + 32 * hf, nl_row, nd_row, sc2, 0, pk, dk);
-        else
-          p_ds_half<kFmt, kKeys, true>(sr, dr, sl + 32 * hf, sl + kBlk + 32 * hf, nl_row, nd_row, sc2,
-                                       hf ? keep1 : keep0, pk, dk);
-        if (kKeys) LN_TMEM_ST16(slot + 16 * hf, pk);
-        LN_TMEM_ST16(slot + 64 + 16 * hf, dk);
+      const bool whole = __all_sync(0xffffffffu, keep == 0xffffffffu);
+      uint32_t sr[32], dr[32], pk[16], dk[16];
+      LN_TMEM_LD32(slot, sr);
+      LN_TMEM_LD32(slot + 64, dr);
+      tmem_wait_ld();
+      if (kTiles == 2) {
+        tc_fence_before();
+        mbar_arrive(bar_ld + st);
       }
+      if (LL::kFold) {
+        if (whole)
+          p_ds_folded<kFmt, false>(sr, dr, sc2, 0, pk, dk);
+        else
+          p_ds_folded<kFmt, true>(sr, dr, sc2, keep, pk, dk);
+      } else if (whole)
+        p_ds_half<kFmt, kKeys, false>(sr, dr, sl + 32 * hf, sl + kBlk + 32 * hf, nl_row, nd_row, sc2, 0, pk, dk);
+      else
+        p_ds_half<kFmt, kKeys, true>(sr, dr, sl + 32 * hf, sl + kBlk + 32 * hf, nl_row, nd_row, sc2, keep, pk, dk);
+      if (kKeys) LN_TMEM_ST16(slot + 64, pk);
+      LN_TMEM_ST16(LL::kBeside ? tmem + lane_base + kColDs + 64 * st + 32 * (done & 1) + 16 * hf : slot + 80, dk);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(bar_p + st);
@@ -667,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // tile; with one tile, the first dV and the second dK
 #pragma unroll 1
       for (int w = 0; w < (kKeys ? 2 : 1); ++w) {
-        if (kTiles == 1 && w != st) continue;
+        if (kTiles == 1 ? w != st || hf : w != hf) continue;
         // w = 0: dV or dQ, w = 1: dK
         const float sc = kKeys && w == 0 ? 1.f / kPScale<kFmt> : a.scale;
         const uint32_t acc = tmem + lane_base + kColAcc + (kTiles == 2 ? (kKeys ? 2 : 1) * kD * st : 0) + w * kD;
