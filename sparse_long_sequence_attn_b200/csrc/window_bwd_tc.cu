@@ -51,11 +51,14 @@
 // Warps 0-15 compute (slot 0, slot 1, and the same for the other half), warp 16
 // loads (TMA; its lanes fetch lse and delta), warps 17 and 18 issue, one for each
 // tile (one tile: warp 17 alone, as both slots add to the same accumulators).  Every wait is bounded.
-// Bound: the compute warps' passes over S and dP (two TMEM reads, an exponential
-// and a TMEM write for each 2 x 2 D multiply-adds); the tensor cores work 20 to 42 %
-// of the cycles.  Measured, query- and key-centric: 8192 tokens, 12/4 heads of 64,
-// window 1024: 93 and 100 us; 16384 tokens, 8 heads of 128, window 4096: 489 and 498
-// us (854 TFLOP/s of the seven products).
+// Bound: query-centric the exponentials' unit while the compute warps work (1024
+// cycles of the 1950 that a block takes both tiles at D = 64), key-centric the
+// products, whose 64-row blocks make the tensor cores read a tile again for every
+// 64 columns (tensor cores at work 30 and 42 % of the cycles at D = 64, 53 and 52 %
+// at D = 128).  Turns of the two tiles at the arithmetic, which kept their
+// exponentials apart, were slower (240 -> 307 us).  Measured, both kernels: 8192
+// tokens, 12/4 heads of 64, window 1024: 168 us; 16384 tokens, 8 heads of 128, window
+// 4096: 850 us (991 TFLOP/s of the seven products).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
