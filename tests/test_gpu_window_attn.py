@@ -224,9 +224,10 @@ def test_fp32_tiles_of_both_sizes(shape):
         within(name, a, r, b)
 
 
-def test_captured_training_step():
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_captured_training_step(dtype):
     """Forward and backward through autograd in one graph; the eager warm-up is dropped before the capture."""
-    q, k, v, dout = inputs(2, 300, 4, 2, 64, BF16, 12)
+    q, k, v, dout = inputs(2, 300, 4, 2, 64, dtype, 12)
     leaves = [z.clone().requires_grad_() for z in (q, k, v)]
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -239,7 +240,7 @@ def test_captured_training_step():
     with torch.cuda.graph(graph):
         out = bd.window_attention(*leaves, 70, 4)
         out.backward(dout)
-    new = inputs(2, 300, 4, 2, 64, BF16, 13)
+    new = inputs(2, 300, 4, 2, 64, dtype, 13)
     with torch.no_grad():
         for z, n in zip((*leaves, dout), new):
             z.copy_(n)
@@ -250,3 +251,20 @@ def test_captured_training_step():
     assert torch.equal(out, want[0])
     for z, w in zip(leaves, want[2:]):
         assert torch.equal(z.grad, w)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("shape", [
+    (1, 1100, 4, 1, 64, 1, 0),       # one block a row tile, then one more where it ends
+    (1, 900, 3, 1, 128, 700, 0),     # tiles of 42 tokens: runs that begin blocks apart
+    (2, 640, 2, 2, 64, 513, 64),     # past the lengths whose delta has a pass of its own
+    (1, 1300, 1, 1, 32, 600, 129),
+    (1, 85, 3, 3, 16, 85, 0),        # the second tile has no keys of its own
+], ids=str)
+def test_backward_runs_of_blocks(shape, dtype):
+    """The two tiles of a block share a ring of streamed blocks, each over a run of its own."""
+    B, N, H, Hkv, D, window, sinks = shape
+    x = inputs(B, N, H, Hkv, D, dtype, 3 + N)
+    ref, bound = window_reference(*x, window, sinks)
+    for name, a, r, b in zip(("out", "lse", "dq", "dk", "dv"), run(*x, window, sinks, AUTO), ref, bound):
+        within(name, a, r, b)
