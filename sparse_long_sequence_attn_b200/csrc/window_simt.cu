@@ -14,11 +14,12 @@
 // side through shared memory as fp32; a thread holds an RT x 4 piece of the
 // scores and an RT x D/16 piece of the accumulators, so that at RT = 4 every
 // value read from shared memory feeds four multiply-adds.  Rows are padded by four
-// floats, which keeps the 16-byte reads of 8 lanes in different banks.  The bound
-// is the fp32 pipe (no TF32: fp32 inputs keep fp32 products) and, for small
-// problems, a CTA's latency.  Measured, fp32, forward, dq, and dk with dv: 997
-// tokens, 6/2 heads of 32, window 200: 26, 29 and 34 us; 1500 tokens, 8 heads of 128,
-// window 500: 171, 224 and 304 us (half of the pipe's rate while a CTA runs).
+// floats, which keeps the 16-byte reads of 8 lanes in different banks.  Products
+// stay fp32 for fp32 inputs (no TF32).  The bound is shared memory, which hands out
+// 128 bytes a clock: at two bytes or more for each multiply-add, half of the fp32
+// pipe's rate at most; and for small problems a CTA's latency.  Measured, fp32,
+// forward, dq, and dk with dv: 997 tokens, 6/2 heads of 32, window 200: 22, 23 and 34
+// us; 1500 tokens, 8 heads of 128, window 500: 171, 224 and 304 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -234,7 +235,7 @@ __device__ __forceinline__ float max16(float x) {
   return x;
 }
 
-// A query tile's key blocks are shared by the CTAs of a cluster (1, 2, 4 or 8),
+// A query tile's key blocks are shared by the CTAs of a cluster (1 to 8),
 // each with a run of them: part `rank` of `parts`.
 struct Part {
   int rank, parts, tile;
@@ -687,18 +688,19 @@ bool small_tiles(const AttnArgs& a) {
   return ((int64_t)a.nq_max * a.G + 15) / 16 * a.S * a.Hkv <= 2 * kSms;
 }
 
-// CTAs that share a query tile's key blocks (a cluster): doubled while the grid
-// fits two to an SM and each has a block (forward and dq of 2 x 276 tokens, one head
-// of 128: 37 and 49 us with one, 19 and 24 with 8).
+// CTAs that share a query tile's key blocks (a cluster): as many as there are
+// blocks and the grid fits two to an SM (forward and dq of 2 x 276 tokens, one head
+// of 128: 37 and 49 us with one, 19 and 23 with 5; of 997 tokens, 6/2 heads of 32,
+// window 200: 27 and 31 us with one, 26 and 29 with 2, 22 and 23 with 3).
 int key_parts(const AttnArgs& a, int64_t tiles, int rows) {
   int64_t keys = a.cu_q ? (int64_t)a.max_pages << a.page_shift : a.nq_max;
   if (a.window) {
     const int64_t seen = (int64_t)a.window + rows / a.G + 2 + (a.sinks + kT - 1) / kT * kT;
     if (seen < keys) keys = seen;
   }
-  int parts = 1;
-  while (parts < 8 && tiles * a.S * a.Hkv * parts <= kSms && 2 * parts * kT <= keys + kT - 1) parts *= 2;
-  return parts;
+  const int64_t fit = 2 * kSms / (tiles * a.S * a.Hkv), blocks = (keys + kT - 1) / kT;
+  const int64_t parts = fit < blocks ? fit : blocks;
+  return parts < 1 ? 1 : parts > 8 ? 8 : (int)parts;
 }
 // fn on (tiles, S Hkv) clusters of `parts` CTAs.
 template <typename... P, typename... V>
