@@ -851,13 +851,15 @@ KeyPlan key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, i
   return k;
 }
 
-// Tiles of 64 keys, or 16 where the items of 64 would leave half of the SMs idle,
-// and then cut down to one block of queries (dk and dv of 2 x 276 tokens, one head of
-// 128: 73 us with tiles of 64 keys, 41 with 16, 27 so cut).
+// Ranges down to one block of queries; tiles of 64 keys, or 16 where the items of 64
+// would leave half of the SMs idle.  (dk and dv of 2 x 276 tokens, one head of 128:
+// 73 us with tiles of 64 keys, 41 with 16, both of two blocks at least, 27 with 16
+// and one; of 600 tokens, 4/2 heads of 64: 33 us with two blocks at least, 25 with
+// one.)
 KeyPlan simt_key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t window, int64_t sinks) {
-  const int ctas = 2 * ws::kSms;
-  const KeyPlan k = key_plan(S, N, H, Hkv, window, sinks, 64, 2, ctas);
-  return k.items() * S * Hkv >= ws::kSms / 2 ? k : key_plan(S, N, H, Hkv, window, sinks, 16, 1, ctas);
+  const KeyPlan k = key_plan(S, N, H, Hkv, window, sinks, 64, 1, 2 * ws::kSms);
+  if (k.items() * S * Hkv >= ws::kSms / 2) return k;
+  return key_plan(S, N, H, Hkv, window, sinks, 16, 1, 2 * ws::kSms);
 }
 
 int64_t key_partial_floats(const KeyPlan& k, int64_t S, int64_t Hkv, int64_t D) {
