@@ -27,8 +27,9 @@
 //                  rows are 64 / G tokens by the G query heads that share the
 //                  keys, so shared heads sum in the accumulators.
 //   query-centric  a CTA holds two tiles of 128 packed query rows (Q, dout) and
-//                  streams 64-key blocks (K, V): S, dP, then dQ += dS K.  It runs
-//                  first and computes delta on the way.
+//                  streams 64-key blocks (K, V): S, dP, then dQ += dS K.  Where
+//                  delta takes a pass of its own it runs first; else delta
+//                  comes from its own kernel, and both run as one launch.
 // Two score slots (S and dP, 64 columns each) in TMEM, each with two compute
 // warpgroups, one for each half of a block's columns: no row statistic is
 // shared between columns, so a block's scores are worked off by 256 threads.
@@ -57,8 +58,8 @@
 // 64 columns (tensor cores at work 30 and 42 % of the cycles at D = 64, 53 and 52 %
 // at D = 128).  Turns of the two tiles at the arithmetic, which kept their
 // exponentials apart, were slower (240 -> 307 us).  Measured, both kernels: 8192
-// tokens, 12/4 heads of 64, window 1024: 168 us; 16384 tokens, 8 heads of 128, window
-// 4096: 850 us (991 TFLOP/s of the seven products).
+// tokens, 12/4 heads of 64, window 1024: 148 us and 7 for delta; 16384 tokens, 8 heads of 128, window
+// 4096: 760 us (1109 TFLOP/s of the seven products), in one launch.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -111,7 +112,7 @@ constexpr int kExactKeys = 512;
 
 struct BPlan {
   int tokens;    // of a tile (query-centric) or of a block (key-centric)
-  int exact;     // query-centric: delta by a pass of its own
+  int exact;     // query-centric: delta by a pass of its own (else it is there)
   KeyPlan key;
 };
 
@@ -211,10 +212,10 @@ __device__ __forceinline__ void p_ds_half(const uint32_t (&sr)[32], const uint32
   }
 }
 
+// The work of CTA bx of nx of (batch, key/value head) by.
 template <int kFmt, int kD, bool kKeys>
-__global__ void __launch_bounds__(kThreads, 1)
-    bwd_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ WindowBwdArgs g,
-               const __grid_constant__ BMaps maps, const BPlan plan) {
+__device__ __forceinline__ void bwd_body(const AttnArgs& a, const WindowBwdArgs& g, const BMaps& maps,
+                                         const BPlan& plan, int bx, int nx, int by) {
   using LL = B<kD, kKeys>;
   constexpr int kTiles = LL::kTiles, kPanels = LL::kPanels, S = LL::kStages;
   constexpr int kTilePanel = kTile * LL::kRowBytes, kBlkPanel = kBlk * LL::kRowBytes;
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // delta) is read only from here on
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int s = blockIdx.y / a.Hkv, f = blockIdx.y % a.Hkv;
+  const int s = by / a.Hkv, f = by % a.Hkv;
   const int N = a.nq_max, G = a.G, tok = plan.tokens;
   // ---- the CTA's tiles and the streamed rows
   int first;                // key-centric: first key; query-centric: first token
@@ -234,14 +235,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   int slot_no = -1;         // key-centric: the item's slot
   BlockList bl = {0, 0, 0};
   if (kKeys) {
-    const KeyItem it = key_item(a, plan.key, blockIdx.x);
+    const KeyItem it = key_item(a, plan.key, bx);
     first = it.tile * kTiles * kTile;
     i0 = it.i0;
     i1 = it.i1;
     slot_no = it.slot;
     cnt = i1 > i0 ? (i1 - i0 + tok - 1) / tok : 0;
   } else {
-    first = ((int)gridDim.x - 1 - (int)blockIdx.x) * 2 * tok;  // the longest first
+    first = (nx - 1 - bx) * 2 * tok;  // the longest first
     if (first >= N) return;
     const int end = first + 2 * tok < N ? first + 2 * tok : N;
     bl = blocks_of<kBlk>(a, first, end - 1);
@@ -573,38 +574,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t0 = first + st * tok, i = t0 + row / G, h = f * G + row % G;
     const bool row_ok = kKeys ? j < N : row < tok * G && i < N;
     float lse2 = 0.f, delta = 0.f;
-    if (!kKeys && passes == 1) {
-      // delta of the warp's rows, a row by kRow16 lanes (16 bytes each), kept
-      // by the row's lane and left for the key-centric kernel
-      constexpr int kRow16 = kD / 8, kRows = 32 / kRow16;
-      const int64_t elem = row_ok ? (((int64_t)s * N + i) * a.H + h) * kD : -1;
-      const int c = lane % kRow16;
-#pragma unroll 4
-      for (int r0 = 0; r0 < 32; r0 += kRows) {
-        const int r = r0 + lane / kRow16;
-        const int64_t at = __shfl_sync(0xffffffffu, elem, r);
-        float d = 0.f;
-        if (at >= 0) {
-          const uint4 u = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.out) + at)[c];
-          const uint4 v = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.dout) + at)[c];
-          const uint32_t us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float u0, u1, v0, v1;
-            unpack2<kFmt>(us[e], u0, u1);
-            unpack2<kFmt>(vs[e], v0, v1);
-            d = fmaf(u0, v0, fmaf(u1, v1, d));
-          }
-        }
-#pragma unroll
-        for (int o = kRow16 / 2; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-        // row r0 + k's sum is in lanes k kRow16..
-        const float mine = __shfl_sync(0xffffffffu, d, (lane % kRows) * kRow16);
-        if (lane / kRows == r0 / kRows) delta = mine;
-      }
-    }
     const int64_t stat = ((int64_t)s * a.H + h) * N + i;  // of lse and delta
     if (!kKeys && row_ok) lse2 = a.lse[stat] * kLog2e;
+    if (!kKeys && passes == 1 && row_ok) delta = g.delta[stat];
     const uint64_t sc2 = f32x2(a.scale_log2, a.scale_log2);
     const uint64_t nl_row = f32x2(-lse2, -lse2);
     const Run r = run_of(st);
@@ -658,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       delta = hf ? other + (d0 + d1) : (d0 + d1) + other;
     }
-    if (!kKeys && row_ok && hf == 0) g.delta[stat] = delta;  // the key-centric kernel's
+    if (!kKeys && passes == 2 && row_ok && hf == 0) g.delta[stat] = delta;  // the key-centric kernel's
     const uint64_t nd_row = f32x2(-delta, -delta);
     for (int n = r.begin; n < r.end && ok; n += r.step) {
       const float* sl = reinterpret_cast<const float*>(sStage + (n % S) * LL::kStageBytes + 2 * LL::kBlkBytes);
@@ -725,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         // [S Hkv][slot][dK, dV][tile rows][D]
-        float* part = g.partial + (((int64_t)blockIdx.y * plan.key.slots() + slot_no) * 2 + (w == 0 ? 1 : 0)) *
+        float* part = g.partial + (((int64_t)by * plan.key.slots() + slot_no) * 2 + (w == 0 ? 1 : 0)) *
                                       (int64_t)(kTiles * kTile * kD) + (int64_t)(j - first) * kD;
         if constexpr (kD >= 64) {
           store_rows_f32<kD>(tile_ptr(kTiles == 2 ? st : 0, w), acc, any, sc, 32 * (warp & 3), lane, part);
@@ -757,6 +729,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
+}
+
+template <int kFmt, int kD, bool kKeys>
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ WindowBwdArgs g,
+               const __grid_constant__ BMaps maps, const __grid_constant__ BPlan plan) {
+  bwd_body<kFmt, kD, kKeys>(a, g, maps, plan, blockIdx.x, gridDim.x, blockIdx.y);
+}
+
+// Both at once, when delta is there: first the CTAs that take longer, key-centric
+// (256 keys by three heads' rows, say) up to D = 64 and query-centric (256 rows
+// against 128 keys) at D = 128; the others fill up their last wave.  nq: query-centric
+// ones of a (batch, head).  One launch after the other: 240 us for the step of 8192
+// tokens, 12/4 heads of 64, against 237; 1093 against 1009 for 16384 tokens, 8 heads of
+// 128; 78 against 60 for 1024 tokens, 8 heads of 64, window 600.
+template <int kFmt, int kD>
+__global__ void __launch_bounds__(kThreads, 1)
+    both_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ WindowBwdArgs g,
+                const __grid_constant__ BMaps mq, const __grid_constant__ BMaps mk, const __grid_constant__ BPlan pq,
+                const __grid_constant__ BPlan pk, int nq) {
+  const int nk = pk.key.items(), first = (kD > 64 ? nq : nk) * a.S * a.Hkv;
+  const bool head = (int)blockIdx.x < first;
+  const int x = head ? blockIdx.x : blockIdx.x - first;
+  if (head == (kD > 64))
+    bwd_body<kFmt, kD, false>(a, g, mq, pq, x % nq, nq, x / nq);
+  else
+    bwd_body<kFmt, kD, true>(a, g, mk, pk, x % nk, nk, x / nk);
 }
 
 // Query rows [B, N, H, D] as (d, h, token, batch): a box is one panel of G
@@ -798,6 +797,16 @@ int launch_typed(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream)
   if (!opt_in_smem<bwd_kernel<kFmt, kD, true>>(LK::kSmem) || !opt_in_smem<bwd_kernel<kFmt, kD, false>>(LQ::kSmem))
     return LONGNET_ERR_CUDA;
   const int64_t pairs = ((int64_t)a.nq_max + 2 * pq.tokens - 1) / (2 * pq.tokens);
+  if (!pq.exact) {
+    if ((pairs + pk.key.items()) * a.S * a.Hkv > INT32_MAX) return LONGNET_ERR_UNSUPPORTED;
+    int rc = launch_window_delta(a, g, stream);
+    if (rc) return rc;
+    constexpr int smem = LK::kSmem > LQ::kSmem ? LK::kSmem : LQ::kSmem;
+    if (!opt_in_smem<both_kernel<kFmt, kD>>(smem)) return LONGNET_ERR_CUDA;
+    rc = launch_after(both_kernel<kFmt, kD>, dim3((unsigned)((pairs + pk.key.items()) * a.S * a.Hkv)), kThreads,
+                      smem, stream, a, g, mq, mk, pq, pk, (int)pairs);
+    return rc ? rc : launch_key_reduce(a, g, pk.key, stream);
+  }
   // dq first: it leaves delta for dk and dv
   int rc = launch_after(bwd_kernel<kFmt, kD, false>, dim3((unsigned)pairs, (unsigned)(a.S * a.Hkv)), kThreads, LQ::kSmem,
                         stream, a, g, mq, pq);
