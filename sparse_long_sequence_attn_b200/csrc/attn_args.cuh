@@ -121,13 +121,15 @@ int launch_window_fwd_simt(const AttnArgs& a, cudaStream_t stream);
 int launch_weights_simt(const AttnArgs& a, float* weights, cudaStream_t stream);
 
 // The backward's extra arguments: gradients in the inputs' dtype, and the
-// workspace: delta [S, H, N] fp32, then the far partials of the sink tiles.
+// workspace: delta [S, H, N] fp32, fp16's peaks, then the partials of the key
+// tiles.
 struct WindowBwdArgs {
   const void* dout;
   void* dq;
   void* dk;
   void* dv;
   float* delta;
+  float* peaks;  // [2] largest |dout_x|^2 and |v_j|^2
   float* partial;
 };
 // How dk and dv are cut into work items, one CTA each: a tile of keys by a
@@ -180,6 +182,8 @@ KeyPlan simt_key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t wind
 int launch_window_bwd_simt(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream);
 // delta = <dout, out> of every row, and the last step both families share.
 int launch_window_delta(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream);
+// fp16: g.peaks, and with them, when asked for, delta.
+int launch_window_peaks(const AttnArgs& a, const WindowBwdArgs& g, bool with_delta, cudaStream_t stream);
 int launch_key_reduce(const AttnArgs& a, const WindowBwdArgs& g, const KeyPlan& k, cudaStream_t stream);
 
 int launch_paged_append(const AttnArgs& a, const void* k_tok, const void* v_tok, float* weights, cudaStream_t stream);

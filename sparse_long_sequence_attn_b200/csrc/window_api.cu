@@ -72,15 +72,17 @@ void fill_window(AttnArgs* a, const void* q, const void* k, const void* v, void*
 
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
-// The workspace of the backward: delta, then the partials of the family
-// that needs most, so that it does not depend on the family.
-int64_t bwd_workspace(int64_t B, int64_t N, int64_t H, int64_t Hkv, int64_t D, int64_t window, int64_t sinks) {
+// The workspace of the backward: delta, fp16's peaks, then the partials of the
+// family that needs most, so that it does not depend on the family.
+int64_t peak_bytes(int dtype) { return dtype == LONGNET_DTYPE_F16 ? 256 : 0; }
+int64_t bwd_workspace(int64_t B, int64_t N, int64_t H, int64_t Hkv, int64_t D, int64_t window, int64_t sinks,
+                      int dtype) {
   window = window < N ? window : N;
   sinks = sinks < N ? sinks : N;
   const KeyPlan ks = simt_key_plan(B, N, H, Hkv, window, sinks);
   const KeyPlan kt = key_plan(B, N, H, Hkv, window, sinks, window_bwd_tc_tile(D), kTcMinBlocks, kTcCtas);
   const int64_t simt = key_partial_floats(ks, B, Hkv, D), tc = key_partial_floats(kt, B, Hkv, D);
-  return round256(4 * B * N * H) + round256(4 * (simt > tc ? simt : tc));
+  return round256(4 * B * N * H) + peak_bytes(dtype) + round256(4 * (simt > tc ? simt : tc));
 }
 
 int check_cache(int64_t S, int64_t Hkv, int64_t D, int64_t n_pages, int64_t page, int64_t max_pages, int dtype) {
@@ -136,7 +138,7 @@ extern "C" int64_t longnet_window_bwd_workspace_bytes(int64_t B, int64_t N, int6
                                                       int64_t window, int64_t sinks, int dtype) {
   const int rc = check_window(B, N, H, Hkv, D, window, sinks, dtype);
   if (rc) return rc;
-  return bwd_workspace(B, N, H, Hkv, D, window, sinks);
+  return bwd_workspace(B, N, H, Hkv, D, window, sinks, dtype);
 }
 
 extern "C" int longnet_window_attn_bwd(const void* q, const void* k, const void* v, const void* out,
@@ -168,7 +170,8 @@ extern "C" int longnet_window_attn_bwd(const void* q, const void* k, const void*
   g.dk = dk;
   g.dv = dv;
   g.delta = static_cast<float*>(workspace);
-  g.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + round256(4 * B * N * H));
+  g.peaks = reinterpret_cast<float*>(static_cast<char*>(workspace) + round256(4 * B * N * H));
+  g.partial = reinterpret_cast<float*>(reinterpret_cast<char*>(g.peaks) + peak_bytes(dtype));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return tc && impl != LONGNET_IMPL_SIMT ? launch_window_bwd_tc(a, g, st) : launch_window_bwd_simt(a, g, st);
 }

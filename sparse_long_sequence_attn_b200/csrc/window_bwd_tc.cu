@@ -15,7 +15,13 @@
 //     window of 64: 2.6e-3 -> 2.4e-3, where the plain 32-bit form rounded once has
 //     1.7e-3);
 //   - in fp16, P is rounded as 2^8 P, since a weight of one in thousands of keys
-//     is below that format's normal range; dV is scaled back at the end.
+//     is below that format's normal range; dV is scaled back at the end.  And dS
+//     is rounded as 2^e dS, where gradients may be of any size: e is such that
+//     2^15 >= 2^e 2 max |dout_x| max |v_j| >= |2^e dS| (the norms' maxima are found by the
+//     pass that makes delta, or one of its own: launch_window_peaks); dQ and dK
+//     are scaled back at the end.  (dk of 4096 tokens, window 2048, D = 64, dout
+//     of 1e-4: relative error 1.5e-2 without, 2.7e-3 with, which is the exact
+//     gradient's own rounding.)
 //
 // Design.  Two kernels, so that no gradient row is summed by two CTAs and no
 // atomics are needed (the same bits every run), at the price of computing the
@@ -47,8 +53,8 @@
 // -lse and -delta, the same for all 32 lanes, cost a load's full bandwidth (512
 // bytes of registers for 16).  Key-centric up to D = 64 they are therefore added
 // by the tensor cores: the tiles get a further 16 operand columns, constants,
-// and the blocks three parts of each number in the input format (24 bits or
-// more of it), which makes the scores s - lse / scale and dP - delta.
+// and the blocks three parts of each number in the input format, which makes
+// the scores s - lse / scale and dP - delta (three_parts: what the parts hold).
 // Warps 0-15 compute (slot 0, slot 1, and the same for the other half), warp 16
 // loads (TMA; its lanes fetch lse and delta), warps 17 and 18 issue, one for each
 // tile (one tile: warp 17 alone, as both slots add to the same accumulators).  Every wait is bounded.
@@ -94,7 +100,7 @@ struct B : Panels<kD> {
   // Query-centric up to D = 64, TMEM has room for dS beside the scores (two
   // buffers a tile): both products of the next block run during this one's.
   static constexpr bool kBeside = !kKeys && kD <= 64;
-  static constexpr int kFoldBytes = kFold ? kTile * 32 : 0;  // the tiles' extra columns: 128 rows of 16
+  static constexpr int kFoldBytes = kFold ? 2 * kTile * 32 : 0;  // the extra columns of K's and of V's tiles: 128 rows of 16
   static constexpr int kStageBytes = 2 * kBlkBytes + (kFold ? 2 * kBlk * 32 : kKeys ? 1024 : 0);  // two blocks, then these
   static constexpr int kStages = kD == 128 ? (kKeys ? 4 : 3) : 6;
   static constexpr int kStage0 = kTiles * 2 * kTileBytes;
@@ -123,19 +129,31 @@ struct Run {
 
 // P and dS of 32 streamed rows for this thread's tile row, packed in pairs:
 // P = 2^(s scale log2(e) - lse log2(e)), dS = P (dP - delta); 0 where keep has
-// no bit.  Key-centric in fp16, P is 2^8 P (its lse says so) and dP and delta
-// come times 2^-8.
+// no bit.  In fp16, dS comes times the call's unit 2^e; key-centric, P is 2^8 P
+// (its lse says so), so that 2^e dS is 2^8 P times 2^(e-8) (dP - delta).
 template <int kFmt>
 constexpr float kPScale = kFmt == kFmtF16 ? 256.f : 1.f;
 
-// x as three parts of the input format whose sum, times the tiles' constant
-// kUnit, is x to 2^-24 or better.  fp16: kUnit 256 keeps parts of |x| up to 1.6e7
-// in range, and what is lost below its range under 1e-5.
+// 2^e from the largest |dout_x|^2 and |v_j|^2: |dP| <= B = |dout_x| |v_j| < 2^k, and
+// delta, a mean of dP, too, so e = 14 - k keeps 2^e (dP - delta) within 2^15.  (1
+// when there is nothing to scale.)
+__device__ __forceinline__ float grad_unit(float dout2, float v2) {
+  const float b2 = dout2 * v2;  // of fp16 values: 0 or from 2^-96 to 2^79
+  if (b2 == 0.f) return 1.f;
+  const int k = (((int)(__float_as_uint(b2) >> 23) - 127) >> 1) + 1;
+  return __uint_as_float((uint32_t)(127 + 14 - k) << 23);
+}
+
+// x as three parts of the input format whose sum, times the tiles' constant, is
+// x: by is 1 / constant.  bf16, constant 1: to 2^-24 of x.  fp16: to 2^-33 of x, or
+// 2^-25 of the constant where that is more.  For lse / scale the constant is 256,
+// which keeps |x| up to 1.6e7 in range and |x| to 1e-5; for delta it is 2^-e, as
+// far as fp16 has it, which leaves parts of at most 2^15 and an error of 2^-39 of
+// the largest |dP| there may be.
+constexpr float kLseUnit = 256.f;
 template <int kFmt>
-constexpr float kUnit = kFmt == kFmtF16 ? 256.f : 1.f;
-template <int kFmt>
-__device__ __forceinline__ uint4 three_parts(float x) {
-  x *= 1.f / kUnit<kFmt>;
+__device__ __forceinline__ uint4 three_parts(float x, float by) {
+  x *= by;
   float hi, mid, none;
   unpack2<kFmt>(pack2<kFmt>(x, 0.f), hi, none);
   unpack2<kFmt>(pack2<kFmt>(x - hi, 0.f), mid, none);
@@ -145,19 +163,21 @@ __device__ __forceinline__ uint4 three_parts(float x) {
 __device__ __forceinline__ int fold_at(int r, int c) { return r * 32 + ((c ^ ((r >> 2) & 1)) << 4); }
 
 // The same with -lse and -delta already in sr (times the softmax scale) and dr.
+// up2: 2^(e-8) in fp16, twice.
 template <int kFmt, bool kMask>
 __device__ __forceinline__ void p_ds_folded(const uint32_t (&sr)[32], const uint32_t (&dr)[32], uint64_t sc2,
-                                            uint32_t keep, uint32_t (&pk)[16], uint32_t (&dk)[16]) {
+                                            uint64_t up2, uint32_t keep, uint32_t (&pk)[16], uint32_t (&dk)[16]) {
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
     float x0, x1;
     const uint64_t s2 = f32x2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-    // fp16: 2^8 P for dV, P for dS
+    // fp16: 2^8 P
     f32x2_split(kPScale<kFmt> == 1.f ? mul_f32x2(s2, sc2) : fma_f32x2(s2, sc2, f32x2(8.f, 8.f)), x0, x1);
     float p0 = ex2(x0), p1 = ex2(x1), d0, d1;
-    uint64_t pp = f32x2(p0, p1);
-    if (kPScale<kFmt> != 1.f) pp = mul_f32x2(pp, f32x2(1.f / kPScale<kFmt>, 1.f / kPScale<kFmt>));
-    f32x2_split(mul_f32x2(pp, f32x2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1]))), d0, d1);
+    const uint64_t pp = f32x2(p0, p1);
+    uint64_t dp = f32x2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1]));
+    if (kFmt == kFmtF16) dp = mul_f32x2(dp, up2);
+    f32x2_split(mul_f32x2(pp, dp), d0, d1);
     if (kMask) {
       const bool v0 = (keep >> c) & 1, v1 = (keep >> (c + 1)) & 1;
       p0 = v0 ? p0 : 0.f;
@@ -170,10 +190,12 @@ __device__ __forceinline__ void p_ds_folded(const uint32_t (&sr)[32], const uint
   }
 }
 
+// The others, with -lse and -delta of the columns or of the row, delta in fp16
+// times up2: key-centric 2^(e-8), query-centric 2^e, twice.
 template <int kFmt, bool kKeys, bool kMask>
 __device__ __forceinline__ void p_ds_half(const uint32_t (&sr)[32], const uint32_t (&dr)[32], const float* nl_col,
                                           const float* nd_col, uint64_t nl_row, uint64_t nd_row, uint64_t sc2,
-                                          uint32_t keep, uint32_t (&pk)[16], uint32_t (&dk)[16]) {
+                                          uint64_t up2, uint32_t keep, uint32_t (&pk)[16], uint32_t (&dk)[16]) {
 #pragma unroll
   for (int c = 0; c < 32; c += 4) {
     uint64_t nl[2], nd[2];
@@ -195,9 +217,7 @@ __device__ __forceinline__ void p_ds_half(const uint32_t (&sr)[32], const uint32
                   x1);
       float p0 = ex2(x0), p1 = ex2(x1), d0, d1;
       const uint64_t dp = f32x2(__uint_as_float(dr[c + e]), __uint_as_float(dr[c + e + 1]));
-      constexpr float kDown = kKeys ? 1.f / kPScale<kFmt> : 1.f;
-      f32x2_split(mul_f32x2(f32x2(p0, p1), kDown == 1.f ? add_f32x2(dp, nd[e / 2])
-                                                        : fma_f32x2(dp, f32x2(kDown, kDown), nd[e / 2])),
+      f32x2_split(mul_f32x2(f32x2(p0, p1), kFmt == kFmtF16 ? fma_f32x2(dp, up2, nd[e / 2]) : add_f32x2(dp, nd[e / 2])),
                   d0, d1);
       if (kMask) {
         const bool v0 = (keep >> (c + e)) & 1, v1 = (keep >> (c + e + 1)) & 1;
@@ -308,13 +328,23 @@ __device__ __forceinline__ void bwd_body(const AttnArgs& a, const WindowBwdArgs&
     *abort_flag = 0;
     fence_barrier_init();
   }
+  // fp16: the call's unit 2^e, and the constant of delta's parts, 2^-e as far as
+  // fp16 holds it
+  float unit = 1.f, part_unit = 1.f;
+  if constexpr (kFmt == kFmtF16) {
+    unit = grad_unit(g.peaks[0], g.peaks[1]);
+    part_unit = fminf(fmaxf(1.f / unit, 5.9604645e-8f), 32768.f);  // 2^-24, 2^15
+  }
   if (LL::kFold) {
     // the tiles' extra columns, three constants and zeros, and the blocks'
     // second chunk of theirs, zeros
-    const uint32_t one = pack2<kFmt>(kUnit<kFmt>, kUnit<kFmt>);
-    for (int e = threadIdx.x; e < kTile * 2; e += kThreads)
-      *reinterpret_cast<uint4*>(smem + LL::kFold0 + fold_at(e >> 1, e & 1)) =
+    for (int e = threadIdx.x; e < 2 * kTile * 2; e += kThreads) {
+      const int w = e / (2 * kTile);  // K's, V's
+      const float c = w ? part_unit : kFmt == kFmtF16 ? kLseUnit : 1.f;
+      const uint32_t one = pack2<kFmt>(c, c);
+      *reinterpret_cast<uint4*>(smem + LL::kFold0 + w * kTile * 32 + fold_at((e >> 1) % kTile, e & 1)) =
           (e & 1) ? make_uint4(0, 0, 0, 0) : make_uint4(one, one & 0xffffu, 0, 0);
+    }
     for (int e = threadIdx.x; e < S * 2 * kBlk; e += kThreads)
       *reinterpret_cast<uint4*>(sStage + (e / (2 * kBlk)) * LL::kStageBytes + 2 * LL::kBlkBytes +
                                 (e / kBlk % 2) * kBlk * 32 + fold_at(e % kBlk, 1)) = make_uint4(0, 0, 0, 0);
@@ -397,8 +427,9 @@ __device__ __forceinline__ void bwd_body(const AttnArgs& a, const WindowBwdArgs&
         uint8_t* fold = stage + 2 * LL::kBlkBytes;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          *reinterpret_cast<uint4*>(fold + fold_at(lane + 32 * e, 0)) = three_parts<kFmt>(-l2[e] / a.scale);
-          *reinterpret_cast<uint4*>(fold + kBlk * 32 + fold_at(lane + 32 * e, 0)) = three_parts<kFmt>(-dl[e]);
+          *reinterpret_cast<uint4*>(fold + fold_at(lane + 32 * e, 0)) =
+              three_parts<kFmt>(-l2[e] / a.scale, kFmt == kFmtF16 ? 1.f / kLseUnit : 1.f);
+          *reinterpret_cast<uint4*>(fold + kBlk * 32 + fold_at(lane + 32 * e, 0)) = three_parts<kFmt>(-dl[e], 1.f / part_unit);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       } else if (kKeys) {
@@ -406,7 +437,7 @@ __device__ __forceinline__ void bwd_body(const AttnArgs& a, const WindowBwdArgs&
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           sl[lane + 32 * e] = fmaf(-l2[e], kLog2e, kFmt == kFmtF16 ? 8.f : 0.f);
-          sl[kBlk + lane + 32 * e] = -dl[e] * (1.f / kPScale<kFmt>);
+          sl[kBlk + lane + 32 * e] = -dl[e] * (unit / kPScale<kFmt>);
         }
       }
       __syncwarp();  // the bytes are expected before the phase can complete
@@ -448,7 +479,7 @@ __device__ __forceinline__ void bwd_body(const AttnArgs& a, const WindowBwdArgs&
                       (pn > 0 || kk > 0) ? 1u : 0u);
         if (LL::kFold) {
           constexpr uint32_t kHi = (uint32_t)(8 * 32 >> 4) | (1u << 14) | (6u << 29);  // 32-byte rows and swizzle
-          const uint32_t fa = (smem_u32(smem + LL::kFold0) >> 4) | (1u << 16);
+          const uint32_t fa = (smem_u32(smem + LL::kFold0 + w * kTile * 32) >> 4) | (1u << 16);
           const uint32_t fb = b_lo + (2 * LL::kBlkBytes >> 4);
           mma_ss_if(leader, tmem + 128 * slot + 64 * w, desc_from(fa, kHi), desc_from(fb + w * (kBlk * 32 >> 4), kHi),
                     kIdScore, 1u);
@@ -631,7 +662,9 @@ __device__ __forceinline__ void bwd_body(const AttnArgs& a, const WindowBwdArgs&
       delta = hf ? other + (d0 + d1) : (d0 + d1) + other;
     }
     if (!kKeys && passes == 2 && row_ok && hf == 0) g.delta[stat] = delta;  // the key-centric kernel's
-    const uint64_t nd_row = f32x2(-delta, -delta);
+    const uint64_t nd_row = f32x2(-delta * unit, -delta * unit);
+    const float up = kKeys ? unit / kPScale<kFmt> : unit;
+    const uint64_t up2 = f32x2(up, up);
     for (int n = r.begin; n < r.end && ok; n += r.step) {
       const float* sl = reinterpret_cast<const float*>(sStage + (n % S) * LL::kStageBytes + 2 * LL::kBlkBytes);
       uint32_t keep;  // the half's columns that pair with this row, as bits
@@ -660,13 +693,13 @@ __device__ __forceinline__ void bwd_body(const AttnArgs& a, const WindowBwdArgs&
       }
       if (LL::kFold) {
         if (whole)
-          p_ds_folded<kFmt, false>(sr, dr, sc2, 0, pk, dk);
+          p_ds_folded<kFmt, false>(sr, dr, sc2, up2, 0, pk, dk);
         else
-          p_ds_folded<kFmt, true>(sr, dr, sc2, keep, pk, dk);
+          p_ds_folded<kFmt, true>(sr, dr, sc2, up2, keep, pk, dk);
       } else if (whole)
-        p_ds_half<kFmt, kKeys, false>(sr, dr, sl + 32 * hf, sl + kBlk + 32 * hf, nl_row, nd_row, sc2, 0, pk, dk);
+        p_ds_half<kFmt, kKeys, false>(sr, dr, sl + 32 * hf, sl + kBlk + 32 * hf, nl_row, nd_row, sc2, up2, 0, pk, dk);
       else
-        p_ds_half<kFmt, kKeys, true>(sr, dr, sl + 32 * hf, sl + kBlk + 32 * hf, nl_row, nd_row, sc2, keep, pk, dk);
+        p_ds_half<kFmt, kKeys, true>(sr, dr, sl + 32 * hf, sl + kBlk + 32 * hf, nl_row, nd_row, sc2, up2, keep, pk, dk);
       if (kKeys) LN_TMEM_ST16(slot + 64, pk);
       LN_TMEM_ST16(LL::kBeside ? tmem + lane_base + kColDs + 64 * st + 32 * (done & 1) + 16 * hf : slot + 80, dk);
       tmem_wait_st();
@@ -687,7 +720,7 @@ __device__ __forceinline__ void bwd_body(const AttnArgs& a, const WindowBwdArgs&
       for (int w = 0; w < (kKeys ? 2 : 1); ++w) {
         if (kTiles == 1 ? w != st || hf : w != hf) continue;
         // w = 0: dV or dQ, w = 1: dK
-        const float sc = kKeys && w == 0 ? 1.f / kPScale<kFmt> : a.scale;
+        const float sc = kKeys && w == 0 ? 1.f / kPScale<kFmt> : a.scale / unit;
         const uint32_t acc = tmem + lane_base + kColAcc + (kTiles == 2 ? (kKeys ? 2 : 1) * kD * st : 0) + w * kD;
         uint16_t* dst = kKeys ? static_cast<uint16_t*>(w == 0 ? g.dv : g.dk) + (((int64_t)s * N + j) * a.Hkv + f) * kD
                               : static_cast<uint16_t*>(g.dq) + (((int64_t)s * N + i) * a.H + h) * kD;
@@ -779,6 +812,7 @@ template <int kFmt, int kD>
 int launch_typed(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream) {
   EncodeTiledFn enc = get_encoder();
   if (!enc) return LONGNET_ERR_CUDA;
+  constexpr bool kF16 = kFmt == kFmtF16;
   BPlan pk, pq;
   pk.tokens = kBlk / a.G;
   pq.tokens = kTile / a.G;
@@ -799,7 +833,7 @@ int launch_typed(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream)
   const int64_t pairs = ((int64_t)a.nq_max + 2 * pq.tokens - 1) / (2 * pq.tokens);
   if (!pq.exact) {
     if ((pairs + pk.key.items()) * a.S * a.Hkv > INT32_MAX) return LONGNET_ERR_UNSUPPORTED;
-    int rc = launch_window_delta(a, g, stream);
+    int rc = kF16 ? launch_window_peaks(a, g, true, stream) : launch_window_delta(a, g, stream);
     if (rc) return rc;
     constexpr int smem = LK::kSmem > LQ::kSmem ? LK::kSmem : LQ::kSmem;
     if (!opt_in_smem<both_kernel<kFmt, kD>>(smem)) return LONGNET_ERR_CUDA;
@@ -807,8 +841,10 @@ int launch_typed(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream)
                       smem, stream, a, g, mq, mk, pq, pk, (int)pairs);
     return rc ? rc : launch_key_reduce(a, g, pk.key, stream);
   }
+  int rc = kF16 ? launch_window_peaks(a, g, false, stream) : LONGNET_OK;
+  if (rc) return rc;
   // dq first: it leaves delta for dk and dv
-  int rc = launch_after(bwd_kernel<kFmt, kD, false>, dim3((unsigned)pairs, (unsigned)(a.S * a.Hkv)), kThreads, LQ::kSmem,
+  rc = launch_after(bwd_kernel<kFmt, kD, false>, dim3((unsigned)pairs, (unsigned)(a.S * a.Hkv)), kThreads, LQ::kSmem,
                         stream, a, g, mq, pq);
   if (rc) return rc;
   rc = launch_after(bwd_kernel<kFmt, kD, true>, dim3((unsigned)pk.key.items(), (unsigned)(a.S * a.Hkv)), kThreads, LK::kSmem,

@@ -428,33 +428,85 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const AttnArgs a, flo
   }
 }
 
-// delta of every row, [S, H, N] fp32: a warp's 8 lanes per row.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) delta_kernel(const AttnArgs a, const T* out, const T* dout, float* delta) {
+// The sum of a 16-byte chunk's products x y.
+template <typename T>
+__device__ __forceinline__ float dot16(const uint4& x, const uint4& y, float acc) {
+  T a[16 / sizeof(T)], b[16 / sizeof(T)];
+  *reinterpret_cast<uint4*>(a) = x;
+  *reinterpret_cast<uint4*>(b) = y;
+#pragma unroll
+  for (int i = 0; i < (int)(16 / sizeof(T)); ++i) acc = fmaf(to_f<T>(a[i]), to_f<T>(b[i]), acc);
+  return acc;
+}
+
+// delta of every row, [S, H, N] fp32: a warp's 8 lanes per row.  kPeaks: also the
+// largest |dout_x|^2 and |v_j|^2, to peaks[0] and [1], which are 0 on entry (rows with
+// an infinity or NaN not counted; a maximum does not depend on the atomics' order);
+// with delta null, these alone.
+template <typename T, int D, bool kPeaks>
+__global__ void __launch_bounds__(256) delta_kernel(const AttnArgs a, const T* out, const T* dout, float* delta,
+                                                    float* peaks) {
   constexpr int kVec = 16 / sizeof(T);
   constexpr int kLanes = D / kVec < 8 ? D / kVec : 8;
   const int64_t rows = a.T * a.H;
   const int64_t per = 256 / kLanes;
   const int sub = threadIdx.x % kLanes;
+  float top[2] = {0.f, 0.f};
+  auto sum = [&](float x) {
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+  };
   for (int64_t r0 = blockIdx.x * per; r0 < rows; r0 += gridDim.x * per) {
     const int64_t r = r0 + threadIdx.x / kLanes;
-    float acc = 0.f;
+    float acc = 0.f, square = 0.f;
     if (r < rows) {
 #pragma unroll
       for (int c = sub * kVec; c < D; c += kLanes * kVec) {
-        T x[kVec], y[kVec];
-        *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(out + r * D + c);
-        *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(dout + r * D + c);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) acc = fmaf(to_f<T>(x[i]), to_f<T>(y[i]), acc);
+        const uint4 y = *reinterpret_cast<const uint4*>(dout + r * D + c);
+        if (!kPeaks || delta) acc = dot16<T>(*reinterpret_cast<const uint4*>(out + r * D + c), y, acc);
+        if (kPeaks) square = dot16<T>(y, y, square);
       }
     }
-#pragma unroll
-    for (int o = kLanes / 2; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (r < rows && sub == 0) {
+    acc = sum(acc);
+    if (kPeaks) {
+      square = sum(square);
+      if (square < INFINITY) top[0] = fmaxf(top[0], square);
+    }
+    if (r < rows && sub == 0 && (!kPeaks || delta)) {
       const int64_t h = r % a.H, t = r / a.H;
       const int64_t s = t / a.nq_max, i = t % a.nq_max;
       delta[(s * a.H + h) * a.nq_max + i] = acc;
+    }
+  }
+  if constexpr (kPeaks) {
+    const T* v = static_cast<const T*>(a.v);
+    const int64_t keys = a.T * a.Hkv;
+    for (int64_t r0 = blockIdx.x * per; r0 < keys; r0 += gridDim.x * per) {
+      const int64_t r = r0 + threadIdx.x / kLanes;
+      float square = 0.f;
+      if (r < keys) {
+#pragma unroll
+        for (int c = sub * kVec; c < D; c += kLanes * kVec) {
+          const uint4 y = *reinterpret_cast<const uint4*>(v + r * D + c);
+          square = dot16<T>(y, y, square);
+        }
+      }
+      square = sum(square);
+      if (square < INFINITY) top[1] = fmaxf(top[1], square);
+    }
+    __shared__ uint32_t s_top[2][8];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {  // (numbers from 0 up compare as their bits do)
+      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(top[w]));
+      if (threadIdx.x % 32 == 0) s_top[w][threadIdx.x / 32] = m;
+    }
+    __syncthreads();
+    if (threadIdx.x < 2) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, s_top[threadIdx.x][i]);
+      if (m) atomicMax(reinterpret_cast<uint32_t*>(peaks) + threadIdx.x, m);
     }
   }
 }
@@ -768,12 +820,25 @@ int bwd(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t st) {
   return launch_key_reduce(a, g, kp, st);
 }
 template <typename T, int D>
-int delta(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t st) {
+int delta_blocks(const AttnArgs& a) {
   const int64_t rows = a.T * a.H, per = 256 / (D / (16 / (int)sizeof(T)) < 8 ? D / (16 / (int)sizeof(T)) : 8);
-  int64_t blocks = (rows + per - 1) / per;
-  if (blocks > 148 * 16) blocks = 148 * 16;
-  delta_kernel<T, D><<<(unsigned)blocks, 256, 0, st>>>(a, static_cast<const T*>(a.out),
-                                                       static_cast<const T*>(g.dout), g.delta);
+  const int64_t blocks = (rows + per - 1) / per;
+  return (int)(blocks < 148 * 16 ? blocks : 148 * 16);
+}
+template <typename T, int D>
+int delta(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t st) {
+  delta_kernel<T, D, false><<<delta_blocks<T, D>(a), 256, 0, st>>>(
+      a, static_cast<const T*>(a.out), static_cast<const T*>(g.dout), g.delta, nullptr);
+  return ok_launch();
+}
+template <int D>
+int peaks(const AttnArgs& a, const WindowBwdArgs& g, bool with_delta, cudaStream_t st) {
+  if (cudaMemsetAsync(g.peaks, 0, 8, st) != cudaSuccess) {
+    cudaGetLastError();
+    return LONGNET_ERR_CUDA;
+  }
+  delta_kernel<__half, D, true><<<delta_blocks<__half, D>(a), 256, 0, st>>>(
+      a, static_cast<const __half*>(a.out), static_cast<const __half*>(g.dout), with_delta ? g.delta : nullptr, g.peaks);
   return ok_launch();
 }
 
@@ -797,6 +862,18 @@ int launch_window_bwd_simt(const AttnArgs& a, const WindowBwdArgs& g, cudaStream
 }
 int launch_window_delta(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream) {
   return LN_BY_TYPE(ws::delta, a, g, stream);
+}
+int launch_window_peaks(const AttnArgs& a, const WindowBwdArgs& g, bool with_delta, cudaStream_t stream) {
+  switch (a.D) {
+    case 16:
+      return ws::peaks<16>(a, g, with_delta, stream);
+    case 32:
+      return ws::peaks<32>(a, g, with_delta, stream);
+    case 64:
+      return ws::peaks<64>(a, g, with_delta, stream);
+    default:
+      return ws::peaks<128>(a, g, with_delta, stream);
+  }
 }
 
 int launch_key_reduce(const AttnArgs& a, const WindowBwdArgs& g, const KeyPlan& k, cudaStream_t stream) {
