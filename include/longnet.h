@@ -509,7 +509,8 @@ int longnet_paged_append(const void* k_tok, const void* v_tok, void* k_pages, vo
  * longnet_window_attn_fwd; window = 0: every earlier key.
  *   - q, out: [T, H, D] of dtype; lse: fp32 [T, H] or NULL.  A token at a
  *     negative position (kv_len below its sequence's new tokens) sees
- *     nothing: out 0, lse -inf.
+ *     nothing: out 0, lse -inf.  (A row with a NaN among its scores has out and
+ *     lse NaN, and adds NaN to the weights of the keys it sees.)
  *   - max_q: no sequence has more new tokens (it sizes the launch, so one
  *     captured launch serves every batch within it).  A sequence with more:
  *     LONGNET_ERR_DEVICE_BOUNDS, and it is skipped.

@@ -387,8 +387,8 @@ __global__ void __launch_bounds__(kThreads)
         acc.z = fmaf(sc, t.z, acc.z);
         acc.w = fmaf(sc, t.w, acc.w);
       }
-      const float inv = ll > 0.f ? 1.f / ll : 0.f;
-      const float lse2 = ll > 0.f ? mm + log2f(ll) : -INFINITY;
+      const float inv = ll == 0.f ? 0.f : 1.f / ll;  // (a sum of NaN stays one)
+      const float lse2 = ll == 0.f ? -INFINITY : mm + log2f(ll);
       if (direct) {
         const int i = r / a.G, h = p.f * a.G + r % a.G;
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + ((q.q0 + i) * a.H + h) * (int64_t)kD + d) =
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       }
     }
     if (!mine) return;
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int i = r / a.G, h = f * a.G + r % a.G;
     if (on) {
       uint16_t* o = static_cast<uint16_t*>(a.out) + ((q.q0 + i) * a.H + h) * (int64_t)kD + lane * kE;
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
           *reinterpret_cast<uint32_t*>(o + e) = pack2<kFmt>(acc[e] * inv, acc[e + 1] * inv);
       }
     }
-    if (lane == 0 && a.lse) a.lse[(q.q0 + i) * a.H + h] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+    if (lane == 0 && a.lse) a.lse[(q.q0 + i) * a.H + h] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
     return;
   }
   // ---- weights
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       for (int c = lane; c < p.count; c += 32) sum += ex2(A.part_lse[(p.first + c) * A.rows + r] - base);
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (sum > 0.f) l2 = m + log2f(sum);
+      if (sum != 0.f) l2 = m + log2f(sum);
     }
     if (lane == 0) s_lse[r] = l2;
   }

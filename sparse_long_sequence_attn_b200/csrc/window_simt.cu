@@ -355,9 +355,9 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a) {
         sum = fmaf(w, cluster.map_shared_rank(sL, c)[i], sum);
         o = fmaf(w, cluster.map_shared_rank(sA, c)[e], o);
       }
-      static_cast<T*>(a.out)[R.elem(i, a.H, D) + e % D] = from_f<T>(o * (sum > 0.f ? 1.f / sum : 0.f));
+      static_cast<T*>(a.out)[R.elem(i, a.H, D) + e % D] = from_f<T>(o * (sum == 0.f ? 0.f : 1.f / sum));
       if (e % D == 0 && a.lse)
-        a.lse[lse_index(a, R.q, R.s, R.token(i), R.head(i))] = sum > 0.f ? (base + log2f(sum)) * kLn2 : -INFINITY;
+        a.lse[lse_index(a, R.q, R.s, R.token(i), R.head(i))] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
     }
     cluster.sync();  // no CTA ends while another reads its part
     return;
@@ -366,12 +366,12 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(const AttnArgs a) {
   for (int r = 0; r < RT; ++r) {
     const int i = RT * ty + r;
     if (i >= R.n) continue;
-    const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
+    const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];  // (a sum of NaN stays one)
     T* o = static_cast<T*>(a.out) + R.elem(i, a.H, D);
 #pragma unroll
     for (int c = 0; c < L<D>::kC; ++c) o[L<D>::col(tx, c)] = from_f<T>(acc.at(r, c) * inv);
     if (tx == 0 && a.lse)
-      a.lse[lse_index(a, R.q, R.s, R.token(i), R.head(i))] = l[r] > 0.f ? (m[r] + log2f(l[r])) * kLn2 : -INFINITY;
+      a.lse[lse_index(a, R.q, R.s, R.token(i), R.head(i))] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
   }
 }
 

@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && cnt > 0) ok = wt.wait_warp(bar_q, 0);
     if (ok && ta < tb) {
       tc_fence_after();
-      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      const float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // (a sum of NaN stays one)
       const int h = f * a.G + row % a.G;
       const bool whole = !kPaged || (!alternate && pieces == 1);
       const int64_t prow = ((int64_t)slot * 2 + st) * plan.slot_rows + row;
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                              static_cast<uint16_t*>(a.out) + ((q.q0 + i) * a.H + h) * (int64_t)kD, row_ok);
       }
       if (row_ok) {
-        const float lse2 = l_run > 0.f ? m_use + log2f(l_run) : -INFINITY;
+        const float lse2 = l_run == 0.f ? -INFINITY : m_use + log2f(l_run);
         if (!whole)
           plan.part_lse[prow] = lse2;
         else if (a.lse)
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnA
         }
       }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     if (on) {
       uint16_t* o = static_cast<uint16_t*>(a.out) + ((q.q0 + i) * a.H + h) * (int64_t)kD + lane * kE;
       if constexpr (kE == 1) {
@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnA
           *reinterpret_cast<uint32_t*>(o + e) = pack2<kFmt>(acc[e] * inv, acc[e + 1] * inv);
       }
     }
-    if (lane == 0 && a.lse) a.lse[lse_index(a, q, s, i, h)] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+    if (lane == 0 && a.lse) a.lse[lse_index(a, q, s, i, h)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
   }
 }
 
