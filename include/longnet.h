@@ -526,6 +526,11 @@ int longnet_paged_append(const void* k_tok, const void* v_tok, void* k_pages, vo
  *     longnet_paged_workspace_bytes bytes (weights: 1 when they are asked
  *     for), overlapping no tensor; contents on entry do not matter; NULL when
  *     0 bytes are needed.  Calls that may run at the same time need one each.
+ *     It grows with S and with the rows, max_q H / Hkv.  With weights and at most
+ *     16 rows it also holds the scores, 4 bytes for each row and key that the
+ *     sizes allow to be visible (max_pages * page, or the window and the sinks),
+ *     of as many sequences as fit 256 MiB, or of one: the others follow in
+ *     launches of their own.
  *   The same inputs give the same bits.
  */
 int64_t longnet_paged_workspace_bytes(int64_t S, int64_t max_q, int64_t H, int64_t Hkv, int64_t D,

@@ -21,7 +21,10 @@
 //
 // Weight sums.  The scores are written to the workspace as they are made (4
 // bytes per row and key, against 2 D bytes of the key itself), and the join
-// turns them into weights when lse is known, so keys are not read again.
+// turns them into weights when lse is known, so keys are not read again.  They
+// lie in the order of the visible blocks, so a window's keys alone have a
+// place, and a call whose scores would take more than kMaxScores runs as
+// several, each of as many sequences as fit.
 //
 // Measured (with the join and the append; the kernel itself in brackets): 4
 // sequences of up to 131072 keys, 16/2 heads of 128, fp16: 87 us (75, 6.1 TB/s); 64
@@ -56,7 +59,8 @@ struct Args {
   int* plan;         // [S + 1] blocks before each sequence (of one head), then the run length
   float* part_out;   // [slots, rows, D] normalised pieces
   float* part_lse;   // [slots, rows] log2 domain
-  float* scores;     // [S Hkv, rows, keys] log2 domain, or null
+  float* scores;     // [S Hkv, rows, kept] log2 domain, key by key of the visible blocks, or null
+  int64_t kept;      // keys that the visible blocks have, at most
   float* weights;
 };
 
@@ -237,7 +241,6 @@ __global__ void __launch_bounds__(kThreads)
   }
   // -------------------------------------------------------------- compute
   const int gr = lane >> 2, t4 = lane & 3;
-  const int64_t keys = (int64_t)a.max_pages << a.page_shift;
   int it = 0;
   bool ok = true;  // a warp whose wait ran out goes on to the meetings below, without waiting or computing
   for (int64_t w = w0; w < w1;) {
@@ -295,11 +298,11 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             if (gr + 8 * e < rows) {
-              float* dst = A.scores + ((int64_t)pair * A.rows + gr + 8 * e) * keys + j0 + 2 * t4;
+              float* dst =
+                  A.scores + ((int64_t)pair * A.rows + gr + 8 * e) * A.kept + (p.n0 + n) * kBlk + 16 * warp + 2 * t4;
 #pragma unroll
               for (int nt = 0; nt < 2; ++nt)
-                if (j0 + 8 * nt + 2 * t4 < keys)  // keys is even
-                  *reinterpret_cast<float2*>(dst + 8 * nt) = make_float2(sc[nt][2 * e], sc[nt][2 * e + 1]);
+                *reinterpret_cast<float2*>(dst + 8 * nt) = make_float2(sc[nt][2 * e], sc[nt][2 * e + 1]);
             }
         }
         float base[2];
@@ -528,7 +531,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const Seq q = seq_of(a, s);
   if (j0 >= q.kv || q.nq == 0) return;
   const int rows = q.nq * a.G;
-  const Pieces p = pieces_of(A, s, f, A.plan[s + 1] - A.plan[s]);
+  const BlockList bl = blocks_of<kBlk>(a, q.first, q.kv - 1);
+  const Pieces p = pieces_of(A, s, f, bl.count);
   for (int r = warp; r < rows; r += kJoinThreads / 32) {
     float l2 = -INFINITY;
     if (p.count == 1) {
@@ -549,12 +553,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   __syncthreads();
   const int j = j0 + 4 * (int)threadIdx.x;  // keys is a multiple of 8, j of 4
   if (j >= q.kv) return;
+  const int block = j / kBlk;
+  if (block >= bl.n_sink && block < bl.win0) return;  // no row sees it
+  // the place of the key's block among the visible ones
+  const int64_t at = (int64_t)(block < bl.n_sink ? block : bl.n_sink + block - bl.win0) * kBlk + j % kBlk;
   float acc[4] = {};
 #pragma unroll 4
   for (int r = 0; r < rows; ++r) {
     const int x = q.first + r / a.G;
     if (x < 0) continue;
-    const float4 sc = *reinterpret_cast<const float4*>(A.scores + (pair * A.rows + r) * keys + j);
+    const float4 sc = *reinterpret_cast<const float4*>(A.scores + (pair * A.rows + r) * A.kept + at);
     const float v[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -568,6 +576,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 
 // ---- host
 constexpr int kMaxSeq = 2048;  // the numbering is kept in shared memory
+constexpr int64_t kMaxScores = (int64_t)1 << 26;  // floats: 256 MiB
 
 int rows_of(const AttnArgs& a) { return a.nq_max * a.G; }
 int ctas_of(const AttnArgs& a) {
@@ -577,18 +586,32 @@ int ctas_of(const AttnArgs& a) {
   return (int)(want < 296 ? want : 296);
 }
 int64_t round64(int64_t floats) { return (floats + 63) / 64 * 64; }  // 256 bytes
+// The keys of the blocks that a sequence's rows see, at most: all, or the
+// window of nq_max tokens and the sinks, in whole blocks.
+int64_t kept_keys(const AttnArgs& a) {
+  const int64_t all = (((int64_t)a.max_pages << a.page_shift) + kBlk - 1) / kBlk;
+  if (!a.window) return all * kBlk;
+  const int64_t seen = ((int64_t)a.window + a.nq_max - 2) / kBlk + 2 + ((int64_t)a.sinks + kBlk - 1) / kBlk;
+  return (seen < all ? seen : all) * kBlk;
+}
+// Sequences of one launch: all, or with weights as many as kMaxScores holds.
+int group_of(const AttnArgs& a, bool weights) {
+  if (!weights) return a.S;
+  const int64_t fit = kMaxScores / (a.Hkv * rows_of(a) * kept_keys(a));
+  return fit < 1 ? 1 : fit < a.S ? (int)fit : a.S;
+}
 struct Sizes {
   int64_t plan, out, lse, scores;  // floats, each rounded to 256 bytes
   int64_t all() const { return plan + out + lse + scores; }
 };
+// Of one launch over a's sequences.
 Sizes sizes_of(const AttnArgs& a, bool weights) {
   const int64_t slots = (int64_t)ctas_of(a) + (int64_t)a.S * a.Hkv;
-  const int64_t keys = (int64_t)a.max_pages << a.page_shift;
   Sizes z;
   z.plan = round64(a.S + 2);
   z.out = round64(slots * rows_of(a) * a.D);
   z.lse = round64(slots * rows_of(a));
-  z.scores = weights ? round64((int64_t)a.S * a.Hkv * rows_of(a) * keys) : 0;
+  z.scores = weights ? round64((int64_t)a.S * a.Hkv * rows_of(a) * kept_keys(a)) : 0;
   return z;
 }
 
@@ -603,6 +626,7 @@ int launch_typed(const AttnArgs& a, float* workspace, float* weights, cudaStream
   A.part_out = workspace + z.plan;
   A.part_lse = A.part_out + z.out;
   A.scores = weights ? A.part_lse + z.lse : nullptr;
+  A.kept = kept_keys(a);
   A.weights = weights;
   Maps maps;
   memset(&maps, 0, sizeof(maps));
@@ -629,6 +653,23 @@ int launch_typed(const AttnArgs& a, float* workspace, float* weights, cudaStream
                       0, stream, A, row_blocks);
 }
 
+int launch_group(const AttnArgs& a, float* workspace, float* weights, bool f16, cudaStream_t stream) {
+  switch (a.D) {
+    case 16:
+      return f16 ? launch_typed<tc::kFmtF16, 16>(a, workspace, weights, stream)
+                 : launch_typed<tc::kFmtBF16, 16>(a, workspace, weights, stream);
+    case 32:
+      return f16 ? launch_typed<tc::kFmtF16, 32>(a, workspace, weights, stream)
+                 : launch_typed<tc::kFmtBF16, 32>(a, workspace, weights, stream);
+    case 64:
+      return f16 ? launch_typed<tc::kFmtF16, 64>(a, workspace, weights, stream)
+                 : launch_typed<tc::kFmtBF16, 64>(a, workspace, weights, stream);
+    default:
+      return f16 ? launch_typed<tc::kFmtF16, 128>(a, workspace, weights, stream)
+                 : launch_typed<tc::kFmtBF16, 128>(a, workspace, weights, stream);
+  }
+}
+
 }  // namespace dc
 
 // At most 16 rows per key/value head and kMaxSeq sequences.
@@ -640,24 +681,26 @@ bool decode_supports(const AttnArgs& a) {
          (int64_t)a.S * a.Hkv * ((keys + dc::kBlk - 1) / dc::kBlk) < ((int64_t)1 << 30);
 }
 
-int64_t decode_workspace_floats(const AttnArgs& a, bool weights) { return dc::sizes_of(a, weights).all(); }
+int64_t decode_workspace_floats(const AttnArgs& a, bool weights) {
+  AttnArgs g = a;
+  g.S = dc::group_of(a, weights);
+  return dc::sizes_of(g, weights).all();
+}
 
-int launch_decode(const AttnArgs& a, float* workspace, float* weights, cudaStream_t stream) {
-  const bool f16 = a.dtype == LONGNET_DTYPE_F16;
-  switch (a.D) {
-    case 16:
-      return f16 ? dc::launch_typed<tc::kFmtF16, 16>(a, workspace, weights, stream)
-                 : dc::launch_typed<tc::kFmtBF16, 16>(a, workspace, weights, stream);
-    case 32:
-      return f16 ? dc::launch_typed<tc::kFmtF16, 32>(a, workspace, weights, stream)
-                 : dc::launch_typed<tc::kFmtBF16, 32>(a, workspace, weights, stream);
-    case 64:
-      return f16 ? dc::launch_typed<tc::kFmtF16, 64>(a, workspace, weights, stream)
-                 : dc::launch_typed<tc::kFmtBF16, 64>(a, workspace, weights, stream);
-    default:
-      return f16 ? dc::launch_typed<tc::kFmtF16, 128>(a, workspace, weights, stream)
-                 : dc::launch_typed<tc::kFmtBF16, 128>(a, workspace, weights, stream);
+int launch_decode(const AttnArgs& all, float* workspace, float* weights, cudaStream_t stream) {
+  const bool f16 = all.dtype == LONGNET_DTYPE_F16;
+  const int group = dc::group_of(all, weights != nullptr);
+  for (int s = 0; s < all.S; s += group) {
+    AttnArgs a = all;  // sequences [s, s + S): token rows stay where they are
+    a.S = all.S - s < group ? all.S - s : group;
+    a.cu_q += s;
+    a.kv_len += s;
+    a.table += (int64_t)s * a.max_pages;
+    float* w = weights ? weights + ((int64_t)s * a.Hkv * a.max_pages << a.page_shift) : nullptr;
+    const int rc = dc::launch_group(a, workspace, w, f16, stream);
+    if (rc) return rc;
   }
+  return LONGNET_OK;
 }
 
 }  // namespace longnet

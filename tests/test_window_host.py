@@ -104,3 +104,18 @@ def test_binding_refuses_other_tensors():
         bd.paged_append(q[0], q[0], q, q, q, q, torch.zeros((1, 1), dtype=torch.int32))
     with pytest.raises(bd.LongNetError):
         bd.longnet_window_bwd_workspace_bytes(1, 8, 3, 2, 16, 4, 0, torch.float32)
+
+
+def test_few_token_workspace_is_bounded():
+    """The scores kept for the weights: at most 256 MiB, or one sequence's, whatever the table's capacity; with a
+    window, of what it reaches."""
+    size = lambda *a, w=True: bd.longnet_paged_workspace_bytes(*a, torch.bfloat16, w)  # noqa: E731
+    for S, max_q, H, Hkv in ((64, 1, 32, 8), (64, 4, 32, 8), (256, 4, 32, 8), (2000, 1, 16, 1)):
+        plain = size(S, max_q, H, Hkv, 128, 64, 2048, 0, 0, w=False)
+        assert 0 < size(S, max_q, H, Hkv, 128, 64, 2048, 0, 0) - plain <= (256 << 20) + 1024
+        rows, seen = max_q * H // Hkv, (1024 + 4 + 3 * 64) + 64
+        windowed = size(S, max_q, H, Hkv, 128, 64, 2048, 1024, 4) - size(S, max_q, H, Hkv, 128, 64, 2048, 1024, 4, w=False)
+        assert windowed <= min(256 << 20, 4 * S * Hkv * rows * seen) + 1024
+    # one sequence's scores always fit
+    one = size(1, 4, 32, 8, 128, 256, 1 << 14, 0, 0)
+    assert one >= 4 * 8 * 16 * (1 << 22) and size(9, 4, 32, 8, 128, 256, 1 << 14, 0, 0) < one + (1 << 26)
