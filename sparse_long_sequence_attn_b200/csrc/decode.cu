@@ -231,12 +231,7 @@ __global__ void __launch_bounds__(kThreads)
       w += p.cnt;
     }
     // drain: every issued load has landed before the CTA may exit
-    if (lane == 0)
-      for (int i = it > stages ? it - stages : 0; i < it && ok; ++i)
-        if (!mbar_wait(bar_full + (i % stages), (i / stages) & 1, kWaitLimitNs)) {
-          record_status(a.status, kStatusTimeout);
-          break;
-        }
+    if (lane == 0) drain_loads(bar_full, it, stages, a.status);
     return;
   }
   // -------------------------------------------------------------- compute

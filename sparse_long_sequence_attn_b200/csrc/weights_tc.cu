@@ -186,11 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // drain: every issued load has landed before the CTA may exit
     if (lane == 0) {
       if (!mbar_wait(bar_k, 0, kWaitLimitNs)) record_status(a.status, kStatusTimeout);
-      for (int n = issued > S ? issued - S : 0; n < issued; ++n)
-        if (!mbar_wait(bar_full + (n % S), (n / S) & 1, kWaitLimitNs)) {
-          record_status(a.status, kStatusTimeout);
-          break;
-        }
+      drain_loads(bar_full, issued, S, a.status);
     }
   } else if (warp == kMma) {
     // ------------------------------------------------------------ MMA issue

@@ -448,11 +448,7 @@ __device__ __forceinline__ void bwd_body(const AttnArgs& a, const WindowBwdArgs&
     // drain: every issued load has landed before the CTA may exit
     if (lane == 0) {
       if (cnt > 0 && !mbar_wait(bar_tile, 0, kWaitLimitNs)) record_status(a.status, kStatusTimeout);
-      for (int n = issued > S ? issued - S : 0; n < issued; ++n)
-        if (!mbar_wait(bar_full + (n % S), (n / S) & 1, kWaitLimitNs)) {
-          record_status(a.status, kStatusTimeout);
-          break;
-        }
+      drain_loads(bar_full, issued, S, a.status);
     }
   } else if (warp >= kMma) {
     // ------------------------------------------------------------ MMA issue

@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       (int)(q.q0 + t0 + st * tpt));
     }
     int issued = 0;
+    bool tail_issued = false;
     for (int n = -ahead; n < cnt && ok; ++n, ++issued) {
       const int st = issued % S;
       if (issued >= S) ok = wt.wait_warp(bar_empty + st, ((issued / S) - 1) & 1);
@@ -304,10 +305,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (k) load_pages<kD>(a, q, s, f, block_key(n + ahead), kBlk, &maps.m[1], dst + LL::kHalf, bar_full + st, lane);
         if (v) {
           const int j0 = block_key(n);
-          const bool tail = j0 + kBlk > q.kv;  // the sequence's last block
+          const bool tail = j0 + kBlk > q.kv;  // the sequence's last block, with no keys after it in this item
           load_pages<kD>(a, q, s, f, j0, kBlk, &maps.m[2], dst, tail ? bar_tail : bar_full + st, lane);
           if (tail) {
             if (lane == 0) mbar_arrive(bar_tail);
+            tail_issued = true;
             ok = wt.wait_warp(bar_tail, 0);
             if (!ok) break;
             zero_rows<kD>(dst, kBlk, q.kv - j0, lane);
@@ -319,11 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // drain: every issued load has landed before the CTA may exit
     if (lane == 0) {
       if (cnt > 0 && !mbar_wait(bar_q, 0, kWaitLimitNs)) record_status(a.status, kStatusTimeout);
-      for (int it = issued > S ? issued - S : 0; it < issued; ++it)
-        if (!mbar_wait(bar_full + (it % S), (it / S) & 1, kWaitLimitNs)) {
-          record_status(a.status, kStatusTimeout);
-          break;
-        }
+      if (tail_issued && !mbar_wait(bar_tail, 0, kWaitLimitNs)) record_status(a.status, kStatusTimeout);
+      drain_loads(bar_full, issued, S, a.status);
     }
   } else if (warp >= kMma) {
     // ------------------------------------------------------------ MMA issue

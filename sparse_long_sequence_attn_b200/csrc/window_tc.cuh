@@ -240,6 +240,25 @@ struct Waiter {
   __device__ bool wait_warp(uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); }
 };
 
+// Waits for the loads of a ring's last items: of `issued` items, item n lies in
+// stage n % stages and completes the phase of parity n / stages there (those
+// before the last `stages` landed before their stage was filled again).  wait(stage,
+// parity) is bounded and says whether the load landed.  A CTA must not exit with
+// loads in flight, which would land in the next one's shared memory, so this is
+// called whatever became of the waits before it.
+template <typename Wait>
+__host__ __device__ __forceinline__ void drain_ring(int issued, int stages, Wait wait) {
+  for (int n = issued > stages ? issued - stages : 0; n < issued; ++n)
+    if (!wait(n % stages, (uint32_t)(n / stages) & 1u)) return;
+}
+__device__ __forceinline__ void drain_loads(uint64_t* bars, int issued, int stages, int* status) {
+  drain_ring(issued, stages, [&](int stage, uint32_t parity) {
+    const bool landed = mbar_wait(bars + stage, parity, kWaitLimitNs);
+    if (!landed) record_status(status, kStatusTimeout);
+    return landed;
+  });
+}
+
 // The largest of three, in one instruction.
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float m;
