@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kThreads)
             m[e] = mx[e];
             grow = true;
           }
-          base[e] = m[e] == -INFINITY ? 0.f : m[e];
+          base[e] = m[e] == -INFINITY ? 0.f : m[e] - kUp<kFmt>;
         }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads)
         acc.w = fmaf(sc, t.w, acc.w);
       }
       const float inv = ll == 0.f ? 0.f : 1.f / ll;  // (a sum of NaN stays one)
-      const float lse2 = ll == 0.f ? -INFINITY : mm + log2f(ll);
+      const float lse2 = ll == 0.f ? -INFINITY : mm - kUp<kFmt> + log2f(ll);
       if (direct) {
         const int i = r / a.G, h = p.f * a.G + r % a.G;
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + ((q.q0 + i) * a.H + h) * (int64_t)kD + d) =

@@ -3,8 +3,8 @@
 //
 // Mathematics: softmax(Q K^T / sqrt(D)) V over the visible keys in one pass,
 // with each row's running maximum and sum in fp32; P is rounded to the input
-// format for the second product (the tensor cores take 16-bit operands), the
-// sum is of the unrounded values.
+// format for the second product (the tensor cores take 16-bit operands; fp16 as
+// 2^7 P, see kUp), the sum is of the unrounded values.
 //
 // Layout.  The G query heads of a key/value head read the same keys, so a
 // tile's 128 rows are 128 / G tokens by G heads.  A CTA owns two row tiles (A
@@ -447,8 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         corr = ex2(m_use - m_blk);
         m_use = m_blk;
       }
-      // P = 2^(s scale - m), packed over the buffer's first 32 columns
-      const float base = m_use == -INFINITY ? 0.f : m_use;  // a row with nothing to see so far
+      // P = 2^(s scale - m + kUp), packed over the buffer's first 32 columns
+      const float base = m_use == -INFINITY ? 0.f : m_use - kUp<kFmt>;  // a row with nothing to see so far
       const uint64_t nm2 = f32x2(-base, -base);
       uint64_t ls[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                              static_cast<uint16_t*>(a.out) + ((q.q0 + i) * a.H + h) * (int64_t)kD, row_ok);
       }
       if (row_ok) {
-        const float lse2 = l_run == 0.f ? -INFINITY : m_use + log2f(l_run);
+        const float lse2 = l_run == 0.f ? -INFINITY : m_use - kUp<kFmt> + log2f(l_run);
         if (!whole)
           plan.part_lse[prow] = lse2;
         else if (a.lse)

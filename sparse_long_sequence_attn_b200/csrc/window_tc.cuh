@@ -45,6 +45,11 @@ using Plan = WindowTcPlan;
 constexpr int kTile = 128;  // rows of a tile, keys of a block
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
+// P and its row sum in the forward are times 2^kUp.  fp16: a weight of 2^-21 of the
+// row's largest is then still a normal number (beside a sink the others' weights
+// are that small), and the largest, up to 2^8 while the running maximum lags, fits.
+template <int kFmt>
+constexpr float kUp = kFmt == kFmtF16 ? 7.f : 0.f;
 
 // Rows of D 16-bit elements as swizzle panels: D = 64 or 128 is one or two
 // panels of 128-byte rows, D = 32 or 16 one panel of 64- or 32-byte rows.
