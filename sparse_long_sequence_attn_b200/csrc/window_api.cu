@@ -89,8 +89,9 @@ int check_cache(int64_t S, int64_t Hkv, int64_t D, int64_t n_pages, int64_t page
   if (S <= 0 || Hkv <= 0 || D <= 0 || n_pages <= 0 || page <= 0 || max_pages <= 0 || !dtype_ok(dtype))
     return LONGNET_ERR_INVALID_ARG;
   if (!dim_ok(D) || page < 8 || page > 256 || (page & (page - 1)) != 0) return LONGNET_ERR_UNSUPPORTED;
-  if (S > 65535 || Hkv > 65535 || S * Hkv > 65535 || n_pages * page > ((int64_t)1 << 40) ||
-      n_pages > ((int64_t)1 << 30) || max_pages * page > ((int64_t)1 << 30))
+  // each factor before its product, which could pass 64 bits
+  constexpr int64_t kMost = (int64_t)1 << 30;
+  if (S > 65535 || Hkv > 65535 || S * Hkv > 65535 || n_pages > kMost || max_pages > kMost || max_pages * page > kMost)
     return LONGNET_ERR_UNSUPPORTED;
   return LONGNET_OK;
 }
@@ -208,7 +209,7 @@ int check_paged(int64_t S, int64_t max_q, int64_t H, int64_t Hkv, int64_t D, int
   const int rc = check_cache(S, Hkv, D, 1, page, max_pages, dtype);
   if (rc) return rc;
   if (max_q <= 0 || H <= 0 || H % Hkv != 0 || window < 0 || sinks < 0) return LONGNET_ERR_INVALID_ARG;
-  if (H > 65535 || max_q * H > ((int64_t)1 << 30) || max_q > ((int64_t)1 << 30)) return LONGNET_ERR_UNSUPPORTED;
+  if (H > 65535 || max_q > ((int64_t)1 << 30) || max_q * H > ((int64_t)1 << 30)) return LONGNET_ERR_UNSUPPORTED;
   return LONGNET_OK;
 }
 

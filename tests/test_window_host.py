@@ -119,3 +119,14 @@ def test_few_token_workspace_is_bounded():
     # one sequence's scores always fit
     one = size(1, 4, 32, 8, 128, 256, 1 << 14, 0, 0)
     assert one >= 4 * 8 * 16 * (1 << 22) and size(9, 4, 32, 8, 128, 256, 1 << 14, 0, 0) < one + (1 << 26)
+
+
+@pytest.mark.parametrize("kw", [dict(max_pages=1 << 60), dict(max_pages=(1 << 60) + 4), dict(n_pages=1 << 60),
+                                dict(n_pages=1 << 62), dict(max_q=1 << 62), dict(max_q=(1 << 62) + 1)])
+def test_sizes_whose_products_pass_64_bits(kw):
+    """Counts of pages and tokens whose product with the page size or the heads is small again modulo 2^64."""
+    a, b, c = paged(**kw)
+    assert a == UNSUPPORTED and ("max_q" in kw or b == UNSUPPORTED) and ("n_pages" in kw or c == UNSUPPORTED)
+    if "max_q" not in kw:
+        assert evict(**kw) == UNSUPPORTED
+        assert evict(**{{"max_pages": "max_out", "n_pages": "n_out"}[n]: x for n, x in kw.items()}) == UNSUPPORTED
