@@ -511,13 +511,14 @@ int longnet_paged_append(const void* k_tok, const void* v_tok, void* k_pages, vo
  *     negative position (kv_len below its sequence's new tokens) sees
  *     nothing: out 0, lse -inf.  (A row with a NaN among its scores has out and
  *     lse NaN, and adds NaN to the weights of the keys it sees.)
- *   - max_q: no sequence has more new tokens (it sizes the launch, so one
+ *   - T = 0 does nothing.
+ *   - max_q >= 1: no sequence has more new tokens (it sizes the launch, so one
  *     captured launch serves every batch within it).  A sequence with more:
  *     LONGNET_ERR_DEVICE_BOUNDS, and it is skipped.
  *   - weights: NULL, or fp32 [S, Hkv, max_pages * page] to which each key's
  *     received weight is added: weights[s, f, j] += sum of P_xj over the new
  *     tokens x of sequence s and the query heads of key/value head f.
- *     Needs lse.
+ *     Needs lse (unless T = 0).
  *   - impl: LONGNET_IMPL_AUTO, LONGNET_IMPL_DECODE (bf16 and fp16, at most 16
  *     query rows, max_q H / Hkv, per key/value head and 2048 sequences), LONGNET_IMPL_TCGEN05
  *     (bf16 and fp16, H / Hkv <= 128) or LONGNET_IMPL_SIMT (fp32 arithmetic,

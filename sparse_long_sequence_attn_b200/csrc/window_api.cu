@@ -262,7 +262,7 @@ extern "C" int longnet_paged_attn_fwd(const void* q, const void* k_pages, const 
   if (rc) return rc;
   rc = check_cache(S, Hkv, D, n_pages, page, max_pages, dtype);
   if (rc) return rc;
-  if (!k_pages || !v_pages || !cu_q || !kv_len || !table || (T > 0 && (!q || !out)) || (weights && !lse))
+  if (!k_pages || !v_pages || !cu_q || !kv_len || !table || (T > 0 && (!q || !out || (weights && !lse))))
     return LONGNET_ERR_INVALID_ARG;
   if (T > ((int64_t)1 << 30)) return LONGNET_ERR_UNSUPPORTED;
   const int64_t need =

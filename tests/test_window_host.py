@@ -130,3 +130,10 @@ def test_sizes_whose_products_pass_64_bits(kw):
     if "max_q" not in kw:
         assert evict(**kw) == UNSUPPORTED
         assert evict(**{{"max_pages": "max_out", "n_pages": "n_out"}[n]: x for n, x in kw.items()}) == UNSUPPORTED
+
+
+def test_no_token_needs_no_rows():
+    """T = 0: an empty tensor has no address, and none is needed, with weights or without."""
+    ok = bd.LONGNET_OK if torch.cuda.is_available() else bd.LONGNET_ERR_NO_DEVICE
+    for weights in (0, 0x1000):
+        assert paged(T=0, q=0, lse=0, weights=weights)[:2] == (ok, ok)
