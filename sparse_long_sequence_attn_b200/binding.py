@@ -603,6 +603,13 @@ def _window_bwd(q, k, v, out, lse, dout, dq, dk, dv, window, sinks, workspace, i
           workspace.numel() * workspace.element_size())
 
 
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    """t contiguous and 16-byte aligned, as the library takes it: itself, or a
+    copy (differentiable) where it is strided or a view that starts in between."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def window_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, sinks: int = 0,
                 impl: int = LONGNET_IMPL_AUTO, want_lse: bool = True, stream=None):
     """Allocate out (and lse) with torch and run longnet_window_attn_fwd.
@@ -625,7 +632,7 @@ def window_attn_bwd(q, k, v, out, lse, dout, window: int, sinks: int = 0, impl: 
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         ws = q.new_empty(longnet_window_bwd_workspace_bytes(B, N, H, k.shape[2], D, window, sinks, q.dtype),
                          dtype=torch.uint8)
-        _window_bwd(q, k, v, out, lse, dout.contiguous(), dq, dk, dv, window, sinks, ws, impl, stream)
+        _window_bwd(q, k, v, out, lse, _dense(dout), dq, dk, dv, window, sinks, ws, impl, stream)
     return dq, dk, dv
 
 
@@ -655,7 +662,7 @@ def window_attention(q, k, v, window: int, sinks: int = 0):
     eagerly from the same leaves first (warm up on a side stream, then drop it),
     since torch adds a leaf's gradient on the stream of the leaf's live graph,
     which a capture does not allow."""
-    return WindowAttnFunction.apply(q.contiguous(), k.contiguous(), v.contiguous(), int(window), int(sinks))
+    return WindowAttnFunction.apply(_dense(q), _dense(k), _dense(v), int(window), int(sinks))
 
 
 def _cache_sizes(k_pages: torch.Tensor, table: torch.Tensor):
