@@ -478,7 +478,11 @@ int longnet_window_attn_bwd(const void* q, const void* k, const void* v,
  *     table[s][j / page], slot j mod page.  Entries past a sequence's keys
  *     are not read and may hold anything; those of its keys must all be
  *     pages, also where the mask hides the keys, which may be read (and weigh
- *     0, so they must be finite).
+ *     0, so they must be finite).  But with a window, no key j is read with
+ *       128 ceil(sinks / 128) <= j < 128 floor((x0 - window + 1) / 128),
+ *     x0 = kv_len[s] less the sequence's new tokens, and no entry of a page
+ *     that holds only such keys: a cache that only grows may give these pages
+ *     back.
  *   - kv_len [S]: keys of each sequence, the new tokens' among them;
  *     0 <= kv_len <= max_pages * page.
  *   - cu_q [S + 1]: the new tokens of sequence s are the token rows

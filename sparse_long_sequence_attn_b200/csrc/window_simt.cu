@@ -387,10 +387,6 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const AttnArgs a, flo
   const Seq q = seq_of(a, s);
   const int j0 = blockIdx.x * kT;
   if (j0 >= q.kv || q.nq == 0) return;
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  load_rows<T, D>(sK, static_cast<const T*>(a.k),
-                  [&](int r) -> int64_t { return j0 + r < q.kv ? kv_row(a, q, s, f, j0 + r) : -1; });
-  float acc[4] = {};
   // rows from the first query at or after the tile on
   int i0 = j0 - q.first;
   if (i0 < 0) i0 = 0;
@@ -400,6 +396,11 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const AttnArgs a, flo
     const int64_t last = (int64_t)j0 + kT - 1 + a.window - q.first;
     if (last < i1) i1 = last < 0 ? 0 : (int)last;
   }
+  if (i0 >= i1) return;  // keys that no query sees are not read
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  load_rows<T, D>(sK, static_cast<const T*>(a.k),
+                  [&](int r) -> int64_t { return j0 + r < q.kv ? kv_row(a, q, s, f, j0 + r) : -1; });
+  float acc[4] = {};
   for (int r0 = i0 * a.G; r0 < i1 * a.G; r0 += kT) {
     Rows R{q, s, f, a.G, r0, i1 * a.G - r0 < kT ? i1 * a.G - r0 : kT};
     __syncthreads();
