@@ -498,7 +498,8 @@ int longnet_window_attn_bwd(const void* q, const void* k, const void* v,
  *
  * longnet_paged_append — writes the new tokens' keys and values, k_tok and
  * v_tok [T, Hkv, D], to their slots.  weights (may be NULL): fp32
- * [S, Hkv, max_pages * page], set to 0 there.  T = 0 does nothing.
+ * [S, Hkv, max_pages * page], set to 0 there.  A token at a negative position
+ * has no slot: it is skipped, and recorded as out of range.  T = 0 does nothing.
  */
 int longnet_paged_append(const void* k_tok, const void* v_tok, void* k_pages, void* v_pages, float* weights,
                          const int32_t* cu_q, const int32_t* kv_len, const int32_t* table,

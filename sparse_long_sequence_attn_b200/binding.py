@@ -565,14 +565,19 @@ def _window_fwd(q, k, v, out, lse, window, sinks, impl, stream) -> None:
 
 
 @functools.lru_cache(maxsize=1024)
+def _bytes(name: str, *sizes: int) -> int:
+    # kept by value: every size is an int, not a tensor whose value may change
+    n = getattr(load_library(), name)(*sizes)
+    if n < 0:
+        raise LongNetError(n, name)
+    return int(n)
+
+
 def longnet_window_bwd_workspace_bytes(B: int, N: int, H: int, Hkv: int, D: int, window: int, sinks: int,
                                        dtype: torch.dtype) -> int:
     """Device workspace bytes longnet_window_attn_bwd needs."""
-    n = load_library().longnet_window_bwd_workspace_bytes(B, N, H, Hkv, D, int(window), int(sinks),
-                                                          _DTYPE_CODES[dtype])
-    if n < 0:
-        raise LongNetError(n, "longnet_window_bwd_workspace_bytes")
-    return int(n)
+    return _bytes("longnet_window_bwd_workspace_bytes", int(B), int(N), int(H), int(Hkv), int(D), int(window),
+                  int(sinks), _DTYPE_CODES[dtype])
 
 
 def longnet_window_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
@@ -695,15 +700,11 @@ def paged_append(k_tok: torch.Tensor, v_tok: torch.Tensor, k_pages: torch.Tensor
           table.data_ptr(), T, S, Hkv, D, n_pages, page, max_pages, _dtype_code(k_tok))
 
 
-@functools.lru_cache(maxsize=1024)
 def longnet_paged_workspace_bytes(S: int, max_q: int, H: int, Hkv: int, D: int, page: int, max_pages: int,
                                   window: int, sinks: int, dtype: torch.dtype, weights: bool = False) -> int:
     """Device workspace bytes longnet_paged_attn_fwd needs."""
-    n = load_library().longnet_paged_workspace_bytes(S, int(max_q), H, Hkv, D, page, max_pages, int(window),
-                                                     int(sinks), _DTYPE_CODES[dtype], int(bool(weights)))
-    if n < 0:
-        raise LongNetError(n, "longnet_paged_workspace_bytes")
-    return int(n)
+    return _bytes("longnet_paged_workspace_bytes", int(S), int(max_q), int(H), int(Hkv), int(D), int(page),
+                  int(max_pages), int(window), int(sinks), _DTYPE_CODES[dtype], int(bool(weights)))
 
 
 def paged_workspace(q: torch.Tensor, k_pages: torch.Tensor, table: torch.Tensor, max_q: int, window: int = 0,

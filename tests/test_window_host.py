@@ -137,3 +137,20 @@ def test_no_token_needs_no_rows():
     ok = bd.LONGNET_OK if torch.cuda.is_available() else bd.LONGNET_ERR_NO_DEVICE
     for weights in (0, 0x1000):
         assert paged(T=0, q=0, lse=0, weights=weights)[:2] == (ok, ok)
+
+
+def test_workspace_sizes_go_by_value():
+    """A size given as a tensor, or a number whose value a program changes in place, is read anew."""
+    n = torch.tensor(1)
+    small = bd.longnet_paged_workspace_bytes(4, n, 8, 2, 64, 16, 64, 0, 0, torch.bfloat16)
+    n.fill_(700)
+    large = bd.longnet_paged_workspace_bytes(4, n, 8, 2, 64, 16, 64, 0, 0, torch.bfloat16)
+    assert small == bd.longnet_paged_workspace_bytes(4, 1, 8, 2, 64, 16, 64, 0, 0, torch.bfloat16)
+    assert large == bd.longnet_paged_workspace_bytes(4, 700, 8, 2, 64, 16, 64, 0, 0, torch.bfloat16) != small
+    w = torch.tensor(10)
+    sizes = []
+    for x in (10, 4000):
+        w.fill_(x)
+        sizes.append(bd.longnet_window_bwd_workspace_bytes(1, 8000, 4, 2, 64, w, 70, torch.bfloat16))
+        assert sizes[-1] == bd.longnet_window_bwd_workspace_bytes(1, 8000, 4, 2, 64, x, 70, torch.bfloat16)
+    assert sizes[0] != sizes[1]
