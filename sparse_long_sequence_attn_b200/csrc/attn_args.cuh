@@ -129,9 +129,10 @@ struct WindowBwdArgs {
   void* dk;
   void* dv;
   float* delta;
-  float* peaks;  // [2] largest |dout_x|^2 and |v_j|^2
+  float* peaks;  // [kPeakBlocks][2]
   float* partial;
 };
+constexpr int kPeakBlocks = 148 * 6;  // of launch_window_peaks, at most
 // How dk and dv are cut into work items, one CTA each: a tile of keys by a
 // range of the queries that see it.  A tile's near queries (those its window
 // reaches) are cut into `near` ranges where the tiles alone would leave SMs
@@ -182,8 +183,9 @@ KeyPlan simt_key_plan(int64_t S, int64_t N, int64_t H, int64_t Hkv, int64_t wind
 int launch_window_bwd_simt(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream);
 // delta = <dout, out> of every row, and the last step both families share.
 int launch_window_delta(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream);
-// fp16: g.peaks, and with them, when asked for, delta.
-int launch_window_peaks(const AttnArgs& a, const WindowBwdArgs& g, bool with_delta, cudaStream_t stream);
+// fp16: the largest |dout_x|^2 and |v_j|^2 of each of its *blocks blocks' rows, to
+// g.peaks, and with them, when asked for, delta.
+int launch_window_peaks(const AttnArgs& a, const WindowBwdArgs& g, bool with_delta, int* blocks, cudaStream_t stream);
 int launch_key_reduce(const AttnArgs& a, const WindowBwdArgs& g, const KeyPlan& k, cudaStream_t stream);
 
 int launch_paged_append(const AttnArgs& a, const void* k_tok, const void* v_tok, float* weights, cudaStream_t stream);

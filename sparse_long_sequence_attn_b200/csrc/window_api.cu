@@ -74,7 +74,7 @@ int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
 // The workspace of the backward: delta, fp16's peaks, then the partials of the
 // family that needs most, so that it does not depend on the family.
-int64_t peak_bytes(int dtype) { return dtype == LONGNET_DTYPE_F16 ? 256 : 0; }
+int64_t peak_bytes(int dtype) { return dtype == LONGNET_DTYPE_F16 ? round256(8 * kPeakBlocks) : 0; }
 int64_t bwd_workspace(int64_t B, int64_t N, int64_t H, int64_t Hkv, int64_t D, int64_t window, int64_t sinks,
                       int dtype) {
   window = window < N ? window : N;

@@ -119,6 +119,7 @@ constexpr int kExactKeys = 512;
 struct BPlan {
   int tokens;    // of a tile (query-centric) or of a block (key-centric)
   int exact;     // query-centric: delta by a pass of its own (else it is there)
+  int peaks;     // fp16: blocks that left their rows' largest norms in g.peaks
   KeyPlan key;
 };
 
@@ -312,6 +313,16 @@ __device__ __forceinline__ void bwd_body(const AttnArgs& a, const WindowBwdArgs&
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  // fp16: the largest norms, by warps; all of it between the set-up's steps, whose
+  // waits it shares (numbers from 0 up compare as their bits do)
+  uint32_t* s_top = reinterpret_cast<uint32_t*>(smem + LL::kBars + 256);  // [2][warps]
+  uint32_t top[2] = {0, 0};
+  if constexpr (kFmt == kFmtF16)
+    for (int i = threadIdx.x; i < plan.peaks; i += kThreads) {
+      const uint2 x = reinterpret_cast<const uint2*>(g.peaks)[i];
+      top[0] = max(top[0], x.x);
+      top[1] = max(top[1], x.y);
+    }
   if (threadIdx.x == 0) {
     mbar_init(bar_tile, 1);
     for (int i = 0; i < S; ++i) {
@@ -328,23 +339,14 @@ __device__ __forceinline__ void bwd_body(const AttnArgs& a, const WindowBwdArgs&
     *abort_flag = 0;
     fence_barrier_init();
   }
-  // fp16: the call's unit 2^e, and the constant of delta's parts, 2^-e as far as
-  // fp16 holds it
-  float unit = 1.f, part_unit = 1.f;
-  if constexpr (kFmt == kFmtF16) {
-    unit = grad_unit(g.peaks[0], g.peaks[1]);
-    part_unit = fminf(fmaxf(1.f / unit, 5.9604645e-8f), 32768.f);  // 2^-24, 2^15
-  }
   if (LL::kFold) {
-    // the tiles' extra columns, three constants and zeros, and the blocks'
-    // second chunk of theirs, zeros
-    for (int e = threadIdx.x; e < 2 * kTile * 2; e += kThreads) {
-      const int w = e / (2 * kTile);  // K's, V's
-      const float c = w ? part_unit : kFmt == kFmtF16 ? kLseUnit : 1.f;
-      const uint32_t one = pack2<kFmt>(c, c);
-      *reinterpret_cast<uint4*>(smem + LL::kFold0 + w * kTile * 32 + fold_at((e >> 1) % kTile, e & 1)) =
+    // K's tiles' extra columns, three constants and zeros (V's: the loading warp),
+    // and the blocks' second chunk of theirs, zeros
+    const float c = kFmt == kFmtF16 ? kLseUnit : 1.f;
+    const uint32_t one = pack2<kFmt>(c, c);
+    for (int e = threadIdx.x; e < kTile * 2; e += kThreads)
+      *reinterpret_cast<uint4*>(smem + LL::kFold0 + fold_at(e >> 1, e & 1)) =
           (e & 1) ? make_uint4(0, 0, 0, 0) : make_uint4(one, one & 0xffffu, 0, 0);
-    }
     for (int e = threadIdx.x; e < S * 2 * kBlk; e += kThreads)
       *reinterpret_cast<uint4*>(sStage + (e / (2 * kBlk)) * LL::kStageBytes + 2 * LL::kBlkBytes +
                                 (e / kBlk % 2) * kBlk * 32 + fold_at(e % kBlk, 1)) = make_uint4(0, 0, 0, 0);
@@ -368,11 +370,25 @@ __device__ __forceinline__ void bwd_body(const AttnArgs& a, const WindowBwdArgs&
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if constexpr (kFmt == kFmtF16) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const uint32_t m = __reduce_max_sync(0xffffffffu, top[w]);
+      if (lane == 0) s_top[w * (kThreads / 32) + warp] = m;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   Waiter wt{abort_flag, a.status, kWaitLimitNs};
+  float unit = 1.f;  // fp16: the call's 2^e
+  if constexpr (kFmt == kFmtF16) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+      top[w] = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? s_top[w * (kThreads / 32) + lane] : 0u);
+    unit = grad_unit(__uint_as_float(top[0]), __uint_as_float(top[1]));
+  }
   const int passes = !kKeys && plan.exact ? 2 : 1;  // over the blocks; the first of two sums delta
   auto tile_ptr = [&](int st, int which) { return smem + (st * 2 + which) * LL::kTileBytes; };
 
@@ -389,6 +405,15 @@ __device__ __forceinline__ void bwd_body(const AttnArgs& a, const WindowBwdArgs&
           for (int pn = 0; pn < kPanels; ++pn)
             tma_load_4d(tile_ptr(st, w) + pn * kTilePanel, &maps.t[w], bar_tile, LL::kPanelElems * pn,
                         kKeys ? f : f * G, first + st * (kKeys ? kTile : tok), s);
+    }
+    // the constant of delta's parts: 2^-e as far as fp16 holds it, 2^-24 to 2^15
+    const float part_unit = kFmt == kFmtF16 ? fminf(fmaxf(1.f / unit, 5.9604645e-8f), 32768.f) : 1.f;
+    if (LL::kFold) {  // V's tiles' extra columns, there before the first block is (it arrives after the fence)
+      const uint32_t one = pack2<kFmt>(part_unit, part_unit);
+      for (int e = lane; e < kTile * 2; e += 32)
+        *reinterpret_cast<uint4*>(smem + LL::kFold0 + kTile * 32 + fold_at(e >> 1, e & 1)) =
+            (e & 1) ? make_uint4(0, 0, 0, 0) : make_uint4(one, one & 0xffffu, 0, 0);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     // key-centric: -lse (log2 domain) and -delta of a block's rows, fetched a
     // block ahead (their latency would otherwise stand between the loads)
@@ -812,7 +837,7 @@ int launch_typed(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream)
   BPlan pk, pq;
   pk.tokens = kBlk / a.G;
   pq.tokens = kTile / a.G;
-  pk.exact = 0;
+  pk.exact = pk.peaks = pq.peaks = 0;
   pq.exact = (int64_t)a.window + a.sinks <= kExactKeys || a.nq_max <= kExactKeys;
   using LK = B<kD, true>;
   using LQ = B<kD, false>;
@@ -829,16 +854,18 @@ int launch_typed(const AttnArgs& a, const WindowBwdArgs& g, cudaStream_t stream)
   const int64_t pairs = ((int64_t)a.nq_max + 2 * pq.tokens - 1) / (2 * pq.tokens);
   if (!pq.exact) {
     if ((pairs + pk.key.items()) * a.S * a.Hkv > INT32_MAX) return LONGNET_ERR_UNSUPPORTED;
-    int rc = kF16 ? launch_window_peaks(a, g, true, stream) : launch_window_delta(a, g, stream);
+    int rc = kF16 ? launch_window_peaks(a, g, true, &pk.peaks, stream) : launch_window_delta(a, g, stream);
     if (rc) return rc;
+    pq.peaks = pk.peaks;
     constexpr int smem = LK::kSmem > LQ::kSmem ? LK::kSmem : LQ::kSmem;
     if (!opt_in_smem<both_kernel<kFmt, kD>>(smem)) return LONGNET_ERR_CUDA;
     rc = launch_after(both_kernel<kFmt, kD>, dim3((unsigned)((pairs + pk.key.items()) * a.S * a.Hkv)), kThreads,
                       smem, stream, a, g, mq, mk, pq, pk, (int)pairs);
     return rc ? rc : launch_key_reduce(a, g, pk.key, stream);
   }
-  int rc = kF16 ? launch_window_peaks(a, g, false, stream) : LONGNET_OK;
+  int rc = kF16 ? launch_window_peaks(a, g, false, &pk.peaks, stream) : LONGNET_OK;
   if (rc) return rc;
+  pq.peaks = pk.peaks;
   // dq first: it leaves delta for dk and dv
   rc = launch_after(bwd_kernel<kFmt, kD, false>, dim3((unsigned)pairs, (unsigned)(a.S * a.Hkv)), kThreads, LQ::kSmem,
                         stream, a, g, mq, pq);

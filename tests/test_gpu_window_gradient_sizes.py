@@ -101,3 +101,20 @@ def test_zero_and_infinite_cotangents(shape):
     dq = gradients(q, k, v, dout, window, sinks)[0]
     rest = [i for i in range(N) if i != at]
     close("dq", dq[:, rest], ref[2][:, rest], F16)
+
+
+@pytest.mark.parametrize("shape", SHAPES[:2], ids=str)
+def test_a_captured_step_takes_cotangents_of_other_sizes(shape):
+    q, k, v, dout = inputs(shape, F16, 1.0)
+    graph = torch.cuda.CUDAGraph()
+    gradients(q, k, v, dout, *shape[5:])
+    out, lse = bd.window_attn(q, k, v, *shape[5:])
+    with torch.cuda.graph(graph):
+        captured = bd.window_attn_bwd(q, k, v, out, lse, dout, *shape[5:])
+    for size in (1.0, 1e-4, 100.0, 1e-4):
+        dout.copy_(inputs(shape, F16, size, seed=8)[3])
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(captured, bd.window_attn_bwd(q, k, v, out, lse, dout, *shape[5:])):
+            assert torch.equal(a, b)
+    assert bd.longnet_last_device_status() == 0
