@@ -65,7 +65,9 @@
 // at D = 128).  Turns of the two tiles at the arithmetic, which kept their
 // exponentials apart, were slower (240 -> 307 us).  Measured, both kernels: 8192
 // tokens, 12/4 heads of 64, window 1024: 148 us and 7 for delta; 16384 tokens, 8 heads of 128, window
-// 4096: 760 us (1109 TFLOP/s of the seven products), in one launch.
+// 4096, fp16: 775 us (1088 TFLOP/s of the seven products), in one launch.  608 threads
+// leave each 96 registers; at D = 128 the one launch spills 72 bytes of stores and 152
+// of loads a thread in bf16, 24 and 36 in fp16.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -796,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // (256 keys by three heads' rows, say) up to D = 64 and query-centric (256 rows
 // against 128 keys) at D = 128; the others fill up their last wave.  nq: query-centric
 // ones of a (batch, head).  One launch after the other: 240 us for the step of 8192
-// tokens, 12/4 heads of 64, against 237; 1093 against 1009 for 16384 tokens, 8 heads of
+// tokens, 12/4 heads of 64, against 237; 1093 against 1015 for 16384 tokens, 8 heads of
 // 128; 78 against 60 for 1024 tokens, 8 heads of 64, window 600.
 template <int kFmt, int kD>
 __global__ void __launch_bounds__(kThreads, 1)

@@ -33,7 +33,7 @@
 // 128 and the exponentials' unit 38 %.  Measured: 8192 tokens, 12/4 heads of 64,
 // window 1024: 68 us (357 TFLOP/s of visible products); 16384 tokens, 8 heads of
 // 128, window 4096: 242 us (995); two chunks of up to 4096 tokens over up to 16384
-// keys, 16/4 heads of 128: 704 us (1100).
+// keys, 16/4 heads of 128: 709 us (1092).
 // Slots past a sequence's keys may hold anything: their scores are masked
 // before use and their value rows are overwritten with zeros in shared memory.
 // Every wait is bounded; on a timeout the kernel records the status word,
