@@ -449,6 +449,8 @@ int longnet_window_attn_fwd(const void* q, const void* k, const void* v, void* o
  *   dq = dS K / sqrt(D), dk = dS^T Q / sqrt(D), dv = P^T dout,
  * dk and dv summed over the query heads that share a key/value head.
  *   - out, lse: the forward's results; dout: [B, N, H, D] of dtype.
+ *     delta is made from out as it was rounded; by LONGNET_IMPL_TCGEN05, where
+ *     window + sinks or N is at most 512, from P and v instead.
  *   - dq [B, N, H, D], dk and dv [B, N, Hkv, D]: of dtype, written in full,
  *     summed in fp32 and rounded once.  They must not alias the inputs.
  *   - workspace: device memory of the caller, 256-byte aligned, at least

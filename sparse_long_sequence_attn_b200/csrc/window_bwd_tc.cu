@@ -13,7 +13,8 @@
 //     to kExactKeys visible keys, delta is summed as P dout V^T in fp32 instead,
 //     by a first pass over the same blocks (relative error of dq and dk at a
 //     window of 64: 2.6e-3 -> 2.4e-3, where the plain 32-bit form rounded once has
-//     1.7e-3);
+//     1.7e-3).  Beyond, the rounding is left where it shows most: with values whose
+//     mean is five times their spread, 900 keys, bf16: 1.4e-2 in dq, 1.0e-2 in dk;
 //   - in fp16, P is rounded as 2^8 P, since a weight of one in thousands of keys
 //     is below that format's normal range; dV is scaled back at the end.  And dS
 //     is rounded as 2^e dS, where gradients may be of any size: e is such that
